@@ -21,18 +21,24 @@ namespace sar {
 // 8.2 -> 6.1 us per call eager and 6.4 -> 6.0 us in a CUDA graph, 8 x 64 MiB
 // fp16 155.8 -> 153.2 us eager.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args&&... args) {
+cudaError_t launch_kernel_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                               Args&&... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args&&... args) {
+    return launch_kernel_smem(kernel, grid, block, 0, s, std::forward<Args>(args)...);
 }
 
 // What an rsag launch writes: the fused allreduce writes the reduced chunk to
@@ -116,5 +122,73 @@ cudaError_t launch_convert(const void* src, sar_dtype src_dt, void* dst, sar_dty
                            size_t count, bool vec, cudaStream_t stream);
 
 size_t esize_of(sar_dtype dt);
+
+// Layer norm (layer_norm.cu).  Leading dimensions in elements; weight, bias,
+// mean, rstd of the forward call and dweight, dbias of the backward call may
+// be null.
+struct NormArgs {
+    const void* x;
+    size_t ldx;
+    const void* weight;
+    const void* bias;
+    void* y;
+    size_t ldy;
+    float* mean;
+    float* rstd;
+    size_t rows, cols;
+    float eps;
+};
+cudaError_t launch_layer_norm(sar_dtype dt, sar_dtype wdt, const NormArgs& a, cudaStream_t stream);
+
+struct NormGradArgs {
+    const void* dy;
+    size_t lddy;
+    const void* x;
+    size_t ldx;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    void* dx;
+    size_t lddx;
+    void* dweight;
+    void* dbias;
+    size_t rows, cols;
+    float* partial;      // layer_norm_partials(rows, cols) rows of 2 * cols sums
+};
+size_t layer_norm_partials(size_t rows, size_t cols);
+cudaError_t launch_layer_norm_backward(sar_dtype dt, sar_dtype wdt, const NormGradArgs& a, cudaStream_t stream);
+
+// Tokens to experts and back (experts.cu).
+struct SortArgs {
+    const void* ids;
+    uint32_t slots;
+    int experts, align;
+    uint32_t capacity;
+    int32_t* counts;
+    int32_t* offsets;
+    int32_t* position;
+    int32_t* source;
+};
+cudaError_t launch_expert_sort(int id_bytes, const SortArgs& a, cudaStream_t stream);
+
+struct ExpertArgs {
+    const void* tok;         // tokens x cols: x of the dispatch, dout of the backward call
+    size_t ldt;
+    const void* rows_in;     // capacity x cols: the rows that the combine calls read
+    size_t ldi;
+    void* out;               // rows (dispatch), out (combine), drows (backward)
+    size_t ldo;
+    const int32_t* position;
+    const int32_t* counts;   // null: no padding to clear
+    const int32_t* offsets;
+    const void* weights;     // null: every weight is 1
+    void* dweights;          // null: not wanted
+    int experts, topk;
+    uint32_t capacity;
+    size_t tokens, cols;
+};
+cudaError_t launch_expert_dispatch(size_t esize, const ExpertArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_combine(sar_dtype dt, sar_dtype wdt, const ExpertArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_combine_backward(sar_dtype dt, sar_dtype wdt, const ExpertArgs& a, cudaStream_t stream);
 
 }  // namespace sar

@@ -438,6 +438,169 @@ SAR_API sar_status sar_fp8_convert(const void* src, sar_dtype src_dtype, void* d
                            size_t count, sar_stream_t stream);
 
 /*
+ * Operators around the allreduce: layer norm, whose weight gradient is what a
+ * data-parallel step sums over the ranks, and the movement of tokens to
+ * experts and back, whose way back is a weighted sum of rows.
+ *
+ * Conventions, beside those at the top of this file:
+ *  - Every pointer is a DEVICE pointer and belongs to one rank; a simulated
+ *    rank's step is a call of its own.  Nothing is allocated, nothing is
+ *    synchronised and no state is kept, so calls may overlap on the GPU (with
+ *    buffers and workspaces of their own) and may be captured.
+ *  - A matrix is `rows` rows of `cols` elements, dense within a row; its
+ *    leading dimension ld* (elements from one row to the next) is at least
+ *    `cols`.  Element offsets are 64-bit.  Rows that all start on 16-byte
+ *    boundaries (base address and ld * element size) move as 16-byte vectors;
+ *    other layouts run slower kernels with the same results to rounding.
+ *  - Elements are widened exactly to binary32; sums, statistics and products
+ *    are held in binary32; every output element is rounded once.  Sums run in
+ *    an order that depends on the sizes and the alignment only: no atomics, so
+ *    a call repeated on the same data gives the same bits.
+ *  - dtype is SAR_BF16, SAR_FP16 or SAR_FP32 (sar_expert_dispatch, which
+ *    copies, takes every type); the type of the parameters or weights is
+ *    SAR_FP32 or `dtype`.  Others return SAR_ERR_UNSUPPORTED_DTYPE.
+ *  - NULL where a pointer is not marked optional, a leading dimension below
+ *    cols, or sizes whose product does not fit return SAR_ERR_INVALID_ARG;
+ *    a pointer off its element's alignment SAR_ERR_MISALIGNED.  All before any
+ *    launch.  Pointers to matrices without elements are not looked at.
+ *  - Outputs must not overlap other buffers unless a call says so.
+ */
+
+/*
+ * sar_layer_norm -- for every row:
+ *   mean = (sum_c x[c]) / cols
+ *   rstd = 1 / sqrt((sum_c (x[c] - mean)^2) / cols + eps)
+ *   y[c] = R((x[c] - mean) * rstd * weight[c] + bias[c])
+ * with the variance from the deviations (not from the squares' sum).
+ *
+ * weight, bias : optional (NULL: 1 and 0), `cols` elements of type wdtype.
+ * mean, rstd   : optional outputs, `rows` binary32 values, for
+ *                sar_layer_norm_backward.
+ * eps          : not negative and finite, else SAR_ERR_INVALID_ARG.
+ * y may be x (same ld).  rows == 0 or cols == 0 launches nothing.
+ * A row with an infinity or NaN gives NaN throughout, as the formula does.
+ */
+SAR_API sar_status sar_layer_norm(const void* x, size_t ldx, const void* weight, const void* bias, void* y,
+                                  size_t ldy, float* mean, float* rstd, size_t rows, size_t cols, float eps,
+                                  sar_dtype dtype, sar_dtype wdtype, sar_stream_t stream);
+
+/*
+ * sar_layer_norm_backward_workspace_bytes -- bytes of the workspace that
+ * sar_layer_norm_backward needs for the parameters' gradients (0 when the
+ * sizes do not fit; never 0 otherwise).
+ */
+SAR_API size_t sar_layer_norm_backward_workspace_bytes(size_t rows, size_t cols);
+
+/*
+ * sar_layer_norm_backward -- with h[c] = (x[c] - mean) * rstd and
+ * g[c] = dy[c] * weight[c], for every row:
+ *   dx[c] = R(rstd * (g[c] - (sum g) / cols - h[c] * (sum g*h) / cols))
+ * and over the rows:
+ *   dweight[c] = R(sum_rows dy[c] * h[c]),   dbias[c] = R(sum_rows dy[c]).
+ *
+ * weight          : optional (NULL: 1).
+ * mean, rstd      : what sar_layer_norm wrote for x.
+ * dweight, dbias  : optional outputs of type wdtype; with rows == 0 they are
+ *                   set to zero (an empty sum).
+ * workspace       : needed when dweight or dbias is given: 16-byte aligned, of
+ *                   sar_layer_norm_backward_workspace_bytes(rows, cols) bytes;
+ *                   its contents do not matter before and after.  A smaller
+ *                   workspace_bytes returns SAR_ERR_INVALID_ARG.
+ * dx may be dy or x (same ld).
+ */
+SAR_API sar_status sar_layer_norm_backward(const void* dy, size_t lddy, const void* x, size_t ldx,
+                                           const void* weight, const float* mean, const float* rstd, void* dx,
+                                           size_t lddx, void* dweight, void* dbias, size_t rows, size_t cols,
+                                           sar_dtype dtype, sar_dtype wdtype, void* workspace,
+                                           size_t workspace_bytes, sar_stream_t stream);
+
+/* Largest number of experts of the sar_expert_* calls. */
+#define SAR_MAX_EXPERTS 1024
+
+/*
+ * sar_expert_rows -- rows that hold every expert's segment whatever the
+ * routing: tokens * topk, plus align - 1 for every expert that can get a
+ * slot.  0 for invalid arguments (or when there is nothing to hold).
+ */
+SAR_API size_t sar_expert_rows(size_t tokens, int topk, int experts, int align);
+
+/*
+ * sar_expert_sort -- sorts the tokens' choices by expert.  Slot s = t * topk + j
+ * is choice j of token t; ids[s] in 0 .. experts - 1 is its expert, any other
+ * value (-1, say: a choice over an expert's capacity, or a token that only
+ * fills the batch) drops the slot.
+ *
+ * The kept slots take places 0, 1, ... sorted by expert, in the order of their
+ * slots within an expert (a stable sort).  Every expert's segment starts at a
+ * multiple of `align` rows, for matrix products that work on whole tiles:
+ *   counts[e]      kept slots of expert e                     (experts values)
+ *   offsets[e]     first place of e's segment; offsets[e + 1] = offsets[e] +
+ *                  counts[e] rounded up to align           (experts + 1 values)
+ *   position[s]    the place of slot s, or -1 if it is dropped  (tokens * topk)
+ *   source[p]      the slot at place p, or -1 where there is none (padding, and
+ *                  places past offsets[experts])     (capacity values; optional)
+ * Places from `capacity` on do not exist: a slot that would get one is dropped
+ * (position -1); counts and offsets still count it.  With capacity =
+ * sar_expert_rows(...) this cannot happen.
+ *
+ * id_bytes : 4 or 8, the size of the signed integers in ids.
+ * topk >= 1, 1 <= experts <= SAR_MAX_EXPERTS, align >= 1, and tokens * topk,
+ * capacity and sar_expert_rows at most 2^31 - 1, else SAR_ERR_INVALID_ARG.
+ * With tokens == 0 the outputs are those of an empty batch.
+ */
+SAR_API sar_status sar_expert_sort(const void* ids, int id_bytes, size_t tokens, int topk, int experts, int align,
+                                   size_t capacity, int32_t* counts, int32_t* offsets, int32_t* position,
+                                   int32_t* source, sar_stream_t stream);
+
+/*
+ * sar_expert_dispatch -- copies each token's row to the places of its slots:
+ *   rows[position[t * topk + j]] = x[t]
+ * bit for bit, for every slot with a position in 0 .. capacity - 1 (others are
+ * dropped).  With counts and offsets (both or neither), the rows that pad the
+ * experts' segments, offsets[e] + counts[e] .. offsets[e + 1] - 1, become zero;
+ * without, they are left as they are, as rows past the last segment always are.
+ *
+ * x : tokens x cols, rows : capacity x cols, position : tokens * topk values.
+ * The gradient with respect to x is sar_expert_combine without weights.
+ */
+SAR_API sar_status sar_expert_dispatch(const void* x, size_t ldx, const int32_t* position, const int32_t* counts,
+                                       const int32_t* offsets, int experts, void* rows, size_t ldr,
+                                       size_t capacity, size_t tokens, int topk, size_t cols, sar_dtype dtype,
+                                       sar_stream_t stream);
+
+/*
+ * sar_expert_combine -- the way back: for every token,
+ *   out[t] = R(sum_j weights[t * topk + j] * rows[position[t * topk + j]])
+ * over the kept slots j in ascending order, each step one binary32 fused
+ * multiply-add; weights NULL: the plain sum, seeded with the first kept row
+ * (so one choice is the identity).  A token without a kept slot gets zeros.
+ * Weights and rows of dropped slots are not read.
+ *
+ * weights : optional, tokens * topk values of type wdtype.
+ */
+SAR_API sar_status sar_expert_combine(const void* rows, size_t ldr, size_t capacity, const int32_t* position,
+                                      const void* weights, void* out, size_t ldo, size_t tokens, int topk,
+                                      size_t cols, sar_dtype dtype, sar_dtype wdtype, sar_stream_t stream);
+
+/*
+ * sar_expert_combine_backward -- the gradients of sar_expert_combine with
+ * respect to its rows and weights:
+ *   drows[position[s]] = R(weights[s] * dout[t])        (s = t * topk + j)
+ *   dweights[s]        = R(sum_c dout[t][c] * rows[position[s]][c]),
+ * 0 for dropped slots.  counts and offsets as in sar_expert_dispatch (padding
+ * rows of drows become zero).
+ *
+ * dweights is optional; without it rows is not read and may be NULL.
+ * drows may be rows (same ld).
+ */
+SAR_API sar_status sar_expert_combine_backward(const void* dout, size_t ldo, const void* rows, size_t ldr,
+                                               size_t capacity, const int32_t* position, const void* weights,
+                                               const int32_t* counts, const int32_t* offsets, int experts,
+                                               void* drows, size_t lddr, void* dweights, size_t tokens, int topk,
+                                               size_t cols, sar_dtype dtype, sar_dtype wdtype,
+                                               sar_stream_t stream);
+
+/*
  * sar_read_device_status -- synchronises `stream`, reads *d_status and returns
  * it as a sar_status (SAR_OK or SAR_ERR_TIMEOUT), or SAR_ERR_CUDA if the copy
  * fails.  Not for use inside a CUDA graph capture.

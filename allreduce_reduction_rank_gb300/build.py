@@ -30,9 +30,10 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 # Slowest first, so the parallel build finishes sooner.
 SOURCES = ["ll_writeback.cu", "ll_fused.cu", "ll_cluster.cu", "ll_cta.cu", "rsag_e4m3b15.cu", "rsag_e4m3b15_acc.cu",
            "ll.cu", "rsag_e4m3fn_acc.cu", "rsag_e4m3fn.cu", "rsag_bf16_acc.cu", "rsag_fp16_acc.cu", "rsag_fp32_acc.cu", "rsag_fp16.cu",
-           "rsag_bf16.cu", "rsag_fp32.cu", "layer_norm.cu", "experts.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
+           "rsag_bf16.cu", "rsag_fp32.cu", "layer_norm_bf16.cu", "layer_norm_fp16.cu", "layer_norm_fp32.cu",
+           "layer_norm.cu", "experts.cu", "expert_sort.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
            "noalloc.cu"]
-HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh"]
+HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-std=c++17", "-lineinfo",

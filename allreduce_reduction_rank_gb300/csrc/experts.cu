@@ -1,219 +1,369 @@
-// experts.cu -- tokens sorted by expert, their rows dispatched and combined.
+// experts.cu -- tokens' rows dispatched to their experts' segments, combined
+// again, and the combine's gradient.
 //
-// First form: one block sorts; one block per token (or segment's padding)
-// moves rows element by element.
-//
-// The sort is a stable counting sort.  Warp w of the block has the w-th run of
-// consecutive slots.  It counts its slots per expert, 32 at a time: lanes with
-// the same expert find each other (match_any), the lowest adds their number.
-// The exclusive sum of the counts over the warps, per expert, gives every warp
-// its first place in each segment, and a second walk over the slots hands the
-// places out in order.
+// All three read or write topk scattered rows for each token's row, and are
+// bound by HBM: whole rows move in granules of up to 16 bytes, a thread owns
+// one granule of a token's row at a time and has the topk rows' accesses (kJ at
+// a time) in flight together.  A token's own row is touched once.
+#include <algorithm>
+#include <initializer_list>
+
 #include "sar_device.cuh"
 #include "sar_internal.h"
 
 namespace sar {
 namespace {
 
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kBlock = 256;
 
-__device__ __forceinline__ int expert_of(const void* ids, int id_bytes, size_t i, int experts) {
-    const long long e = id_bytes == 8 ? static_cast<const long long*>(ids)[i]
-                                      : static_cast<long long>(static_cast<const int*>(ids)[i]);
-    return e >= 0 && e < experts ? static_cast<int>(e) : -1;
+// Granules: GB bytes moved by one access, as 32-bit words.
+template <int GB> struct Granule { uint32_t w[GB < 4 ? 1 : GB / 4]; };
+
+template <int GB> __device__ __forceinline__ Granule<GB> load(const void* base, size_t byte) {
+    const char* p = static_cast<const char*>(base) + byte;
+    Granule<GB> g;
+    if constexpr (GB == 16) {
+        const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
+        g.w[0] = v.x, g.w[1] = v.y, g.w[2] = v.z, g.w[3] = v.w;
+    } else if constexpr (GB == 8) {
+        asm("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(p));
+    } else if constexpr (GB == 4) {
+        asm("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(g.w[0]) : "l"(p));
+    } else if constexpr (GB == 2) {
+        g.w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else {
+        g.w[0] = *reinterpret_cast<const uint8_t*>(p);
+    }
+    return g;
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a, int id_bytes) {
-    extern __shared__ int hist[];                   // [kSortWarps][experts], then [experts + 1] offsets
-    int* offs = hist + kSortWarps * a.experts;
+template <int GB> __device__ __forceinline__ void store(void* base, size_t byte, const Granule<GB>& g) {
+    char* p = static_cast<char*>(base) + byte;
+    if constexpr (GB == 16) {
+        st_stream(reinterpret_cast<uint4*>(p), make_uint4(g.w[0], g.w[1], g.w[2], g.w[3]));
+    } else if constexpr (GB == 8) {
+        asm volatile("st.global.L1::no_allocate.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(g.w[0]), "r"(g.w[1]) : "memory");
+    } else if constexpr (GB == 4) {
+        asm volatile("st.global.L1::no_allocate.u32 [%0], %1;" ::"l"(p), "r"(g.w[0]) : "memory");
+    } else if constexpr (GB == 2) {
+        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(g.w[0]);
+    } else {
+        *reinterpret_cast<uint8_t*>(p) = static_cast<uint8_t>(g.w[0]);
+    }
+}
+
+// Elements of a granule in binary32, and back.  A 2-byte granule holds one
+// element in the low half.
+template <int DT, int GB> struct Elements { static constexpr int kN = GB / Elem<DT>::kSize; };
+
+template <int DT, int GB> __device__ __forceinline__ void widen(const Granule<GB>& g, float* x) {
+    if constexpr (GB < 4) {
+        float two[2];
+        widen_word<DT>(g.w[0], two);
+        x[0] = two[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < GB / 4; ++i) widen_word<DT>(g.w[i], x + i * PerWord<DT>::kN);
+    }
+}
+
+template <int DT, int GB> __device__ __forceinline__ Granule<GB> narrow(const float* x) {
+    Granule<GB> g;
+    if constexpr (GB < 4) {
+        const float two[2] = {x[0], 0.0f};
+        g.w[0] = narrow_word<DT>(two);
+    } else {
+#pragma unroll
+        for (int i = 0; i < GB / 4; ++i) g.w[i] = narrow_word<DT>(x + i * PerWord<DT>::kN);
+    }
+    return g;
+}
+
+// The place of slot j of token t, -1 where there is none.
+__device__ __forceinline__ int place_of(const ExpertArgs& a, size_t t, int j) {
+    if (j >= a.topk) return -1;
+    const int p = a.position[t * a.topk + j];
+    return static_cast<uint32_t>(p) < a.capacity ? p : -1;
+}
+
+// A block's threads over tokens and columns: TX threads (a power of two) for
+// each of kBlock / TX tokens; gridDim.y shares a row's granules.
+struct Shape {
+    unsigned tx, granules;       // threads, granules per row
+    unsigned token_blocks;       // blocks (x) of tokens; then one per expert
+};
+
+// Clears the padding rows of segment e.
+template <int GB> __device__ void clear_padding(const ExpertArgs& a, const Shape& sh, unsigned e, size_t es) {
+    const int64_t first = static_cast<int64_t>(a.offsets[e]) + a.counts[e], end = a.offsets[e + 1];
+    const int64_t last = end < static_cast<int64_t>(a.capacity) ? end : static_cast<int64_t>(a.capacity);
+    Granule<GB> zero = {};
+    for (int64_t p = first; p < last; ++p)
+        for (unsigned v = blockIdx.y * kBlock + threadIdx.x; v < sh.granules; v += gridDim.y * kBlock)
+            store<GB>(a.out, (static_cast<size_t>(p) * a.ldo) * es + static_cast<size_t>(v) * GB, zero);
+}
+
+constexpr int kJ = 8;
+
+template <int GB>
+__global__ void __launch_bounds__(kBlock) dispatch_kernel(ExpertArgs a, Shape sh, unsigned es) {
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* mine = hist + warp * a.experts;
-    for (int i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
-    const size_t per = (static_cast<size_t>(a.slots) + kSortThreads - 1) / kSortThreads * 32;
-    const size_t begin = per * warp, end = begin + per < a.slots ? begin + per : a.slots;
-    for (size_t i0 = begin; i0 < end; i0 += 32) {
-        const size_t i = i0 + lane;
-        const int e = i < end ? expert_of(a.ids, id_bytes, i, a.experts) : -1;
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
+    if (blockIdx.x >= sh.token_blocks) {
+        clear_padding<GB>(a, sh, blockIdx.x - sh.token_blocks, es);
+        return;
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kSortThreads) {
-        int sum = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = hist[w * a.experts + e];
-            hist[w * a.experts + e] = sum;
-            sum += c;
+    const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    if (t >= a.tokens) return;
+    const unsigned first = blockIdx.y * sh.tx + threadIdx.x % sh.tx, step = gridDim.y * sh.tx;
+    for (int j0 = 0; j0 < a.topk; j0 += kJ) {
+        int p[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) p[j] = place_of(a, t, j0 + j);
+        for (unsigned v = first; v < sh.granules; v += step) {
+            const Granule<GB> g = load<GB>(a.tok, t * a.ldt * es + static_cast<size_t>(v) * GB);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+                if (p[j] >= 0) store<GB>(a.out, static_cast<size_t>(p[j]) * a.ldo * es + static_cast<size_t>(v) * GB, g);
         }
-        a.counts[e] = sum;
-        offs[e + 1] = (sum + a.align - 1) / a.align * a.align;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        offs[0] = 0;
-        for (int e = 0; e < a.experts; ++e) offs[e + 1] += offs[e];
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) a.offsets[e] = offs[e];
-    if (a.source != nullptr) {
-        for (uint32_t p = threadIdx.x; p < a.capacity; p += kSortThreads) a.source[p] = -1;
-    }
-    __syncthreads();
-    for (size_t i0 = begin; i0 < end; i0 += 32) {
-        const size_t i = i0 + lane;
-        const int e = i < end ? expert_of(a.ids, id_bytes, i, a.experts) : -1;
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
-        int place = -1;
-        if (e >= 0) place = offs[e] + mine[e] + __popc(peers & ((1u << lane) - 1));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-        if (place >= 0 && static_cast<uint32_t>(place) >= a.capacity) place = -1;
-        if (i < end) a.position[i] = place;
-        if (place >= 0 && a.source != nullptr) a.source[place] = static_cast<int>(i);
     }
 }
 
-// Rows of the padding of segment e: offsets[e] + counts[e] .. offsets[e + 1] - 1,
-// as far as they exist.
-template <typename T> __device__ void clear_padding(const ExpertArgs& a, size_t e) {
-    const long long first = static_cast<long long>(a.offsets[e]) + a.counts[e];
-    const long long last = a.offsets[e + 1] < a.capacity ? a.offsets[e + 1] : static_cast<long long>(a.capacity);
-    for (long long p = first; p < last; ++p)
-        for (size_t c = threadIdx.x; c < a.cols; c += blockDim.x)
-            static_cast<T*>(a.out)[static_cast<size_t>(p) * a.ldo + c] = T(0);
+template <int WDT> __device__ __forceinline__ float weight_at(const ExpertArgs& a, size_t slot) {
+    return a.weights != nullptr ? load_elem<WDT>(a.weights, slot) : 1.0f;
 }
 
-__device__ __forceinline__ bool kept(const ExpertArgs& a, int p) {
-    return p >= 0 && static_cast<uint32_t>(p) < a.capacity;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(ExpertArgs a) {
+// out = sum of w * row over the kept slots.  The sum starts from -0, the exact
+// identity of the round-to-nearest add, so that one row is copied bit for bit.
+template <int DT, int WDT, int GB>
+__global__ void __launch_bounds__(kBlock) combine_kernel(ExpertArgs a, Shape sh) {
+    constexpr int N = Elements<DT, GB>::kN;
+    constexpr size_t es = Elem<DT>::kSize;
     pdl_wait();
-    const size_t n = a.tokens + (a.counts != nullptr ? a.experts : 0);
-    for (size_t t = blockIdx.x; t < n; t += gridDim.x) {
-        if (t >= a.tokens) {
-            clear_padding<T>(a, t - a.tokens);
-            continue;
-        }
-        for (size_t c = threadIdx.x; c < a.cols; c += kThreads) {
-            const T v = static_cast<const T*>(a.tok)[t * a.ldt + c];
-            for (int j = 0; j < a.topk; ++j) {
-                const int p = a.position[t * a.topk + j];
-                if (kept(a, p)) static_cast<T*>(a.out)[static_cast<size_t>(p) * a.ldo + c] = v;
-            }
-        }
-    }
-}
-
-template <int DT, int WDT>
-__global__ void __launch_bounds__(kThreads) combine_kernel(ExpertArgs a) {
-    pdl_wait();
-    for (size_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        for (size_t c = threadIdx.x; c < a.cols; c += kThreads) {
-            float acc = 0.0f;
-            bool first = true;
-            for (int j = 0; j < a.topk; ++j) {
-                const int p = a.position[t * a.topk + j];
-                if (!kept(a, p)) continue;
-                const float v = load_elem<DT>(a.rows_in, static_cast<size_t>(p) * a.ldi + c);
-                if (a.weights != nullptr) acc = __fmaf_rn(load_elem<WDT>(a.weights, t * a.topk + j), v, acc);
-                else acc = first ? v : __fadd_rn(acc, v);
-                first = false;
-            }
-            store_elem<DT>(a.out, t * a.ldo + c, acc);
-        }
-    }
-}
-
-template <int DT, int WDT>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(ExpertArgs a) {
-    __shared__ float red[kThreads / 32];
-    pdl_wait();
-    const size_t n = a.tokens + (a.counts != nullptr ? a.experts : 0);
-    for (size_t t = blockIdx.x; t < n; t += gridDim.x) {
-        if (t >= a.tokens) {
-            if (Elem<DT>::kSize == 4) clear_padding<uint32_t>(a, t - a.tokens);
-            else clear_padding<uint16_t>(a, t - a.tokens);
-            continue;
-        }
-        for (int j = 0; j < a.topk; ++j) {
-            const size_t slot = t * a.topk + j;
-            const int p = a.position[slot];
-            float dot = 0.0f;
-            if (kept(a, p)) {
-                const float w = load_elem<WDT>(a.weights, slot);
-                for (size_t c = threadIdx.x; c < a.cols; c += kThreads) {
-                    const float d = load_elem<DT>(a.tok, t * a.ldt + c);
-                    if (a.dweights != nullptr)
-                        dot = __fmaf_rn(d, load_elem<DT>(a.rows_in, static_cast<size_t>(p) * a.ldi + c), dot);
-                    store_elem<DT>(a.out, static_cast<size_t>(p) * a.ldo + c, __fmul_rn(w, d));
+    const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    if (t >= a.tokens) return;
+    const unsigned first = blockIdx.y * sh.tx + threadIdx.x % sh.tx, step = gridDim.y * sh.tx;
+    for (unsigned v = first; v < sh.granules; v += step) {
+        float acc[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = -0.0f;
+        bool any = false;
+        for (int j0 = 0; j0 < a.topk; j0 += kJ) {
+            int p[kJ];
+            Granule<GB> g[kJ];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) p[j] = place_of(a, t, j0 + j);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+                if (p[j] >= 0) g[j] = load<GB>(a.rows_in, static_cast<size_t>(p[j]) * a.ldi * es + static_cast<size_t>(v) * GB);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                if (p[j] < 0) continue;
+                any = true;
+                float x[N];
+                widen<DT, GB>(g[j], x);
+                if (a.weights != nullptr) {
+                    const float w = load_elem<WDT>(a.weights, t * a.topk + j0 + j);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[e] = __fmaf_rn(w, x[e], acc[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], x[e]);
                 }
             }
-            if (a.dweights == nullptr) continue;
+        }
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xFFFFFFFFu, dot, d));
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                float s = 0.0f;
-                for (int w = 0; w < kThreads / 32; ++w) s = __fadd_rn(s, red[w]);
-                store_elem<WDT>(a.dweights, slot, s);
+        for (int e = 0; e < N; ++e) acc[e] = any ? acc[e] : 0.0f;
+        store<GB>(a.out, t * a.ldo * es + static_cast<size_t>(v) * GB, narrow<DT, GB>(acc));
+    }
+}
+
+// drows = w * dout, dweights = <dout, row>.  TX threads (whole warps) have a
+// token's row; gridDim.y shares the slots, J at a time.  The dot products are
+// summed over the threads in a fixed order.
+template <int DT, int WDT, int GB, int TX, int J>
+__global__ void __launch_bounds__(kBlock) combine_backward_kernel(ExpertArgs a, Shape sh) {
+    constexpr int N = Elements<DT, GB>::kN, W = TX / 32;
+    constexpr size_t es = Elem<DT>::kSize;
+    __shared__ float red[W > 1 ? W : 1][J];
+    pdl_wait();
+    if (blockIdx.x >= sh.token_blocks) {
+        if (blockIdx.y == 0) {
+            const unsigned e = blockIdx.x - sh.token_blocks;
+            const int64_t first = static_cast<int64_t>(a.offsets[e]) + a.counts[e], end = a.offsets[e + 1];
+            const int64_t last = end < static_cast<int64_t>(a.capacity) ? end : static_cast<int64_t>(a.capacity);
+            Granule<GB> zero = {};
+            for (int64_t p = first; p < last; ++p)
+                for (unsigned v = threadIdx.x; v < sh.granules; v += kBlock)
+                    store<GB>(a.out, static_cast<size_t>(p) * a.ldo * es + static_cast<size_t>(v) * GB, zero);
+        }
+        return;
+    }
+    const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / TX) + threadIdx.x / TX;
+    const unsigned x = threadIdx.x % TX;
+    if (t >= a.tokens) return;                        // whole warps; with W > 1 never
+    for (int j0 = blockIdx.y * J; j0 < a.topk; j0 += gridDim.y * J) {
+        int p[J];
+        float w[J], dot[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            p[j] = place_of(a, t, j0 + j);
+            w[j] = p[j] >= 0 ? load_elem<WDT>(a.weights, t * a.topk + j0 + j) : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (unsigned v = x; v < sh.granules; v += TX) {
+            const size_t at = static_cast<size_t>(v) * GB;
+            const Granule<GB> gd = load<GB>(a.tok, t * a.ldt * es + at);
+            Granule<GB> g[J];
+            if (a.dweights != nullptr) {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (p[j] >= 0) g[j] = load<GB>(a.rows_in, static_cast<size_t>(p[j]) * a.ldi * es + at);
             }
+            float d[N];
+            widen<DT, GB>(gd, d);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (p[j] < 0) continue;
+                float y[N];
+                if (a.dweights != nullptr) {
+                    widen<DT, GB>(g[j], y);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) dot[j] = __fmaf_rn(d[e], y[e], dot[j]);
+                }
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[e] = __fmul_rn(w[j], d[e]);
+                store<GB>(a.out, static_cast<size_t>(p[j]) * a.ldo * es + at, narrow<DT, GB>(y));
+            }
+        }
+        if (a.dweights == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) dot[j] = __fadd_rn(dot[j], __shfl_xor_sync(0xFFFFFFFFu, dot[j], k));
+        if (W == 1) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (x == 0 && j0 + j < a.topk) store_elem<WDT>(a.dweights, t * a.topk + j0 + j, dot[j]);
+        } else {
+            if ((x & 31) == 0) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) red[x / 32][j] = dot[j];
+            }
+            __syncthreads();
+            if (x < J && j0 + static_cast<int>(x) < a.topk) {
+                float s = red[0][x];
+                for (int k = 1; k < W; ++k) s = __fadd_rn(s, red[k][x]);
+                store_elem<WDT>(a.dweights, t * a.topk + j0 + x, s);
+            }
+            __syncthreads();
         }
     }
 }
 
-unsigned blocks_for(size_t items) { return static_cast<unsigned>(items < 1 ? 1 : (items > (1u << 30) ? 1u << 30 : items)); }
+// Largest granule (16, 8, 4, 2 or 1 bytes) that divides every address, leading
+// dimension and the row's length.
+unsigned granule_of(std::initializer_list<const void*> ptrs, std::initializer_list<size_t> lds, size_t cols, size_t es) {
+    size_t bits = cols * es;
+    for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
+    for (size_t ld : lds) bits |= ld * es;
+    unsigned g = 16;
+    while (bits % g != 0) g /= 2;
+    return g;
+}
+
+// Threads per row: a power of two that covers the row's granules, from `least`
+// to kBlock.  gridDim.y: shares of a row, so that a few tokens still fill the
+// SMs (about four blocks each).
+Shape shape_of(size_t tokens, size_t granules, unsigned least) {
+    Shape sh;
+    sh.tx = least;
+    while (sh.tx < kBlock && sh.tx < granules) sh.tx *= 2;
+    sh.granules = static_cast<unsigned>(granules);
+    const size_t per = kBlock / sh.tx;
+    sh.token_blocks = static_cast<unsigned>((tokens + per - 1) / per);
+    return sh;
+}
+
+unsigned row_shares(const Shape& sh) {
+    const unsigned most = (sh.granules + sh.tx - 1) / sh.tx, want = 608 / (sh.token_blocks < 608 ? sh.token_blocks : 608);
+    return want < 1 ? 1 : (want < most ? want : most);
+}
+
+template <int GB> cudaError_t dispatch(const ExpertArgs& a, size_t es, cudaStream_t s) {
+    const Shape sh = shape_of(a.tokens, a.cols * es / GB, 8);
+    const dim3 grid(sh.token_blocks + (a.counts != nullptr ? a.experts : 0), row_shares(sh));
+    return launch_kernel(dispatch_kernel<GB>, grid, dim3(kBlock), s, a, sh, static_cast<unsigned>(es));
+}
+
+template <int DT, int WDT, int GB> cudaError_t combine(const ExpertArgs& a, cudaStream_t s) {
+    const Shape sh = shape_of(a.tokens, a.cols * Elem<DT>::kSize / GB, 8);
+    return launch_kernel(combine_kernel<DT, WDT, GB>, dim3(sh.token_blocks, row_shares(sh)), dim3(kBlock), s, a, sh);
+}
+
+template <int DT, int WDT> cudaError_t combine_by_granule(const ExpertArgs& a, cudaStream_t s) {
+    constexpr int es = Elem<DT>::kSize;
+    const unsigned g = granule_of({a.rows_in, a.out}, {a.ldi, a.ldo}, a.cols, es);
+    if (g == 16) return combine<DT, WDT, 16>(a, s);
+    if (g == 8) return combine<DT, WDT, 8>(a, s);
+    if (g == 4) return combine<DT, WDT, 4>(a, s);
+    return combine<DT, WDT, es>(a, s);
+}
+
+template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const ExpertArgs& a, cudaStream_t s) {
+    Shape sh = shape_of(a.tokens, a.cols * Elem<DT>::kSize / GB, TX);
+    sh.tx = TX;
+    sh.token_blocks = static_cast<unsigned>((a.tokens + kBlock / TX - 1) / (kBlock / TX));
+    const dim3 grid(sh.token_blocks + (a.counts != nullptr ? a.experts : 0), std::min((a.topk + J - 1) / J, 65535));
+    return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(kBlock), s, a, sh);
+}
+
+template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArgs& a, cudaStream_t s) {
+    const bool narrow_rows = a.cols * Elem<DT>::kSize / GB <= 128;
+    // Few tokens: a block for each slot.
+    const bool few = a.tokens * a.topk <= 608;
+    if (narrow_rows) return few ? backward<DT, WDT, GB, 32, 1>(a, s) : backward<DT, WDT, GB, 32, 4>(a, s);
+    return few ? backward<DT, WDT, GB, 256, 1>(a, s) : backward<DT, WDT, GB, 256, 4>(a, s);
+}
+
+template <int DT, int WDT> cudaError_t backward_by_granule(const ExpertArgs& a, cudaStream_t s) {
+    constexpr int es = Elem<DT>::kSize;
+    const unsigned g = a.dweights != nullptr ? granule_of({a.tok, a.rows_in, a.out}, {a.ldt, a.ldi, a.ldo}, a.cols, es)
+                                             : granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es);
+    if (g == 16) return backward_by_shape<DT, WDT, 16>(a, s);
+    if (g == 8) return backward_by_shape<DT, WDT, 8>(a, s);
+    return backward_by_shape<DT, WDT, es>(a, s);
+}
 
 }  // namespace
 
-cudaError_t launch_expert_sort(int id_bytes, const SortArgs& a, cudaStream_t s) {
-    const size_t smem = (static_cast<size_t>(kSortWarps) * a.experts + a.experts + 1) * sizeof(int);
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
+cudaError_t launch_expert_dispatch(size_t es, const ExpertArgs& a, cudaStream_t s) {
+    switch (granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es)) {
+    case 16: return dispatch<16>(a, es, s);
+    case 8: return dispatch<8>(a, es, s);
+    case 4: return dispatch<4>(a, es, s);
+    case 2: return dispatch<2>(a, es, s);
+    default: return dispatch<1>(a, es, s);
     }
-    return launch_kernel_smem(sort_kernel, dim3(1), dim3(kSortThreads), smem, s, a, id_bytes);
-}
-
-cudaError_t launch_expert_dispatch(size_t esize, const ExpertArgs& a, cudaStream_t s) {
-    const dim3 grid(blocks_for(a.tokens + (a.counts != nullptr ? a.experts : 0)));
-    if (esize == 1) return launch_kernel(dispatch_kernel<uint8_t>, grid, dim3(kThreads), s, a);
-    if (esize == 2) return launch_kernel(dispatch_kernel<uint16_t>, grid, dim3(kThreads), s, a);
-    return launch_kernel(dispatch_kernel<uint32_t>, grid, dim3(kThreads), s, a);
 }
 
 cudaError_t launch_expert_combine(sar_dtype dt, sar_dtype wdt, const ExpertArgs& a, cudaStream_t s) {
-    const dim3 grid(blocks_for(a.tokens)), block(kThreads);
     switch (dt) {
     case SAR_BF16:
-        return wdt == SAR_FP32 ? launch_kernel(combine_kernel<SAR_BF16, SAR_FP32>, grid, block, s, a)
-                               : launch_kernel(combine_kernel<SAR_BF16, SAR_BF16>, grid, block, s, a);
+        return wdt == SAR_FP32 ? combine_by_granule<SAR_BF16, SAR_FP32>(a, s) : combine_by_granule<SAR_BF16, SAR_BF16>(a, s);
     case SAR_FP16:
-        return wdt == SAR_FP32 ? launch_kernel(combine_kernel<SAR_FP16, SAR_FP32>, grid, block, s, a)
-                               : launch_kernel(combine_kernel<SAR_FP16, SAR_FP16>, grid, block, s, a);
-    case SAR_FP32: return launch_kernel(combine_kernel<SAR_FP32, SAR_FP32>, grid, block, s, a);
+        return wdt == SAR_FP32 ? combine_by_granule<SAR_FP16, SAR_FP32>(a, s) : combine_by_granule<SAR_FP16, SAR_FP16>(a, s);
+    case SAR_FP32: return combine_by_granule<SAR_FP32, SAR_FP32>(a, s);
     default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_expert_combine_backward(sar_dtype dt, sar_dtype wdt, const ExpertArgs& a, cudaStream_t s) {
-    const dim3 grid(blocks_for(a.tokens + (a.counts != nullptr ? a.experts : 0))), block(kThreads);
     switch (dt) {
     case SAR_BF16:
-        return wdt == SAR_FP32 ? launch_kernel(combine_backward_kernel<SAR_BF16, SAR_FP32>, grid, block, s, a)
-                               : launch_kernel(combine_backward_kernel<SAR_BF16, SAR_BF16>, grid, block, s, a);
+        return wdt == SAR_FP32 ? backward_by_granule<SAR_BF16, SAR_FP32>(a, s) : backward_by_granule<SAR_BF16, SAR_BF16>(a, s);
     case SAR_FP16:
-        return wdt == SAR_FP32 ? launch_kernel(combine_backward_kernel<SAR_FP16, SAR_FP32>, grid, block, s, a)
-                               : launch_kernel(combine_backward_kernel<SAR_FP16, SAR_FP16>, grid, block, s, a);
-    case SAR_FP32: return launch_kernel(combine_backward_kernel<SAR_FP32, SAR_FP32>, grid, block, s, a);
+        return wdt == SAR_FP32 ? backward_by_granule<SAR_FP16, SAR_FP32>(a, s) : backward_by_granule<SAR_FP16, SAR_FP16>(a, s);
+    case SAR_FP32: return backward_by_granule<SAR_FP32, SAR_FP32>(a, s);
     default: return cudaErrorInvalidValue;
     }
 }

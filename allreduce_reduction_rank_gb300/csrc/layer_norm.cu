@@ -5,15 +5,19 @@
 // h = (x - mean) rstd and g = dy w:  dx = rstd (g - mean(g) - h mean(g h)),
 // dw = sum over rows of dy h,  db = sum over rows of dy.
 //
-// First form: one block per row, element by element; the parameters' gradients
-// in a kernel of their own, a thread per column over a share of the rows, and
-// a second one that adds the shares in order.
-#include "sar_device.cuh"
-#include "sar_internal.h"
+// Rows that fit a block's registers run the kernels of layer_norm.cuh.  Longer
+// ones run those here: one block per row, the row read again for each pass
+// (from L2), and the parameters' gradients in a kernel of their own, a thread
+// per column over a share of the rows.
+#include "layer_norm.cuh"
 
 namespace sar {
 namespace {
 
+// Longest rows in registers, in 16-byte vectors.
+constexpr size_t kForwardVecs = 8192, kBackwardVecs = 1024;
+
+// Shares of the rows in the parameters' gradients of longer rows.
 constexpr size_t kShares = 64;
 
 template <int WDT> __device__ __forceinline__ float param(const void* p, size_t i, float none) {
@@ -107,18 +111,46 @@ __global__ void __launch_bounds__(kThreads) norm_shares_kernel(NormGradArgs a) {
     }
 }
 
+// dweight and dbias from the shares' sums: 32 columns a block, the shares over
+// its warps, which are then added in order.
+constexpr int kParamWarps = 16;
 template <int WDT>
-__global__ void __launch_bounds__(kThreads) norm_params_kernel(NormGradArgs a, size_t shares) {
+__global__ void __launch_bounds__(kParamWarps * 32) params_kernel(NormGradArgs a, unsigned shares) {
+    __shared__ float part[kParamWarps][32];
     pdl_wait();
-    for (size_t c = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; c < a.cols;
-         c += static_cast<size_t>(gridDim.x) * kThreads) {
-        float w = 0.0f, b = 0.0f;
-        for (size_t k = 0; k < shares; ++k) {
-            w = __fadd_rn(w, a.partial[k * 2 * a.cols + c]);
-            b = __fadd_rn(b, a.partial[(k * 2 + 1) * a.cols + c]);
+    const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool bias = blockIdx.y != 0;
+    void* out = bias ? a.dbias : a.dweight;
+    if (out == nullptr) return;
+    for (size_t c0 = static_cast<size_t>(blockIdx.x) * 32; c0 < a.cols; c0 += static_cast<size_t>(gridDim.x) * 32) {
+        const size_t c = c0 + lane;
+        float v = 0.0f;
+        if (c < a.cols) {
+#pragma unroll 4
+            for (unsigned k = warp; k < shares; k += kParamWarps)
+                v = __fadd_rn(v, a.partial[(static_cast<size_t>(k) * 2 + bias) * a.cols + c]);
         }
-        if (a.dweight != nullptr) store_elem<WDT>(a.dweight, c, w);
-        if (a.dbias != nullptr) store_elem<WDT>(a.dbias, c, b);
+        part[warp][lane] = v;
+        __syncthreads();
+        if (warp == 0 && c < a.cols) {
+            for (int w = 1; w < kParamWarps; ++w) v = __fadd_rn(v, part[w][lane]);
+            store_elem<WDT>(out, c, v);
+        }
+        __syncthreads();
+    }
+}
+
+template <int WDT> cudaError_t params(const NormGradArgs& a, unsigned shares, cudaStream_t s) {
+    const size_t blocks = (a.cols + 31) / 32;
+    return launch_kernel(params_kernel<WDT>, dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), 2),
+                         dim3(kParamWarps * 32), s, a, shares);
+}
+
+cudaError_t params_of(sar_dtype wdt, const NormGradArgs& a, unsigned shares, cudaStream_t s) {
+    switch (wdt) {
+    case SAR_BF16: return params<SAR_BF16>(a, shares, s);
+    case SAR_FP16: return params<SAR_FP16>(a, shares, s);
+    default: return params<SAR_FP32>(a, shares, s);
     }
 }
 
@@ -127,43 +159,81 @@ unsigned blocks_for(size_t items, size_t per, size_t cap) {
     return static_cast<unsigned>(g < 1 ? 1 : (g > cap ? cap : g));
 }
 
-template <int DT, int WDT> cudaError_t norm(const NormArgs& a, cudaStream_t s) {
+template <int DT, int WDT> cudaError_t long_forward(const NormArgs& a, cudaStream_t s) {
     return launch_kernel(norm_rows_kernel<DT, WDT>, dim3(blocks_for(a.rows, 1, 1u << 30)), dim3(kThreads), s, a);
 }
 
-template <int DT, int WDT> cudaError_t norm_backward(const NormGradArgs& a, cudaStream_t s) {
-    cudaError_t e = cudaSuccess;
+template <int DT, int WDT> cudaError_t long_backward(const NormGradArgs& a, unsigned shares, cudaStream_t s) {
     if (a.dweight != nullptr || a.dbias != nullptr) {
-        const size_t shares = layer_norm_partials(a.rows, a.cols);
-        const unsigned gx = blocks_for(a.cols, kThreads, 1024);
-        e = launch_kernel(norm_shares_kernel<DT>, dim3(gx, static_cast<unsigned>(shares)), dim3(kThreads), s, a);
+        const cudaError_t e = launch_kernel(norm_shares_kernel<DT>, dim3(blocks_for(a.cols, kThreads, 65535), shares),
+                                            dim3(kThreads), s, a);
         if (e != cudaSuccess) return e;
-        e = launch_kernel(norm_params_kernel<WDT>, dim3(gx), dim3(kThreads), s, a, shares);
-        if (e != cudaSuccess || a.rows == 0) return e;
     }
     return launch_kernel(norm_dx_kernel<DT, WDT>, dim3(blocks_for(a.rows, 1, 1u << 30)), dim3(kThreads), s, a);
 }
 
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Rows of `cols` elements of `es` bytes move as whole 16-byte vectors.
+bool rows_on16(const void* p, size_t ld, size_t rows, size_t es) { return on16(p) && (rows <= 1 || ld * es % 16 == 0); }
+
+template <int DT> cudaError_t forward_of(sar_dtype wdt, const NormArgs& a, cudaStream_t s) {
+    constexpr size_t es = Elem<DT>::kSize, VE = Elem<DT>::kVE;
+    if ((a.cols + VE - 1) / VE > kForwardVecs)
+        return wdt == SAR_FP32 ? long_forward<DT, SAR_FP32>(a, s) : long_forward<DT, DT>(a, s);
+    const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.y, a.ldy, a.rows, es) &&
+                     on16(a.weight) && on16(a.bias);
+    return norm::forward<DT>(a, wdt == SAR_FP32, vec, s);
+}
+
+// Blocks of the register kernel: enough groups for the rows, at most what the
+// SMs hold at a time.
+template <int DT> unsigned backward_blocks(size_t rows, size_t cols) {
+    const int tpr = norm::backward_tpr((cols + Elem<DT>::kVE - 1) / Elem<DT>::kVE);
+    const int groups = tpr > 512 ? 1 : 512 / tpr;
+    const size_t need = (rows + groups - 1) / groups, fit = tpr > 512 ? norm::kSMs : 2 * norm::kSMs;
+    return static_cast<unsigned>(need < fit ? need : fit);
+}
+
+template <int DT> cudaError_t backward_of(sar_dtype wdt, const NormGradArgs& a, cudaStream_t s) {
+    constexpr size_t es = Elem<DT>::kSize, VE = Elem<DT>::kVE;
+    unsigned shares = 0;
+    cudaError_t e = cudaSuccess;
+    if (a.rows != 0 && (a.cols + VE - 1) / VE > kBackwardVecs) {
+        shares = static_cast<unsigned>(a.rows < kShares ? a.rows : kShares);
+        e = wdt == SAR_FP32 ? long_backward<DT, SAR_FP32>(a, shares, s) : long_backward<DT, DT>(a, shares, s);
+    } else if (a.rows != 0) {
+        const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.dy, a.lddy, a.rows, es) &&
+                         rows_on16(a.dx, a.lddx, a.rows, es) && on16(a.weight);
+        shares = backward_blocks<DT>(a.rows, a.cols);
+        e = norm::backward<DT>(a, wdt == SAR_FP32, vec, shares, s);
+    }
+    if (e != cudaSuccess || (a.dweight == nullptr && a.dbias == nullptr)) return e;
+    return params_of(wdt, a, shares, s);
+}
+
 }  // namespace
 
-size_t layer_norm_partials(size_t rows, size_t) { return rows < 1 ? 1 : (rows < kShares ? rows : kShares); }
+// Rows of sums in the workspace: the most that any element type writes.
+size_t layer_norm_partials(size_t rows, size_t) {
+    const size_t most = 2 * norm::kSMs;
+    return rows < 1 ? 1 : (rows < most ? rows : most);
+}
 
 cudaError_t launch_layer_norm(sar_dtype dt, sar_dtype wdt, const NormArgs& a, cudaStream_t s) {
     switch (dt) {
-    case SAR_BF16: return wdt == SAR_FP32 ? norm<SAR_BF16, SAR_FP32>(a, s) : norm<SAR_BF16, SAR_BF16>(a, s);
-    case SAR_FP16: return wdt == SAR_FP32 ? norm<SAR_FP16, SAR_FP32>(a, s) : norm<SAR_FP16, SAR_FP16>(a, s);
-    case SAR_FP32: return norm<SAR_FP32, SAR_FP32>(a, s);
+    case SAR_BF16: return forward_of<SAR_BF16>(wdt, a, s);
+    case SAR_FP16: return forward_of<SAR_FP16>(wdt, a, s);
+    case SAR_FP32: return forward_of<SAR_FP32>(wdt, a, s);
     default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_layer_norm_backward(sar_dtype dt, sar_dtype wdt, const NormGradArgs& a, cudaStream_t s) {
     switch (dt) {
-    case SAR_BF16:
-        return wdt == SAR_FP32 ? norm_backward<SAR_BF16, SAR_FP32>(a, s) : norm_backward<SAR_BF16, SAR_BF16>(a, s);
-    case SAR_FP16:
-        return wdt == SAR_FP32 ? norm_backward<SAR_FP16, SAR_FP32>(a, s) : norm_backward<SAR_FP16, SAR_FP16>(a, s);
-    case SAR_FP32: return norm_backward<SAR_FP32, SAR_FP32>(a, s);
+    case SAR_BF16: return backward_of<SAR_BF16>(wdt, a, s);
+    case SAR_FP16: return backward_of<SAR_FP16>(wdt, a, s);
+    case SAR_FP32: return backward_of<SAR_FP32>(wdt, a, s);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -1,0 +1,13 @@
+// layer_norm_fp16.cu -- the layer norm kernels of fp16 rows.
+#include "layer_norm.cuh"
+
+namespace sar {
+namespace norm {
+template <> cudaError_t forward<SAR_FP16>(const NormArgs& a, bool w32, bool vec, cudaStream_t s) {
+    return forward_any<SAR_FP16>(a, w32, vec, s);
+}
+template <> cudaError_t backward<SAR_FP16>(const NormGradArgs& a, bool w32, bool vec, unsigned blocks, cudaStream_t s) {
+    return backward_any<SAR_FP16>(a, w32, vec, blocks, s);
+}
+}  // namespace norm
+}  // namespace sar

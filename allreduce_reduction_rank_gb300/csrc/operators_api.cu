@@ -144,7 +144,7 @@ SAR_API sar_status sar_expert_dispatch(const void* x, size_t ldx, const int32_t*
                                        sar_stream_t stream) {
     const size_t es = esize_of(dtype);
     if (es == 0) return SAR_ERR_UNSUPPORTED_DTYPE;
-    if (!slots_fit(tokens, topk) || capacity > kMaxSlots || !extent_fits(tokens, cols, ldx, es) ||
+    if (!slots_fit(tokens, topk) || capacity > kMaxSlots || cols > kMaxSlots || !extent_fits(tokens, cols, ldx, es) ||
         !extent_fits(capacity, cols, ldr, es))
         return SAR_ERR_INVALID_ARG;
     sar_status st = check_segments(counts, offsets, experts);
@@ -163,7 +163,7 @@ SAR_API sar_status sar_expert_combine(const void* rows, size_t ldr, size_t capac
                                       size_t cols, sar_dtype dtype, sar_dtype wdtype, sar_stream_t stream) {
     if (!dtypes_ok(dtype, wdtype)) return SAR_ERR_UNSUPPORTED_DTYPE;
     const size_t es = esize_of(dtype);
-    if (!slots_fit(tokens, topk) || capacity > kMaxSlots || !extent_fits(tokens, cols, ldo, es) ||
+    if (!slots_fit(tokens, topk) || capacity > kMaxSlots || cols > kMaxSlots || !extent_fits(tokens, cols, ldo, es) ||
         !extent_fits(capacity, cols, ldr, es))
         return SAR_ERR_INVALID_ARG;
     if (tokens == 0 || cols == 0) return SAR_OK;
@@ -184,7 +184,7 @@ SAR_API sar_status sar_expert_combine_backward(const void* dout, size_t ldo, con
                                                sar_stream_t stream) {
     if (!dtypes_ok(dtype, wdtype)) return SAR_ERR_UNSUPPORTED_DTYPE;
     const size_t es = esize_of(dtype), ws = esize_of(wdtype);
-    if (!slots_fit(tokens, topk) || capacity > kMaxSlots || !extent_fits(tokens, cols, ldo, es) ||
+    if (!slots_fit(tokens, topk) || capacity > kMaxSlots || cols > kMaxSlots || !extent_fits(tokens, cols, ldo, es) ||
         !extent_fits(capacity, cols, lddr, es) || (dweights != nullptr && !extent_fits(capacity, cols, ldr, es)))
         return SAR_ERR_INVALID_ARG;
     sar_status st = check_segments(counts, offsets, experts);

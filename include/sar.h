@@ -561,6 +561,8 @@ SAR_API sar_status sar_expert_sort(const void* ids, int id_bytes, size_t tokens,
  * without, they are left as they are, as rows past the last segment always are.
  *
  * x : tokens x cols, rows : capacity x cols, position : tokens * topk values.
+ * topk >= 1, and tokens * topk, capacity and cols at most 2^31 - 1, else
+ * SAR_ERR_INVALID_ARG (also in the calls below).
  * The gradient with respect to x is sar_expert_combine without weights.
  */
 SAR_API sar_status sar_expert_dispatch(const void* x, size_t ldx, const int32_t* position, const int32_t* counts,

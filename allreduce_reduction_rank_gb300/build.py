@@ -33,7 +33,7 @@ SOURCES = ["ll_writeback.cu", "ll_fused.cu", "ll_cluster.cu", "ll_cta.cu", "rsag
            "rsag_bf16.cu", "rsag_fp32.cu", "layer_norm_bf16.cu", "layer_norm_fp16.cu", "layer_norm_fp32.cu",
            "layer_norm.cu", "experts.cu", "expert_sort.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
            "noalloc.cu"]
-HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh"]
+HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh", "layer_norm_ring.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-std=c++17", "-lineinfo",

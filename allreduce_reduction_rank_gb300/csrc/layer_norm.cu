@@ -9,7 +9,7 @@
 // ones run those here: one block per row, the row read again for each pass
 // (from L2), and the parameters' gradients in a kernel of their own, a thread
 // per column over a share of the rows.
-#include "layer_norm.cuh"
+#include "layer_norm_ring.cuh"
 
 namespace sar {
 namespace {
@@ -126,9 +126,17 @@ __global__ void __launch_bounds__(kParamWarps * 32) params_kernel(NormGradArgs a
         const size_t c = c0 + lane;
         float v = 0.0f;
         if (c < a.cols) {
-#pragma unroll 4
-            for (unsigned k = warp; k < shares; k += kParamWarps)
-                v = __fadd_rn(v, a.partial[(static_cast<size_t>(k) * 2 + bias) * a.cols + c]);
+            // Ten shares' loads in flight at a time.
+            for (unsigned k0 = warp; k0 < shares; k0 += 10 * kParamWarps) {
+                float p[10];
+#pragma unroll
+                for (int i = 0; i < 10; ++i) {
+                    const unsigned k = k0 + i * kParamWarps;
+                    p[i] = k < shares ? a.partial[(static_cast<size_t>(k) * 2 + bias) * a.cols + c] : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 10; ++i) v = __fadd_rn(v, p[i]);
+            }
         }
         part[warp][lane] = v;
         __syncthreads();
@@ -177,8 +185,26 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Rows of `cols` elements of `es` bytes move as whole 16-byte vectors.
 bool rows_on16(const void* p, size_t ld, size_t rows, size_t es) { return on16(p) && (rows <= 1 || ld * es % 16 == 0); }
 
+// The same with words of 4 bytes.
+bool rows_on4(const void* p, size_t ld, size_t rows, size_t es) {
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && (rows <= 1 || ld * es % 4 == 0);
+}
+
+// Rows that give every group of the ring kernels' blocks two or more.
+bool many_rows(size_t rows, size_t vecs) {
+    size_t tpr = 32;
+    while (tpr < norm::kRingThreads && tpr < vecs) tpr *= 2;
+    return rows >= 2 * norm::kSMs * (norm::kRingThreads / tpr);
+}
+
 template <int DT> cudaError_t forward_of(sar_dtype wdt, const NormArgs& a, cudaStream_t s) {
     constexpr size_t es = Elem<DT>::kSize, VE = Elem<DT>::kVE;
+    const size_t vecs = (a.cols * es + 15) / 16;
+    if (vecs > 16 && vecs <= norm::kRingVecs && many_rows(a.rows, vecs) && a.cols * es % 4 == 0 &&
+        rows_on4(a.x, a.ldx, a.rows, es) && rows_on4(a.y, a.ldy, a.rows, es)) {
+        const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.y, a.ldy, a.rows, es);
+        return norm::ring_forward<DT>(a, wdt == SAR_FP32, vec, vecs, s);
+    }
     if ((a.cols + VE - 1) / VE > kForwardVecs)
         return wdt == SAR_FP32 ? long_forward<DT, SAR_FP32>(a, s) : long_forward<DT, DT>(a, s);
     const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.y, a.ldy, a.rows, es) &&
@@ -199,7 +225,14 @@ template <int DT> cudaError_t backward_of(sar_dtype wdt, const NormGradArgs& a, 
     constexpr size_t es = Elem<DT>::kSize, VE = Elem<DT>::kVE;
     unsigned shares = 0;
     cudaError_t e = cudaSuccess;
-    if (a.rows != 0 && (a.cols + VE - 1) / VE > kBackwardVecs) {
+    const size_t vecs = (a.cols * es + 15) / 16;
+    if (vecs > 16 && vecs <= norm::kRingVecs && many_rows(a.rows, vecs) && a.cols * es % 4 == 0 &&
+        rows_on4(a.x, a.ldx, a.rows, es) && rows_on4(a.dy, a.lddy, a.rows, es) && rows_on4(a.dx, a.lddx, a.rows, es)) {
+        const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.dy, a.lddy, a.rows, es) &&
+                         rows_on16(a.dx, a.lddx, a.rows, es);
+        shares = norm::kSMs;
+        e = norm::ring_backward<DT>(a, wdt == SAR_FP32, vec, vecs, s);
+    } else if (a.rows != 0 && (a.cols + VE - 1) / VE > kBackwardVecs) {
         shares = static_cast<unsigned>(a.rows < kShares ? a.rows : kShares);
         e = wdt == SAR_FP32 ? long_backward<DT, SAR_FP32>(a, shares, s) : long_backward<DT, DT>(a, shares, s);
     } else if (a.rows != 0) {

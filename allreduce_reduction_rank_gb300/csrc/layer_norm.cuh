@@ -11,6 +11,8 @@
 //            row.
 #pragma once
 
+#include <atomic>
+
 #include "sar_device.cuh"
 #include "sar_internal.h"
 
@@ -57,29 +59,41 @@ __device__ __forceinline__ void load_row(Raw<DT, NV>& r, const void* base, size_
     }
 }
 
-template <int DT> __device__ __forceinline__ void widen(const uint4& v, float* x) {
+// Arithmetic on pairs of elements: one instruction for two (add, mul and fma on
+// .f32x2, each half rounded as the scalar one).  The kernels below issue close
+// to what the SMs can while HBM streams, so the count matters.
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+
+// A vector's elements in pairs, in binary32.
+template <int DT> __device__ __forceinline__ void widen(const uint4& v, float2* x) {
     constexpr int W = PerWord<DT>::kN;
-    widen_word<DT>(v.x, x);
-    widen_word<DT>(v.y, x + W);
-    widen_word<DT>(v.z, x + 2 * W);
-    widen_word<DT>(v.w, x + 3 * W);
+    float f[4 * W];
+    widen_word<DT>(v.x, f);
+    widen_word<DT>(v.y, f + W);
+    widen_word<DT>(v.z, f + 2 * W);
+    widen_word<DT>(v.w, f + 3 * W);
+#pragma unroll
+    for (int p = 0; p < 2 * W; ++p) x[p] = make_float2(f[2 * p], f[2 * p + 1]);
 }
 
 // Stores vector i of a row.
 template <int DT, int TPR, bool kVec>
-__device__ __forceinline__ void store_vec(void* base, size_t first, int i, unsigned t, unsigned cols, const float* x) {
+__device__ __forceinline__ void store_vec(void* base, size_t first, int i, unsigned t, unsigned cols, const float2* x) {
     constexpr int VE = Elem<DT>::kVE, W = PerWord<DT>::kN;
+    float f[VE];
+#pragma unroll
+    for (int p = 0; p < VE / 2; ++p) f[2 * p] = x[p].x, f[2 * p + 1] = x[p].y;
     if (kVec) {
         const unsigned k = i * TPR + t;
         if (k * VE < cols)
             st_stream(reinterpret_cast<uint4*>(static_cast<char*>(base) + first * Elem<DT>::kSize) + k,
-                      make_uint4(narrow_word<DT>(x), narrow_word<DT>(x + W), narrow_word<DT>(x + 2 * W),
-                                 narrow_word<DT>(x + 3 * W)));
+                      make_uint4(narrow_word<DT>(f), narrow_word<DT>(f + W), narrow_word<DT>(f + 2 * W),
+                                 narrow_word<DT>(f + 3 * W)));
     } else {
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             const unsigned c = (i * VE + e) * TPR + t;
-            if (c < cols) store_elem<DT>(base, first + c, x[e]);
+            if (c < cols) store_elem<DT>(base, first + c, f[e]);
         }
     }
 }
@@ -87,34 +101,36 @@ __device__ __forceinline__ void store_vec(void* base, size_t first, int i, unsig
 // Vector i of a parameter (type fp32 or DT; the kVec layout needs it on a
 // 16-byte boundary), or `none` where there is no parameter.
 template <int DT, int TPR, bool kVec>
-__device__ __forceinline__ void load_param(const void* p, bool w32, int i, unsigned t, unsigned cols, float none, float* x) {
+__device__ __forceinline__ void load_param(const void* p, bool w32, int i, unsigned t, unsigned cols, float none,
+                                           float2* x) {
     constexpr int VE = Elem<DT>::kVE;
     if (p == nullptr) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[e] = none;
+        for (int e = 0; e < VE / 2; ++e) x[e] = pair(none);
     } else if (kVec) {
         const unsigned k = i * TPR + t;
-        if (k * VE < cols) {
-            if (w32) {
-                const float4* f = static_cast<const float4*>(p) + k * (VE / 4);
+        if (k * VE >= cols) {
 #pragma unroll
-                for (int q = 0; q < VE / 4; ++q) {
-                    const float4 v = f[q];
-                    x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
-                }
-            } else {
-                widen<DT>(static_cast<const uint4*>(p)[k], x);
+            for (int e = 0; e < VE / 2; ++e) x[e] = pair(none);
+        } else if (w32) {
+            const float4* f = static_cast<const float4*>(p) + k * (VE / 4);
+#pragma unroll
+            for (int q = 0; q < VE / 4; ++q) {
+                const float4 v = f[q];
+                x[2 * q] = make_float2(v.x, v.y), x[2 * q + 1] = make_float2(v.z, v.w);
             }
         } else {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[e] = none;
+            widen<DT>(static_cast<const uint4*>(p)[k], x);
         }
     } else {
+        float f[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             const unsigned c = (i * VE + e) * TPR + t;
-            x[e] = c >= cols ? none : (w32 ? static_cast<const float*>(p)[c] : load_elem<DT>(p, c));
+            f[e] = c >= cols ? none : (w32 ? static_cast<const float*>(p)[c] : load_elem<DT>(p, c));
         }
+#pragma unroll
+        for (int e = 0; e < VE / 2; ++e) x[e] = make_float2(f[2 * e], f[2 * e + 1]);
     }
 }
 
@@ -131,6 +147,30 @@ template <int TPR> __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+__device__ __forceinline__ float2 shfl_xor2(float2 v, int d) {
+    return make_float2(__shfl_xor_sync(0xFFFFFFFFu, v.x, d), __shfl_xor_sync(0xFFFFFFFFu, v.y, d));
+}
+
+// Two sums over groups of N lanes.
+template <int N> __device__ __forceinline__ float2 lanes_sum2(float2 v) {
+#pragma unroll
+    for (int d = N / 2; d > 0; d >>= 1) v = __fadd2_rn(v, shfl_xor2(v, d));
+    return v;
+}
+
+// s / n from the rounded 1 / n, corrected by the remainder.
+__device__ __forceinline__ float quotient(float s, float n, float inv_n) {
+    const float m = __fmul_rn(s, inv_n);
+    return fabsf(m) < __int_as_float(0x7F800000) ? __fmaf_rn(__fmaf_rn(-m, n, s), inv_n, m) : m;
+}
+
+// A warp's squares around `mean` from its sum, its squares q around its own m,
+// and its number of elements (p = s, q, m, n).
+__device__ __forceinline__ float around(const float4& p, float mean) {
+    const float d = __fsub_rn(p.z, mean), off = __fmaf_rn(-p.w, p.z, p.x);
+    return __fmaf_rn(__fmaf_rn(p.w, d, __fmul_rn(2.0f, off)), d, p.y);
+}
+
 // A barrier among the TPR threads of group g of the block.
 template <int TPR, int BT> __device__ __forceinline__ void group_sync(int g) {
     if (TPR == BT) __syncthreads();
@@ -143,12 +183,28 @@ template <int TPR, int BT> __device__ __forceinline__ void group_sync(int g) {
 //   mean = sum s_w / n,   sum (x - mean)^2 = sum (q_w + n_w (m_w - mean)^2),
 // which keeps the digits that sum x^2 - n mean^2 would lose.
 // ---------------------------------------------------------------------------
-template <int DT, int TPR, int NV, bool kVec>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) forward_kernel(NormArgs a, bool w32) {
-    constexpr int VE = Elem<DT>::kVE, BT = TPR < 128 ? 128 : TPR, RPB = BT / TPR, WPG = TPR > 32 ? TPR / 32 : 1;
+// The parameters are loaded after the statistics, except with kEarly (one vector
+// a thread, for calls of few rows, where the loads' latency counts).
+template <int TPR, int NV> struct ForwardShape {
+    static constexpr int kThreads = TPR < 128 ? 128 : TPR;
+    // Resident blocks to compile for: 1024 threads an SM (64 registers).
+    static constexpr int kBlocks = NV > 4 ? 1 : 1024 / kThreads;
+};
+
+template <int DT, int TPR, int NV, bool kVec, bool kEarly>
+__global__ void __launch_bounds__(ForwardShape<TPR, NV>::kThreads, ForwardShape<TPR, NV>::kBlocks)
+forward_kernel(NormArgs a, bool w32, float inv_n) {
+    constexpr int VE = Elem<DT>::kVE, P = VE / 2, BT = ForwardShape<TPR, NV>::kThreads, RPB = BT / TPR;
+    constexpr int WPG = TPR > 32 ? TPR / 32 : 1;
     __shared__ float4 red[TPR > 32 ? WPG : 1];
-    pdl_wait();
     const unsigned t = threadIdx.x % TPR, cols = static_cast<unsigned>(a.cols);
+    const float n = static_cast<float>(cols);
+    pdl_wait();
+    float2 we[kEarly ? P : 1], be[kEarly ? P : 1];
+    if (kEarly) {
+        load_param<DT, TPR, kVec>(a.weight, w32, 0, t, cols, 1.0f, we);
+        load_param<DT, TPR, kVec>(a.bias, w32, 0, t, cols, 0.0f, be);
+    }
     const size_t groups = static_cast<size_t>(gridDim.x) * RPB;
     // All threads of a block make the same number of rounds.
     for (size_t r0 = static_cast<size_t>(blockIdx.x) * RPB; r0 < a.rows; r0 += groups) {
@@ -156,77 +212,82 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) forward_kernel(NormArgs
         const bool live = RPB == 1 || r < a.rows;
         Raw<DT, NV> x;
         load_row<DT, TPR, NV, kVec>(x, a.x, live ? r * a.ldx : 0, t, live ? cols : 0u);
-        float s = 0.0f, have = 0.0f;
+        float2 s2 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[VE];
+            float2 f[P];
             widen<DT>(x.v[i], f);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) s = __fadd_rn(s, f[e]);
+            for (int p = 0; p < P; ++p) s2 = __fadd2_rn(s2, f[p]);
         }
         // Elements of this warp (or group of lanes): whole warps but the last.
+        float have = n;
         if (TPR > 32) {
-            unsigned n = 0;
+            unsigned k = 0;
 #pragma unroll
             for (int i = 0; i < NV * (kVec ? 1 : VE); ++i) {
                 const unsigned from = (i * TPR + (t & ~31u)) * (kVec ? VE : 1);
                 const unsigned left = from < cols ? cols - from : 0u;
-                n += left < 32u * (kVec ? VE : 1) ? left : 32u * (kVec ? VE : 1);
+                k += left < 32u * (kVec ? VE : 1) ? left : 32u * (kVec ? VE : 1);
             }
-            have = static_cast<float>(n);
-        } else {
-            have = static_cast<float>(cols);
+            have = static_cast<float>(k);
         }
-        s = lanes_sum<TPR>(s);
-        float mean = have > 0.0f ? s / have : 0.0f;
-        float q = 0.0f;
+        float s = lanes_sum<TPR>(__fadd_rn(s2.x, s2.y));
+        // Any value near the warp's mean serves: what it is off is made up for
+        // when the warps' parts are joined.
+        float mean = TPR > 32 ? __fmul_rn(s, __fdividef(1.0f, fmaxf(have, 1.0f))) : quotient(s, n, inv_n);
+        float2 q2 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[VE];
+            float2 f[P];
             widen<DT>(x.v[i], f);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float d = __fsub_rn(f[e], mean);
-                if (in_row<DT, TPR, kVec>(i, e, t, cols)) q = __fmaf_rn(d, d, q);
+            for (int p = 0; p < P; ++p) {
+                float2 d = __fadd2_rn(f[p], pair(-mean));
+                if (!in_row<DT, TPR, kVec>(i, 2 * p, t, cols)) d.x = 0.0f;
+                if (!in_row<DT, TPR, kVec>(i, 2 * p + 1, t, cols)) d.y = 0.0f;
+                q2 = __ffma2_rn(d, d, q2);
             }
         }
-        q = lanes_sum<TPR>(q);
-        const float n = static_cast<float>(cols);
+        float q = lanes_sum<TPR>(__fadd_rn(q2.x, q2.y));
         if (TPR > 32) {
             if ((t & 31) == 0) red[t / 32] = make_float4(s, q, mean, have);
             group_sync<TPR, BT>(0);
+            // sum (x - m)^2 = q_w + 2 (m_w - m) (s_w - n_w m_w) + n_w (m_w - m)^2 for a warp.
             if (WPG <= 8) {
                 s = 0.0f;
 #pragma unroll
                 for (int w = 0; w < WPG; ++w) s = __fadd_rn(s, red[w].x);
-                mean = s / n;
+                mean = quotient(s, n, inv_n);
                 q = 0.0f;
 #pragma unroll
-                for (int w = 0; w < WPG; ++w) {
-                    const float d = __fsub_rn(red[w].z, mean);
-                    q = __fadd_rn(q, __fmaf_rn(__fmul_rn(red[w].w, d), d, red[w].y));
-                }
+                for (int w = 0; w < WPG; ++w) q = __fadd_rn(q, around(red[w], mean));
             } else {
                 const float4 p = red[(t & 31) % WPG];
                 s = p.x;
 #pragma unroll
                 for (int d = WPG / 2; d > 0; d >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
-                mean = s / n;
-                const float d0 = __fsub_rn(p.z, mean);
-                q = __fmaf_rn(__fmul_rn(p.w, d0), d0, p.y);
+                mean = quotient(s, n, inv_n);
+                q = around(p, mean);
 #pragma unroll
                 for (int d = WPG / 2; d > 0; d >>= 1) q = __fadd_rn(q, __shfl_xor_sync(0xFFFFFFFFu, q, d));
             }
         }
-        const float rstd = 1.0f / sqrtf(q / n + a.eps);
+        const float rstd = rsqrtf(__fmaf_rn(q, inv_n, a.eps));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[VE], w[VE], b[VE];
-            load_param<DT, TPR, kVec>(a.weight, w32, i, t, cols, 1.0f, w);
-            load_param<DT, TPR, kVec>(a.bias, w32, i, t, cols, 0.0f, b);
+            float2 f[P], w[P], b[P];
+            if (kEarly) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) w[p] = we[p % (kEarly ? P : 1)], b[p] = be[p % (kEarly ? P : 1)];
+            } else {
+                load_param<DT, TPR, kVec>(a.weight, w32, i, t, cols, 1.0f, w);
+                load_param<DT, TPR, kVec>(a.bias, w32, i, t, cols, 0.0f, b);
+            }
             widen<DT>(x.v[i], f);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) f[e] = __fmaf_rn(__fmul_rn(__fsub_rn(f[e], mean), rstd), w[e], b[e]);
+            for (int p = 0; p < P; ++p)
+                f[p] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[p], pair(-mean)), pair(rstd)), w[p], b[p]);
             store_vec<DT, TPR, kVec>(a.y, live ? r * a.ldy : 0, i, t, live ? cols : 0u, f);
         }
         if (live && t == 0) {
@@ -243,28 +304,28 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) forward_kernel(NormArgs
 // flight.  At the end the groups of a block are added in order in shared
 // memory, and each block writes one row of sums, which params_kernel adds.
 // ---------------------------------------------------------------------------
-constexpr int kSMs = 152;
+constexpr int kSMs = 152, kMaxDevices = 64;
 
 template <int TPR> struct BackwardShape {
     static constexpr int kThreads = TPR > 512 ? TPR : 512;
     static constexpr int kGroups = kThreads / TPR;
 };
 
-template <int DT, int TPR, int NV, bool kVec>
-__global__ void __launch_bounds__(BackwardShape<TPR>::kThreads, NV == 1 && TPR <= 512 ? 2 : 1)
-backward_kernel(NormGradArgs a, bool w32) {
-    constexpr int VE = Elem<DT>::kVE, BT = BackwardShape<TPR>::kThreads, G = BT / TPR, WPG = TPR > 32 ? TPR / 32 : 1;
+template <int DT, int TPR, bool kVec>
+__global__ void __launch_bounds__(BackwardShape<TPR>::kThreads, TPR <= 512 ? 2 : 1)
+backward_kernel(NormGradArgs a, bool w32, float inv_n) {
+    constexpr int VE = Elem<DT>::kVE, P = VE / 2, BT = BackwardShape<TPR>::kThreads, G = BT / TPR;
+    constexpr int WPG = TPR > 32 ? TPR / 32 : 1;
     __shared__ float2 red[2][G][WPG];
-    extern __shared__ float sums[];                   // [G][2][NV * TPR * VE], groups of at least a warp
+    extern __shared__ float sums[];                   // [G][2][TPR * VE], groups of at least a warp
     pdl_wait();
     const unsigned t = threadIdx.x % TPR, cols = static_cast<unsigned>(a.cols);
     const int g = threadIdx.x / TPR;
     const size_t step = static_cast<size_t>(gridDim.x) * G;
-    const float n = static_cast<float>(cols);
-    float dw[NV * VE], db[NV * VE];
+    float2 dw[P], db[P];
 #pragma unroll
-    for (int e = 0; e < NV * VE; ++e) dw[e] = db[e] = 0.0f;
-    Raw<DT, NV> x, dy;
+    for (int p = 0; p < P; ++p) dw[p] = db[p] = pair(0.0f);
+    Raw<DT, 1> x, dy;
     float mean = 0.0f, rstd = 0.0f;
     // Groups smaller than a warp keep its lanes together: the warp makes the
     // rounds of its first group, lanes without a row on zeros.
@@ -272,99 +333,79 @@ backward_kernel(NormGradArgs a, bool w32) {
     size_t r = first + g, lead = first + (TPR < 32 ? (threadIdx.x & ~31u) / TPR : g);
     auto fetch = [&] {
         const bool live = r < a.rows;
-        load_row<DT, TPR, NV, kVec>(x, a.x, live ? r * a.ldx : 0, t, live ? cols : 0u);
-        load_row<DT, TPR, NV, kVec>(dy, a.dy, live ? r * a.lddy : 0, t, live ? cols : 0u);
+        load_row<DT, TPR, 1, kVec>(x, a.x, live ? r * a.ldx : 0, t, live ? cols : 0u);
+        load_row<DT, TPR, 1, kVec>(dy, a.dy, live ? r * a.lddy : 0, t, live ? cols : 0u);
         mean = live ? a.mean[r] : 0.0f;
         rstd = live ? a.rstd[r] : 0.0f;
     };
     fetch();
     for (int buf = 0; lead < a.rows; lead += step, buf ^= 1) {
         const size_t row = r;
-        const Raw<DT, NV> cx = x, cdy = dy;
-        const float m = mean, rs = rstd;
-        r += step;
-        if (NV == 1) fetch();
-        float s = 0.0f, q = 0.0f;
+        const float rs = rstd;
+        float2 h[P], gr[P], s2 = pair(0.0f), q2 = pair(0.0f);
+        {
+            float2 d[P], w[P];
+            widen<DT>(x.v[0], h);
+            widen<DT>(dy.v[0], d);
+            const float m = -mean;
+            r += step;
+            fetch();
+            load_param<DT, TPR, kVec>(a.weight, w32, 0, t, cols, 1.0f, w);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float fx[VE], fd[VE], w[VE];
-            widen<DT>(cx.v[i], fx);
-            widen<DT>(cdy.v[i], fd);
-            load_param<DT, TPR, kVec>(a.weight, w32, i, t, cols, 1.0f, w);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float h = __fmul_rn(__fsub_rn(fx[e], m), rs), gr = __fmul_rn(fd[e], w[e]);
-                s = __fadd_rn(s, gr);
-                q = __fmaf_rn(gr, h, q);
-                dw[i * VE + e] = __fmaf_rn(fd[e], h, dw[i * VE + e]);
-                db[i * VE + e] = __fadd_rn(db[i * VE + e], fd[e]);
+            for (int p = 0; p < P; ++p) {
+                h[p] = __fmul2_rn(__fadd2_rn(h[p], pair(m)), pair(rs));
+                gr[p] = __fmul2_rn(d[p], w[p]);
+                s2 = __fadd2_rn(s2, gr[p]);
+                q2 = __ffma2_rn(gr[p], h[p], q2);
+                dw[p] = __ffma2_rn(d[p], h[p], dw[p]);
+                db[p] = __fadd2_rn(db[p], d[p]);
             }
         }
-        s = lanes_sum<TPR>(s);
-        q = lanes_sum<TPR>(q);
+        float2 sum = make_float2(__fadd_rn(s2.x, s2.y), __fadd_rn(q2.x, q2.y));
+        sum = lanes_sum2<(TPR < 32 ? TPR : 32)>(sum);
         if (TPR > 32) {
-            if ((t & 31) == 0) red[buf][g][t / 32] = make_float2(s, q);
+            if ((t & 31) == 0) red[buf][g][t / 32] = sum;
             group_sync<TPR, BT>(g);
-            const float2 p = red[buf][g][(t & 31) % WPG];
-            s = p.x, q = p.y;
-#pragma unroll
-            for (int d = WPG / 2; d > 0; d >>= 1) {
-                s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
-                q = __fadd_rn(q, __shfl_xor_sync(0xFFFFFFFFu, q, d));
-            }
+            sum = lanes_sum2<WPG>(red[buf][g][(t & 31) % WPG]);
         }
-        const float mg = s / n, mgh = q / n;
+        // dx = rstd g - rstd mean(g) - h rstd mean(g h)
+        const float c0 = -__fmul_rn(rs, __fmul_rn(sum.x, inv_n)), c1 = -__fmul_rn(rs, __fmul_rn(sum.y, inv_n));
         const bool live = row < a.rows;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float fx[VE], fd[VE], w[VE];
-            widen<DT>(cx.v[i], fx);
-            widen<DT>(cdy.v[i], fd);
-            load_param<DT, TPR, kVec>(a.weight, w32, i, t, cols, 1.0f, w);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float h = __fmul_rn(__fsub_rn(fx[e], m), rs), gr = __fmul_rn(fd[e], w[e]);
-                fx[e] = __fmul_rn(rs, __fmaf_rn(-h, mgh, __fsub_rn(gr, mg)));
-            }
-            store_vec<DT, TPR, kVec>(a.dx, live ? row * a.lddx : 0, i, t, live ? cols : 0u, fx);
-        }
-        if (NV != 1) fetch();
+        for (int p = 0; p < P; ++p) gr[p] = __ffma2_rn(gr[p], pair(rs), __ffma2_rn(h[p], pair(c1), pair(c0)));
+        store_vec<DT, TPR, kVec>(a.dx, live ? row * a.lddx : 0, 0, t, live ? cols : 0u, gr);
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return;
     float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * cols;
     if (G == 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const unsigned c = kVec ? (i * TPR + t) * VE + e : (i * VE + e) * TPR + t;
-                if (c < cols) {
-                    out[c] = dw[i * VE + e];
-                    out[cols + c] = db[i * VE + e];
-                }
+        for (int e = 0; e < VE; ++e) {
+            const unsigned c = kVec ? t * VE + e : e * TPR + t;
+            if (c < cols) {
+                out[c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
+                out[cols + c] = e % 2 ? db[e / 2].y : db[e / 2].x;
             }
+        }
         return;
     }
-    constexpr int C = NV * TPR * VE, S = TPR < 32 ? BT / 32 : G;
+    constexpr int C = TPR * VE, S = TPR < 32 ? BT / 32 : G;
     if (TPR < 32) {
 #pragma unroll
-        for (int e = 0; e < NV * VE; ++e)
+        for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int d = TPR; d < 32; d <<= 1) {
-                dw[e] = __fadd_rn(dw[e], __shfl_xor_sync(0xFFFFFFFFu, dw[e], d));
-                db[e] = __fadd_rn(db[e], __shfl_xor_sync(0xFFFFFFFFu, db[e], d));
+                dw[p] = __fadd2_rn(dw[p], shfl_xor2(dw[p], d));
+                db[p] = __fadd2_rn(db[p], shfl_xor2(db[p], d));
             }
     }
     const int slot = TPR < 32 ? threadIdx.x / 32 : g;
     if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const unsigned c = kVec ? (i * TPR + t) * VE + e : (i * VE + e) * TPR + t;
-                sums[(slot * 2) * C + c] = dw[i * VE + e];
-                sums[(slot * 2 + 1) * C + c] = db[i * VE + e];
-            }
+        for (int e = 0; e < VE; ++e) {
+            const unsigned c = kVec ? t * VE + e : e * TPR + t;
+            sums[(slot * 2) * C + c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
+            sums[(slot * 2 + 1) * C + c] = e % 2 ? db[e / 2].y : db[e / 2].x;
+        }
     }
     __syncthreads();
     for (unsigned c = threadIdx.x; c < 2 * cols; c += BT) {
@@ -375,8 +416,7 @@ backward_kernel(NormGradArgs a, bool w32) {
     }
 }
 
-// Threads per row of the backward kernel for a row of `vecs` vectors, and its
-// vectors per thread (0: the row does not fit the registers).
+// Threads per row of the backward kernel for a row of `vecs` vectors.
 inline int backward_tpr(size_t vecs) {
     int tpr = 8;
     while (tpr < 1024 && static_cast<size_t>(tpr) < vecs) tpr *= 2;
@@ -385,27 +425,43 @@ inline int backward_tpr(size_t vecs) {
 
 template <int DT> cudaError_t forward(const NormArgs& a, bool w32, bool vec, cudaStream_t s);
 template <int DT> cudaError_t backward(const NormGradArgs& a, bool w32, bool vec, unsigned blocks, cudaStream_t s);
+// The kernels for many rows (layer_norm_ring.cuh); `vec`: 16-byte accesses, else
+// 4-byte ones.
+constexpr size_t kRingVecs = 2048;
+template <int DT> cudaError_t ring_forward(const NormArgs& a, bool w32, bool vec, size_t vecs, cudaStream_t s);
+template <int DT> cudaError_t ring_backward(const NormGradArgs& a, bool w32, bool vec, size_t vecs, cudaStream_t s);
 
-template <int DT, int TPR, int NV>
+template <int DT, int TPR, int NV, bool kEarly = false>
 cudaError_t forward_launch(const NormArgs& a, bool w32, bool vec, cudaStream_t s) {
-    constexpr int BT = TPR < 128 ? 128 : TPR, RPB = BT / TPR;
+    constexpr int BT = ForwardShape<TPR, NV>::kThreads, RPB = BT / TPR;
     const size_t blocks = (a.rows + RPB - 1) / RPB;
     const dim3 grid(static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
-    return vec ? launch_kernel(forward_kernel<DT, TPR, NV, true>, grid, dim3(BT), s, a, w32)
-               : launch_kernel(forward_kernel<DT, TPR, NV, false>, grid, dim3(BT), s, a, w32);
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    return vec ? launch_kernel(forward_kernel<DT, TPR, NV, true, kEarly>, grid, dim3(BT), s, a, w32, inv_n)
+               : launch_kernel(forward_kernel<DT, TPR, NV, false, kEarly>, grid, dim3(BT), s, a, w32, inv_n);
 }
 
-template <int DT, int TPR, int NV>
+template <int DT, int TPR>
 cudaError_t backward_launch(const NormGradArgs& a, bool w32, bool vec, unsigned blocks, cudaStream_t s) {
     constexpr int BT = BackwardShape<TPR>::kThreads, G = BT / TPR, S = TPR < 32 ? BT / 32 : G;
-    const size_t smem = G == 1 ? 0 : static_cast<size_t>(S) * 2 * NV * TPR * Elem<DT>::kVE * sizeof(float);
-    return vec ? launch_kernel_smem(backward_kernel<DT, TPR, NV, true>, dim3(blocks), dim3(BT), smem, s, a, w32)
-               : launch_kernel_smem(backward_kernel<DT, TPR, NV, false>, dim3(blocks), dim3(BT), smem, s, a, w32);
+    const size_t smem = G == 1 ? 0 : static_cast<size_t>(S) * 2 * TPR * Elem<DT>::kVE * sizeof(float);
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    return vec ? launch_kernel_smem(backward_kernel<DT, TPR, true>, dim3(blocks), dim3(BT), smem, s, a, w32, inv_n)
+               : launch_kernel_smem(backward_kernel<DT, TPR, false>, dim3(blocks), dim3(BT), smem, s, a, w32, inv_n);
 }
+
+// Rows up to which a call is a matter of latency: one vector a thread.
+constexpr size_t kFewRows = 2 * kSMs;
 
 // Definitions for one element type (layer_norm_<type>.cu).
 template <int DT> cudaError_t forward_any(const NormArgs& a, bool w32, bool vec, cudaStream_t s) {
     const size_t vecs = (a.cols + Elem<DT>::kVE - 1) / Elem<DT>::kVE;
+    if (a.rows <= kFewRows && vecs > 32 && vecs <= 1024) {
+        if (vecs <= 128) return forward_launch<DT, 128, 1, true>(a, w32, vec, s);
+        if (vecs <= 256) return forward_launch<DT, 256, 1, true>(a, w32, vec, s);
+        if (vecs <= 512) return forward_launch<DT, 512, 1, true>(a, w32, vec, s);
+        return forward_launch<DT, 1024, 1, true>(a, w32, vec, s);
+    }
     if (vecs <= 8) return forward_launch<DT, 8, 1>(a, w32, vec, s);
     if (vecs <= 32) return forward_launch<DT, 32, 1>(a, w32, vec, s);
     if (vecs <= 64) return forward_launch<DT, 32, 2>(a, w32, vec, s);
@@ -421,14 +477,14 @@ template <int DT> cudaError_t forward_any(const NormArgs& a, bool w32, bool vec,
 
 template <int DT> cudaError_t backward_any(const NormGradArgs& a, bool w32, bool vec, unsigned blocks, cudaStream_t s) {
     switch (backward_tpr((a.cols + Elem<DT>::kVE - 1) / Elem<DT>::kVE)) {
-    case 8: return backward_launch<DT, 8, 1>(a, w32, vec, blocks, s);
-    case 16: return backward_launch<DT, 16, 1>(a, w32, vec, blocks, s);
-    case 32: return backward_launch<DT, 32, 1>(a, w32, vec, blocks, s);
-    case 64: return backward_launch<DT, 64, 1>(a, w32, vec, blocks, s);
-    case 128: return backward_launch<DT, 128, 1>(a, w32, vec, blocks, s);
-    case 256: return backward_launch<DT, 256, 1>(a, w32, vec, blocks, s);
-    case 512: return backward_launch<DT, 512, 1>(a, w32, vec, blocks, s);
-    default: return backward_launch<DT, 1024, 1>(a, w32, vec, blocks, s);
+    case 8: return backward_launch<DT, 8>(a, w32, vec, blocks, s);
+    case 16: return backward_launch<DT, 16>(a, w32, vec, blocks, s);
+    case 32: return backward_launch<DT, 32>(a, w32, vec, blocks, s);
+    case 64: return backward_launch<DT, 64>(a, w32, vec, blocks, s);
+    case 128: return backward_launch<DT, 128>(a, w32, vec, blocks, s);
+    case 256: return backward_launch<DT, 256>(a, w32, vec, blocks, s);
+    case 512: return backward_launch<DT, 512>(a, w32, vec, blocks, s);
+    default: return backward_launch<DT, 1024>(a, w32, vec, blocks, s);
     }
 }
 

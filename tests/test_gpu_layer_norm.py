@@ -109,6 +109,46 @@ def test_backward(sar, shape, types):
     check_backward(sar, dy, x, w, wt)
 
 
+# Rows enough to stay in the blocks for long, at every split of a row over threads, whole and partly filled.
+MANY = [(305, 4096), (611, 4090), (330, 8192), (333, 5004), (320, 16384), (306, 12290), (613, 2048), (1217, 1024), (1300, 520),
+        (2434, 512), (2500, 300), (4870, 256), (5001, 132), (9730, 140), (20011, 64)]
+
+
+@pytest.mark.parametrize("types", TYPES, ids="/".join)
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_many_rows(sar, shape, types):
+    dt, wt = (ref.DTYPES[t] for t in types)
+    x, dy, w, b = inputs(*shape, dt, wt, seed=shape[0])
+    check_forward(sar, x, w, b)
+    check_backward(sar, dy, x, w, wt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("gap,offset", [(8, 8), (2, 4), (1, 0), (0, 1)])
+@pytest.mark.parametrize("shape", [(610, 1000), (620, 2048), (2440, 400)], ids=str)
+def test_many_rows_strides_and_alignment(sar, shape, gap, offset, dtype):
+    dt = ref.DTYPES[dtype]
+    x, dy, w, b = inputs(*shape, dt, dt, seed=1)
+    check_forward(sar, x, w, b, gap=gap, offset=offset)
+    check_backward(sar, dy, x, w, dt, gap=gap, offset=offset)
+
+
+@pytest.mark.parametrize("shape", [(700, 4096), (1300, 1021)], ids=str)
+def test_many_rows_without_parameters_in_place(sar, shape):
+    """No weight or bias, statistics not wanted, y over x and dx over dy; a NaN row stays alone."""
+    x, dy, _, _ = inputs(*shape, torch.float32, torch.float32, seed=2)
+    x[5, 7] = float("nan")
+    (wy, mean, rstd), (by, _, _) = ref.layer_norm(x, None, None, 1e-5)
+    y = x.clone()
+    sar.sar_layer_norm(y, y)
+    assert bool(torch.isnan(y[5]).all())
+    ref.check(y, torch.where(torch.isnan(wy), float("nan"), wy), ref.rounded(by, wy, x.dtype), "y")
+    mean, rstd = mean.float(), rstd.float()
+    (wx, _, _), (bx, _, _) = ref.layer_norm_backward(dy, x, None, mean, rstd)
+    sar.sar_layer_norm_backward(dy, x, None, mean, rstd, dy)
+    ref.check(dy, wx, ref.rounded(bx, wx, x.dtype), "dx")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("gap,offset", [(0, 1), (8, 0), (5, 0), (16, 8), (3, 2), (1, 16)])
 @pytest.mark.parametrize("shape", [(6, 100), (5, 1024), (3, 4096), (3, 9000)], ids=str)
@@ -262,7 +302,7 @@ def test_gradient_against_differences(sar, cols):
         assert allowed < 0.05 * (abs(truth) + (exact.abs() * d.abs()).sum().item() ** 0.5)     # the check says something
 
 
-@pytest.mark.parametrize("shape", [(8, 4096), (515, 1024), (300, 1021), (70, 12000)], ids=str)
+@pytest.mark.parametrize("shape", [(8, 4096), (515, 1024), (300, 1021), (70, 12000), (1500, 2048)], ids=str)
 def test_same_bits_on_every_run_and_stream(sar, shape):
     x, dy, w, b = inputs(*shape, torch.bfloat16, torch.float32, seed=9)
     y, mean, rstd = forward(sar, x, w, b)

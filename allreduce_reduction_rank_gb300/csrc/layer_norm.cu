@@ -9,6 +9,9 @@
 // ones run those here: one block per row, the row read again for each pass
 // (from L2), and the parameters' gradients in a kernel of their own, a thread
 // per column over a share of the rows.
+#include <algorithm>
+#include <initializer_list>
+
 #include "layer_norm_ring.cuh"
 
 namespace sar {
@@ -111,47 +114,63 @@ __global__ void __launch_bounds__(kThreads) norm_shares_kernel(NormGradArgs a) {
     }
 }
 
-// dweight and dbias from the shares' sums: 32 columns a block, the shares over
-// its warps, which are then added in order.
+// dweight and dbias from the shares' sums: a warp reads 32 * N columns of a share
+// (N = 4, as float4, where the columns allow it), a block's warps have every
+// kParamWarps-th share, ten loads in flight, and are then added in order.
 constexpr int kParamWarps = 16;
-template <int WDT>
+template <int WDT, int N>
 __global__ void __launch_bounds__(kParamWarps * 32) params_kernel(NormGradArgs a, unsigned shares) {
-    __shared__ float part[kParamWarps][32];
+    __shared__ float part[kParamWarps][32 * N];
     pdl_wait();
     const unsigned lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool bias = blockIdx.y != 0;
     void* out = bias ? a.dbias : a.dweight;
     if (out == nullptr) return;
-    for (size_t c0 = static_cast<size_t>(blockIdx.x) * 32; c0 < a.cols; c0 += static_cast<size_t>(gridDim.x) * 32) {
-        const size_t c = c0 + lane;
-        float v = 0.0f;
+    for (size_t c0 = static_cast<size_t>(blockIdx.x) * 32 * N; c0 < a.cols; c0 += static_cast<size_t>(gridDim.x) * 32 * N) {
+        const size_t c = c0 + lane * N;
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = 0.0f;
         if (c < a.cols) {
-            // Ten shares' loads in flight at a time.
             for (unsigned k0 = warp; k0 < shares; k0 += 10 * kParamWarps) {
-                float p[10];
+                float p[10][N];
 #pragma unroll
                 for (int i = 0; i < 10; ++i) {
                     const unsigned k = k0 + i * kParamWarps;
-                    p[i] = k < shares ? a.partial[(static_cast<size_t>(k) * 2 + bias) * a.cols + c] : 0.0f;
+                    const float* from = a.partial + (static_cast<size_t>(k) * 2 + bias) * a.cols + c;
+                    if constexpr (N == 4) {
+                        const float4 f = k < shares ? *reinterpret_cast<const float4*>(from) : make_float4(0, 0, 0, 0);
+                        p[i][0] = f.x, p[i][1] = f.y, p[i][2] = f.z, p[i][3] = f.w;
+                    } else {
+                        p[i][0] = k < shares ? *from : 0.0f;
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 10; ++i) v = __fadd_rn(v, p[i]);
+                for (int i = 0; i < 10; ++i)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[e] = __fadd_rn(v[e], p[i][e]);
             }
         }
-        part[warp][lane] = v;
+#pragma unroll
+        for (int e = 0; e < N; ++e) part[warp][lane * N + e] = v[e];
         __syncthreads();
-        if (warp == 0 && c < a.cols) {
-            for (int w = 1; w < kParamWarps; ++w) v = __fadd_rn(v, part[w][lane]);
-            store_elem<WDT>(out, c, v);
+        if (threadIdx.x < 32 * N && c0 + threadIdx.x < a.cols) {
+            float sum = part[0][threadIdx.x];
+            for (int w = 1; w < kParamWarps; ++w) sum = __fadd_rn(sum, part[w][threadIdx.x]);
+            store_elem<WDT>(out, c0 + threadIdx.x, sum);
         }
         __syncthreads();
     }
 }
 
-template <int WDT> cudaError_t params(const NormGradArgs& a, unsigned shares, cudaStream_t s) {
-    const size_t blocks = (a.cols + 31) / 32;
-    return launch_kernel(params_kernel<WDT>, dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), 2),
+template <int WDT, int N> cudaError_t params_launch(const NormGradArgs& a, unsigned shares, cudaStream_t s) {
+    const size_t blocks = (a.cols + 32 * N - 1) / (32 * N);
+    return launch_kernel(params_kernel<WDT, N>, dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), 2),
                          dim3(kParamWarps * 32), s, a, shares);
+}
+
+template <int WDT> cudaError_t params(const NormGradArgs& a, unsigned shares, cudaStream_t s) {
+    return a.cols % 4 == 0 && a.cols >= 4096 ? params_launch<WDT, 4>(a, shares, s) : params_launch<WDT, 1>(a, shares, s);
 }
 
 cudaError_t params_of(sar_dtype wdt, const NormGradArgs& a, unsigned shares, cudaStream_t s) {
@@ -185,26 +204,38 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Rows of `cols` elements of `es` bytes move as whole 16-byte vectors.
 bool rows_on16(const void* p, size_t ld, size_t rows, size_t es) { return on16(p) && (rows <= 1 || ld * es % 16 == 0); }
 
-// The same with words of 4 bytes.
-bool rows_on4(const void* p, size_t ld, size_t rows, size_t es) {
-    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && (rows <= 1 || ld * es % 4 == 0);
-}
+// A matrix of a call to the kernels for many rows.
+struct Matrix {
+    const void* p;
+    size_t ld;
+};
 
-// Rows that give every group of the ring kernels' blocks two or more.
-bool many_rows(size_t rows, size_t vecs) {
-    size_t tpr = 32;
-    while (tpr < norm::kRingThreads && tpr < vecs) tpr *= 2;
-    return rows >= 2 * norm::kSMs * (norm::kRingThreads / tpr);
+// Whether those kernels take the call: rows that they hold and that give every
+// group of their blocks two or more, and matrices whose rows start alike.
+bool ring_takes(std::initializer_list<Matrix> all, size_t rows, size_t cols, size_t es, size_t* vecs, norm::Alignment* al) {
+    const size_t ve = 16 / es;
+    const Matrix& m = *all.begin();
+    const size_t start = reinterpret_cast<uintptr_t>(m.p) / es % ve, step = m.ld % ve;
+    for (const Matrix& o : all)
+        if (reinterpret_cast<uintptr_t>(o.p) / es % ve != start || o.ld % ve != step) return false;
+    size_t most = 0, period = 1;                      // largest shift, rows until it repeats
+    if (start != 0 || step != 0) {
+        while (period * step % ve != 0) period *= 2;
+        for (size_t r = 0; r < period; ++r) most = std::max(most, (start + r * step) % ve);
+    }
+    const bool whole = start == 0 && step == 0 && cols % ve == 0;
+    *vecs = (cols + most + ve - 1) / ve;
+    *al = {static_cast<unsigned>(start), static_cast<unsigned>(step), static_cast<unsigned>(whole ? 0 : period)};
+    return *vecs > 16 && *vecs <= norm::kRingVecs && rows <= 0x7FFFFFFF && 
+           rows >= 2 * norm::kSMs * norm::ring_split(*vecs, norm::ring_vectors(*vecs)).groups;
 }
 
 template <int DT> cudaError_t forward_of(sar_dtype wdt, const NormArgs& a, cudaStream_t s) {
     constexpr size_t es = Elem<DT>::kSize, VE = Elem<DT>::kVE;
-    const size_t vecs = (a.cols * es + 15) / 16;
-    if (vecs > 16 && vecs <= norm::kRingVecs && many_rows(a.rows, vecs) && a.cols * es % 4 == 0 &&
-        rows_on4(a.x, a.ldx, a.rows, es) && rows_on4(a.y, a.ldy, a.rows, es)) {
-        const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.y, a.ldy, a.rows, es);
-        return norm::ring_forward<DT>(a, wdt == SAR_FP32, vec, vecs, s);
-    }
+    size_t vecs;
+    norm::Alignment al;
+    if (ring_takes({{a.x, a.ldx}, {a.y, a.ldy}}, a.rows, a.cols, es, &vecs, &al))
+        return norm::ring_forward<DT>(a, wdt == SAR_FP32, vecs, al, s);
     if ((a.cols + VE - 1) / VE > kForwardVecs)
         return wdt == SAR_FP32 ? long_forward<DT, SAR_FP32>(a, s) : long_forward<DT, DT>(a, s);
     const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.y, a.ldy, a.rows, es) &&
@@ -225,13 +256,11 @@ template <int DT> cudaError_t backward_of(sar_dtype wdt, const NormGradArgs& a, 
     constexpr size_t es = Elem<DT>::kSize, VE = Elem<DT>::kVE;
     unsigned shares = 0;
     cudaError_t e = cudaSuccess;
-    const size_t vecs = (a.cols * es + 15) / 16;
-    if (vecs > 16 && vecs <= norm::kRingVecs && many_rows(a.rows, vecs) && a.cols * es % 4 == 0 &&
-        rows_on4(a.x, a.ldx, a.rows, es) && rows_on4(a.dy, a.lddy, a.rows, es) && rows_on4(a.dx, a.lddx, a.rows, es)) {
-        const bool vec = a.cols % VE == 0 && rows_on16(a.x, a.ldx, a.rows, es) && rows_on16(a.dy, a.lddy, a.rows, es) &&
-                         rows_on16(a.dx, a.lddx, a.rows, es);
+    size_t vecs;
+    norm::Alignment al;
+    if (ring_takes({{a.x, a.ldx}, {a.dy, a.lddy}, {a.dx, a.lddx}}, a.rows, a.cols, es, &vecs, &al)) {
         shares = norm::kSMs;
-        e = norm::ring_backward<DT>(a, wdt == SAR_FP32, vec, vecs, s);
+        e = norm::ring_backward<DT>(a, wdt == SAR_FP32, vecs, al, s);
     } else if (a.rows != 0 && (a.cols + VE - 1) / VE > kBackwardVecs) {
         shares = static_cast<unsigned>(a.rows < kShares ? a.rows : kShares);
         e = wdt == SAR_FP32 ? long_backward<DT, SAR_FP32>(a, shares, s) : long_backward<DT, DT>(a, shares, s);

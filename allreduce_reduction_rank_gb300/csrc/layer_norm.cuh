@@ -317,7 +317,7 @@ backward_kernel(NormGradArgs a, bool w32, float inv_n) {
     constexpr int VE = Elem<DT>::kVE, P = VE / 2, BT = BackwardShape<TPR>::kThreads, G = BT / TPR;
     constexpr int WPG = TPR > 32 ? TPR / 32 : 1;
     __shared__ float2 red[2][G][WPG];
-    extern __shared__ float sums[];                   // [G][2][TPR * VE], groups of at least a warp
+    extern __shared__ float sums[];                   // [G][TPR * VE], groups of at least a warp
     pdl_wait();
     const unsigned t = threadIdx.x % TPR, cols = static_cast<unsigned>(a.cols);
     const int g = threadIdx.x / TPR;
@@ -377,17 +377,6 @@ backward_kernel(NormGradArgs a, bool w32, float inv_n) {
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return;
     float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * cols;
-    if (G == 1) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const unsigned c = kVec ? t * VE + e : e * TPR + t;
-            if (c < cols) {
-                out[c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
-                out[cols + c] = e % 2 ? db[e / 2].y : db[e / 2].x;
-            }
-        }
-        return;
-    }
     constexpr int C = TPR * VE, S = TPR < 32 ? BT / 32 : G;
     if (TPR < 32) {
 #pragma unroll
@@ -398,21 +387,26 @@ backward_kernel(NormGradArgs a, bool w32, float inv_n) {
                 db[p] = __fadd2_rn(db[p], shfl_xor2(db[p], d));
             }
     }
+    // The groups' sums, added in order; through shared memory, so that they
+    // leave in whole sectors.
     const int slot = TPR < 32 ? threadIdx.x / 32 : g;
-    if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const unsigned c = kVec ? t * VE + e : e * TPR + t;
-            sums[(slot * 2) * C + c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
-            sums[(slot * 2 + 1) * C + c] = e % 2 ? db[e / 2].y : db[e / 2].x;
+    for (int half = 0; half < 2; ++half) {
+        if (half == 1) __syncthreads();
+        if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const unsigned c = kVec ? t * VE + e : e * TPR + t;
+                const float2 v = half == 0 ? dw[e / 2] : db[e / 2];
+                sums[slot * C + c] = e % 2 ? v.y : v.x;
+            }
         }
-    }
-    __syncthreads();
-    for (unsigned c = threadIdx.x; c < 2 * cols; c += BT) {
-        const unsigned half = c >= cols, k = half * C + (c - half * cols);
-        float v = sums[k];
-        for (int p = 1; p < S; ++p) v = __fadd_rn(v, sums[p * 2 * C + k]);
-        out[c] = v;
+        __syncthreads();
+        for (unsigned c = threadIdx.x; c < cols; c += BT) {
+            float v = sums[c];
+            for (int p = 1; p < S; ++p) v = __fadd_rn(v, sums[p * C + c]);
+            out[half * cols + c] = v;
+        }
     }
 }
 
@@ -425,11 +419,26 @@ inline int backward_tpr(size_t vecs) {
 
 template <int DT> cudaError_t forward(const NormArgs& a, bool w32, bool vec, cudaStream_t s);
 template <int DT> cudaError_t backward(const NormGradArgs& a, bool w32, bool vec, unsigned blocks, cudaStream_t s);
-// The kernels for many rows (layer_norm_ring.cuh); `vec`: 16-byte accesses, else
-// 4-byte ones.
+// The kernels for many rows (layer_norm_ring.cuh).
 constexpr size_t kRingVecs = 2048;
-template <int DT> cudaError_t ring_forward(const NormArgs& a, bool w32, bool vec, size_t vecs, cudaStream_t s);
-template <int DT> cudaError_t ring_backward(const NormGradArgs& a, bool w32, bool vec, size_t vecs, cudaStream_t s);
+// Vectors per thread, and a block's groups and their warps.
+inline int ring_vectors(size_t vecs) { return vecs <= 512 ? 1 : (vecs <= 1024 ? 2 : 4); }
+struct RingSplit {
+    int groups, warps;
+};
+inline RingSplit ring_split(size_t vecs, int nv) {
+    const int warps = static_cast<int>((vecs + 32 * nv - 1) / (32 * nv)), all = nv == 1 ? 32 : 16;
+    const int groups = all / warps;
+    return {warps > 1 && groups > 15 ? 15 : groups, warps};        // 15 barriers beside the block's own
+}
+// Where the rows start: row r is (start + r * step) % (16 / element size)
+// elements past a 16-byte boundary, with this period; period 0: every row starts
+// on a boundary and is whole vectors long.
+struct Alignment {
+    unsigned start, step, period;
+};
+template <int DT> cudaError_t ring_forward(const NormArgs& a, bool w32, size_t vecs, const Alignment& al, cudaStream_t s);
+template <int DT> cudaError_t ring_backward(const NormGradArgs& a, bool w32, size_t vecs, const Alignment& al, cudaStream_t s);
 
 template <int DT, int TPR, int NV, bool kEarly = false>
 cudaError_t forward_launch(const NormArgs& a, bool w32, bool vec, cudaStream_t s) {
@@ -444,7 +453,7 @@ cudaError_t forward_launch(const NormArgs& a, bool w32, bool vec, cudaStream_t s
 template <int DT, int TPR>
 cudaError_t backward_launch(const NormGradArgs& a, bool w32, bool vec, unsigned blocks, cudaStream_t s) {
     constexpr int BT = BackwardShape<TPR>::kThreads, G = BT / TPR, S = TPR < 32 ? BT / 32 : G;
-    const size_t smem = G == 1 ? 0 : static_cast<size_t>(S) * 2 * TPR * Elem<DT>::kVE * sizeof(float);
+    const size_t smem = static_cast<size_t>(S) * TPR * Elem<DT>::kVE * sizeof(float);
     const float inv_n = 1.0f / static_cast<float>(a.cols);
     return vec ? launch_kernel_smem(backward_kernel<DT, TPR, true>, dim3(blocks), dim3(BT), smem, s, a, w32, inv_n)
                : launch_kernel_smem(backward_kernel<DT, TPR, false>, dim3(blocks), dim3(BT), smem, s, a, w32, inv_n);

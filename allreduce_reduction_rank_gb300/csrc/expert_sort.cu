@@ -1,109 +1,154 @@
 // expert_sort.cu -- the tokens' choices sorted by expert.
 //
-// A stable counting sort by one thread-block cluster.  Warp w of the cluster
-// has the w-th run of consecutive slots.
-//   1. It walks its run, 32 slots at a time: lanes with the same expert find
-//      each other (match_any), so a slot's rank within the run is the run's
-//      count so far plus the peers in lower lanes.  The rank is left in
-//      position[]; the warp's counts per expert are in shared memory.
-//   2. Per expert, the counts are summed up over the warps of a block, and
-//      over the blocks through distributed shared memory; the segments'
-//      starts are the running sum of the padded counts over the experts.
-//   3. Each warp walks its run again: place = start + slots of the expert in
-//      earlier runs + rank.
-// Each place is written by exactly one thread and no atomics are used, so the
-// order is that of the slots.
-#include <atomic>
-
+// A stable counting sort.  A warp has a run of consecutive slots, 32 at a time:
+// the lanes with its expert come from one ballot for each bit of the expert's
+// number (four instructions a bit; match_any measured 100 cycles of an SM a
+// warp), so a slot's rank within the run is the run's count so far plus its
+// peers in lower lanes.  The places follow from the experts' counts in earlier
+// runs of the block (shared memory), in earlier blocks, and the segments'
+// starts, the running sum of the padded counts.
+//
+// Up to kTile slots one block does it all.  More slots take three launches over
+// blocks of equal shares: count_kernel leaves each block's counts per expert at
+// the start of the block's own part of position[] (a share has at least kTile
+// slots, more than there can be experts), prefix_kernel sums them over the
+// blocks in place and writes counts[], and place_kernel, whose blocks first
+// take their counts out again, writes the places.  Each place is written by one
+// thread and the only atomics add integers, so the order is that of the slots.
+//
+// Bound by latency: 65536 x 8 slots are 6 MB of traffic, 1 us of HBM time.
 #include "sar_device.cuh"
 #include "sar_internal.h"
 
 namespace sar {
 namespace {
 
-constexpr int kMaxThreads = 1024, kMaxBlocks = 16, kUnroll = 4;
+constexpr unsigned kTile = 4096;                      // slots of one block, as many as 8191
+constexpr int kMaxThreads = 1024, kRounds = 8;        // 32-slot rounds of a warp
+static_assert(kTile >= SAR_MAX_EXPERTS, "a share's counts fit its part of position[]");
 
-// Expert of a slot, -1 outside 0 .. experts - 1.
+// Expert of a slot; `experts` for a dropped one.
 template <typename Id> __device__ __forceinline__ int expert_of(Id id, int experts) {
-    return id >= 0 && id < experts ? static_cast<int>(id) : -1;
+    return id >= 0 && id < experts ? static_cast<int>(id) : experts;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// First slot of share b of `blocks`.
+__device__ __forceinline__ uint32_t share_start(uint32_t slots, uint32_t b, uint32_t blocks) {
+    const uint32_t per = slots / blocks, more = slots % blocks;
+    return per * b + (b < more ? b : more);
 }
 
-// A word of block `rank`'s shared memory, at the address of `p` in this one's.
-__device__ __forceinline__ int ld_cluster(const int* p, unsigned rank) {
-    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), far;
-    int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(far) : "memory");
-    return v;
+template <typename Id> __global__ void __launch_bounds__(kMaxThreads) count_kernel(SortArgs a) {
+    __shared__ int hist[SAR_MAX_EXPERTS];
+    for (int e = threadIdx.x; e < a.experts; e += kMaxThreads) hist[e] = 0;
+    pdl_wait();
+    __syncthreads();
+    const Id* ids = static_cast<const Id*>(a.ids);
+    const uint32_t begin = share_start(a.slots, blockIdx.x, gridDim.x), end = share_start(a.slots, blockIdx.x + 1, gridDim.x);
+    int e[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+        const uint32_t i = begin + u * kMaxThreads + threadIdx.x;
+        e[u] = i < end ? expert_of<Id>(ids[i], a.experts) : a.experts;
+    }
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u)
+        if (e[u] < a.experts) atomicAdd(&hist[e[u]], 1);
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.experts; k += kMaxThreads) a.position[begin + k] = hist[k];
 }
 
-template <typename Id>
-__global__ void __launch_bounds__(kMaxThreads) sort_kernel(SortArgs a) {
+// 32 experts a block, a warp's lanes; the warps share the blocks' counts.
+__global__ void __launch_bounds__(kMaxThreads) prefix_kernel(SortArgs a, uint32_t blocks) {
+    __shared__ int part[32][32];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const uint32_t per = (blocks + 31) / 32, b0 = per * warp, b1 = b0 + per < blocks ? b0 + per : blocks;
+    int sum = 0;
+    if (e < a.experts) {
+#pragma unroll 4
+        for (uint32_t b = b0; b < b1; ++b) sum += a.position[share_start(a.slots, b, blocks) + e];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int before = 0;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) {
+            const int c = part[w][lane];
+            part[w][lane] = before;
+            before += c;
+        }
+        if (e < a.experts) a.counts[e] = before;
+    }
+    __syncthreads();
+    if (e < a.experts) {
+        int before = part[warp][lane];
+        for (uint32_t b = b0; b < b1; ++b) {
+            int* at = a.position + share_start(a.slots, b, blocks) + e;
+            const int c = *at;
+            *at = before;
+            before += c;
+        }
+    }
+}
+
+// Places of one share of the slots; with kSingle the only one, which also
+// counts.
+template <typename Id, bool kSingle>
+__global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, int bits) {
     extern __shared__ int smem[];
-    const int warps = blockDim.x >> 5, E = a.experts;
+    const int warps = blockDim.x >> 5, E = a.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* hist = smem;                                 // [warps][E]: counts, then first places
-    int* total = hist + warps * E;                    // [E]: this block's counts
-    int* start = total + E;                           // [E + 1]: the segments' starts
-    int* filled = start + E + 1;                      // [E]: the ends of their slots
+    int* start = hist + warps * E;                    // [E]: the segments' starts
+    int* filled = start + E;                          // [E]: the ends of their slots
     int* carry = filled + E;                          // [32]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = gridDim.x, block = blockIdx.x;
     int* mine = hist + warp * E;
     for (int i = lane; i < E; i += 32) mine[i] = 0;
     __syncwarp();
     pdl_wait();
 
     const Id* ids = static_cast<const Id*>(a.ids);
-    const uint32_t runs = static_cast<uint32_t>(warps) * nb;
-    const uint32_t per = ((a.slots + runs - 1) / runs + 31) / 32 * 32;
-    const uint64_t begin = static_cast<uint64_t>(per) * (static_cast<uint32_t>(block) * warps + warp);
-    const uint64_t end = begin + per < a.slots ? begin + per : a.slots;
+    const uint32_t begin = share_start(a.slots, blockIdx.x, gridDim.x), end = share_start(a.slots, blockIdx.x + 1, gridDim.x);
+    const uint32_t rounds = (end - begin + blockDim.x - 1) / blockDim.x;
+    const uint32_t first = begin + warp * rounds * 32 + lane;
     const unsigned below = (1u << lane) - 1;
-    for (uint64_t i0 = begin; i0 < end; i0 += 32 * kUnroll) {
-        int e[kUnroll];
+    int e[kRounds], rank[kRounds];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint64_t i = i0 + 32 * u + lane;
-            e[u] = i < end ? expert_of<Id>(ids[i], E) : -1;
-        }
+    for (int u = 0; u < kRounds; ++u) {
+        const uint32_t i = first + u * 32;
+        e[u] = static_cast<uint32_t>(u) < rounds && i < end ? expert_of<Id>(ids[i], E) : E;
+    }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint64_t i = i0 + 32 * u + lane;
-            const unsigned peers = __match_any_sync(0xFFFFFFFFu, e[u]);
-            const int before = e[u] >= 0 ? mine[e[u]] : 0;
-            __syncwarp();
-            if (e[u] >= 0 && (peers & below) == 0) mine[e[u]] = before + __popc(peers);
-            __syncwarp();
-            if (i < end) a.position[i] = before + __popc(peers & below);
+    for (int u = 0; u < kRounds; ++u) {
+        if (static_cast<uint32_t>(u) >= rounds) break;
+        unsigned peers = 0xFFFFFFFFu;
+        for (int b = 0; b < bits; ++b) {
+            const bool one = (e[u] >> b) & 1;
+            const unsigned with = __ballot_sync(0xFFFFFFFFu, one);
+            peers &= one ? with : ~with;
         }
+        const int before = e[u] < E ? mine[e[u]] : 0;
+        __syncwarp();
+        if (e[u] < E && (peers & below) == 0) mine[e[u]] = before + __popc(peers);
+        __syncwarp();
+        rank[u] = before + __popc(peers & below);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int sum = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int c = hist[w * E + e];
-            hist[w * E + e] = sum;
-            sum += c;
-        }
-        total[e] = sum;
-    }
-    cluster_sync();
-    // Experts in tiles of the block's threads: counts over the cluster, and the
-    // running sum of the padded counts.
+    // Experts in tiles of the block's threads.
     int done = 0;
     for (int e0 = 0; e0 < E; e0 += blockDim.x) {
-        const int e = e0 + threadIdx.x;
+        const int x = e0 + threadIdx.x;
         int count = 0, before = 0;
-        if (e < E) {
-            for (int b = 0; b < nb; ++b) {
-                const int c = ld_cluster(total + e, b);
-                if (b < block) before += c;
-                count += c;
+        if (x < E) {
+            int sum = 0;
+            for (int w = 0; w < warps; ++w) {
+                const int c = hist[w * E + x];
+                hist[w * E + x] = sum;
+                sum += c;
             }
+            count = kSingle ? sum : a.counts[x];
+            before = kSingle ? 0 : a.position[begin + x];
         }
         const int padded = (count + a.align - 1) / a.align * a.align;
         int up = padded;
@@ -114,95 +159,75 @@ __global__ void __launch_bounds__(kMaxThreads) sort_kernel(SortArgs a) {
         }
         if (lane == 31) carry[warp] = up;
         __syncthreads();
-        int base = done, all = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int c = carry[w];
-            if (w < warp) base += c;
-            all += c;
+        int c = lane < warps ? carry[lane] : 0;       // the warps' sums: before this one, and all
+        const int all = __reduce_add_sync(0xFFFFFFFFu, c);
+        c = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? c : 0);
+        if (x < E) {
+            const int at = done + c + up - padded;
+            start[x] = at + before;
+            filled[x] = at + count;
+            if (blockIdx.x == 0) {
+                if (kSingle) a.counts[x] = count;
+                a.offsets[x] = at;
+            }
         }
         done += all;
-        if (e < E) {
-            const int first = base + up - padded;
-            start[e] = first;
-            filled[e] = first + count;
-            if (block == 0) {
-                a.counts[e] = count;
-                a.offsets[e] = first;
-            }
-            for (int w = 0; w < warps; ++w) hist[w * E + e] += first + before;
-        }
         __syncthreads();
     }
-    if (block == 0 && threadIdx.x == 0) a.offsets[E] = done;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = done;
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+        const uint32_t i = first + u * 32;
+        if (static_cast<uint32_t>(u) >= rounds || i >= end) break;
+        int place = e[u] < E ? start[e[u]] + mine[e[u]] + rank[u] : -1;
+        if (static_cast<uint32_t>(place) >= a.capacity) place = -1;
+        a.position[i] = place;
+        if (place >= 0 && a.source != nullptr) a.source[place] = static_cast<int>(i);
+    }
     if (a.source != nullptr) {                        // places without a slot: padding, and past the segments
-        for (int e = block * warps + warp; e < E; e += static_cast<int>(runs)) {
-            const uint32_t last = static_cast<uint32_t>(e + 1 < E ? start[e + 1] : done);
-            for (uint32_t p = filled[e] + lane; p < last && p < a.capacity; p += 32) a.source[p] = -1;
+        const unsigned runs = gridDim.x * warps;
+        if (a.align > 1) {
+            for (int x = blockIdx.x * warps + warp; x < E; x += static_cast<int>(runs)) {
+                // up to the next segment's start
+                const uint32_t from = filled[x];
+                const uint32_t to = (from + a.align - 1) / a.align * a.align;
+                for (uint32_t p = from + lane; p < to && p < a.capacity; p += 32) a.source[p] = -1;
+            }
         }
-        for (uint64_t p = static_cast<uint64_t>(done) + block * blockDim.x + threadIdx.x; p < a.capacity;
-             p += nb * blockDim.x)
+        for (uint64_t p = static_cast<uint64_t>(done) + blockIdx.x * blockDim.x + threadIdx.x; p < a.capacity;
+             p += static_cast<uint64_t>(gridDim.x) * blockDim.x)
             a.source[p] = -1;
     }
-    for (uint64_t i0 = begin; i0 < end; i0 += 32 * kUnroll) {
-        int e[kUnroll], rank[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint64_t i = i0 + 32 * u + lane;
-            e[u] = i < end ? expert_of<Id>(ids[i], E) : -1;
-            rank[u] = i < end ? a.position[i] : 0;
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint64_t i = i0 + 32 * u + lane;
-            int place = e[u] >= 0 ? mine[e[u]] + rank[u] : -1;
-            if (static_cast<uint32_t>(place) >= a.capacity) place = -1;
-            if (i < end) a.position[i] = place;
-            if (place >= 0 && a.source != nullptr) a.source[place] = static_cast<int>(i);
-        }
-    }
-    cluster_sync();                                   // no block leaves while another reads its counts
 }
 
-size_t smem_bytes(int warps, int experts) {
-    return (static_cast<size_t>(warps) * experts + 3 * experts + 1 + 32) * sizeof(int);
+size_t smem_bytes(unsigned warps, int experts) {
+    return (static_cast<size_t>(warps) * experts + 2 * static_cast<size_t>(experts) + 32) * sizeof(int);
+}
+
+template <typename Id, bool kSingle> cudaError_t place(const SortArgs& a, unsigned blocks, unsigned threads, cudaStream_t s) {
+    // Shared memory above 48 KiB is allowed explicitly, once per device (only a
+    // successful call is remembered).
+    static std::atomic<bool> allowed[kDevices];
+    const cudaError_t e = allow_smem(place_kernel<Id, kSingle>, smem_bytes(kMaxThreads / 32, SAR_MAX_EXPERTS), allowed);
+    if (e != cudaSuccess) return e;
+    int bits = 0;
+    while (a.experts >> bits) ++bits;                 // of 0 .. experts
+    return launch_kernel_smem(place_kernel<Id, kSingle>, dim3(blocks), dim3(threads), smem_bytes(threads / 32, a.experts), s, a,
+                              bits);
 }
 
 template <typename Id> cudaError_t sort(const SortArgs& a, cudaStream_t s) {
-    // Clusters above 8 blocks and shared memory above 48 KiB are allowed
-    // explicitly, once per device (only a successful call is remembered).
-    constexpr int kMaxDev = 64;
-    static std::atomic<bool> allowed[kMaxDev];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-    if (!allowed[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem_bytes(kMaxThreads / 32, SAR_MAX_EXPERTS)));
-        if (e != cudaSuccess) return e;
-        allowed[dev].store(true, std::memory_order_release);
+    if (a.slots < 2 * kTile) {
+        unsigned threads = 64;
+        while (threads < kMaxThreads && threads < a.slots) threads *= 2;
+        return place<Id, true>(a, 1, threads, s);
     }
-    // Runs of about 64 slots a warp, then as many blocks as that takes.
-    unsigned threads = 64, blocks = 1;
-    while (threads < kMaxThreads && threads * 2u < a.slots) threads *= 2;
-    while (blocks < kMaxBlocks && static_cast<size_t>(blocks) * kMaxThreads * 4 < a.slots) blocks *= 2;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = blocks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem_bytes(static_cast<int>(threads / 32), a.experts);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sort_kernel<Id>, a);
+    const unsigned blocks = a.slots / kTile;
+    cudaError_t e = launch_kernel(count_kernel<Id>, dim3(blocks), dim3(kMaxThreads), s, a);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(prefix_kernel, dim3((a.experts + 31) / 32), dim3(kMaxThreads), s, a, static_cast<uint32_t>(blocks));
+    if (e != cudaSuccess) return e;
+    return place<Id, false>(a, blocks, kMaxThreads, s);
 }
 
 }  // namespace

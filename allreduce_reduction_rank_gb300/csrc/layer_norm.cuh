@@ -11,8 +11,6 @@
 //            row.
 #pragma once
 
-#include <atomic>
-
 #include "sar_device.cuh"
 #include "sar_internal.h"
 
@@ -304,7 +302,7 @@ forward_kernel(NormArgs a, bool w32, float inv_n) {
 // flight.  At the end the groups of a block are added in order in shared
 // memory, and each block writes one row of sums, which params_kernel adds.
 // ---------------------------------------------------------------------------
-constexpr int kSMs = 152, kMaxDevices = 64;
+constexpr int kSMs = 152;
 
 template <int TPR> struct BackwardShape {
     static constexpr int kThreads = TPR > 512 ? TPR : 512;

@@ -462,24 +462,9 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
     }
 }
 
-// Dynamic shared memory above 48 KiB is allowed explicitly, once per device and
-// kernel (only a successful call is remembered).
-template <class Kernel> cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<bool>* allowed) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!allowed[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-        if (e != cudaSuccess) return e;
-        allowed[dev].store(true, std::memory_order_release);
-    }
-    return cudaSuccess;
-}
-
 template <int DT, int NV, int R, int D, bool kShift, int WPG>
 cudaError_t ring_launch_as(const NormArgs& a, bool w32, size_t vecs, const Alignment& al, cudaStream_t s) {
-    static std::atomic<bool> allowed[kMaxDevices];
+    static std::atomic<bool> allowed[kDevices];
     constexpr size_t smem = static_cast<size_t>(D) * R * NV * kRingThreads<NV> * 16;
     const cudaError_t e = allow_smem(ring_forward_kernel<DT, NV, R, D, kShift, WPG>, smem, allowed);
     if (e != cudaSuccess) return e;
@@ -490,7 +475,7 @@ cudaError_t ring_launch_as(const NormArgs& a, bool w32, size_t vecs, const Align
 
 template <int DT, int NV, int R, int D, bool kShift, int WPG>
 cudaError_t ring_launch_as(const NormGradArgs& a, bool w32, size_t vecs, const Alignment& al, cudaStream_t s) {
-    static std::atomic<bool> allowed[kMaxDevices];
+    static std::atomic<bool> allowed[kDevices];
     constexpr size_t smem = static_cast<size_t>(D) * R * 2 * NV * kRingThreads<NV> * 16;
     const cudaError_t e = allow_smem(ring_backward_kernel<DT, NV, R, D, kShift, WPG>, smem, allowed);
     if (e != cudaSuccess) return e;

@@ -2,6 +2,7 @@
 // All arguments have been validated by the caller.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -39,6 +40,23 @@ cudaError_t launch_kernel_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args&&... args) {
     return launch_kernel_smem(kernel, grid, block, 0, s, std::forward<Args>(args)...);
+}
+
+constexpr int kDevices = 64;
+
+// Dynamic shared memory above 48 KiB is allowed explicitly, once per device and
+// kernel (only a successful call is remembered).
+template <class Kernel> cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<bool>* allowed) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!allowed[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (e != cudaSuccess) return e;
+        allowed[dev].store(true, std::memory_order_release);
+    }
+    return cudaSuccess;
 }
 
 // What an rsag launch writes: the fused allreduce writes the reduced chunk to

@@ -22,6 +22,7 @@ Function names follow the C ABI: :func:`sar_allreduce`,
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -327,207 +328,39 @@ def sar_read_device_status(status, stream=None) -> int:
     return int(lib.sar_read_device_status(_addr(status), _stream(stream)))
 
 
+
 # ---------------------------------------------------------------------------
-# Operators around the allreduce (see include/sar.h).  They take torch tensors:
-# matrices are 2-D with dense rows (a slice of columns is fine), parameters,
-# statistics and positions contiguous.  Shapes, types and devices are checked
-# here (ValueError), since the C ABI sees addresses only.
+# Operators around the allreduce (see include/sar.h).  They take torch tensors
+# and live in a compiled module beside the library (csrc/torch_binding.cpp),
+# which checks shapes, types and devices (ValueError), since the C ABI sees
+# addresses only.
 # ---------------------------------------------------------------------------
-_CODES = {td: code for code, td in TORCH_DTYPES.items()}
-# The current stream's handle without building a Stream object, where torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _load_operators():
+    path = os.path.join(_HERE, "_build", "_sar_torch.so")
+    if not os.path.exists(path):
+        raise ImportError(f"libsar's torch module is not built ({path} missing); run "
+                          "`python allreduce_reduction_rank_gb300/build.py`")
+    spec = importlib.util.spec_from_file_location("_sar_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module._set_error(SarError)
+    return module
 
 
-def _stream_on(stream, device: int) -> int:
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(device)
-    return _stream(stream)
-
-
-def _matrix(t, name, dtype, device):
-    """Address and leading dimension of a 2-D tensor with dense rows."""
-    if t.dim() != 2 or t.dtype != dtype or t.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a 2-D {dtype} tensor on the same CUDA device as the others")
-    ld, step = t.stride()
-    rows, cols = t.shape
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have dense rows")
-    return t.data_ptr(), ld if rows > 1 else cols
-
-
-def _vector(t, name, dtype, n, device):
-    """Address of a contiguous tensor of n elements."""
-    if t.dtype != dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on the same CUDA device")
-    return t.data_ptr()
-
-
-def _param_dtype(dtype, *params):
-    """The type of the given parameters (fp32 or dtype itself), as torch's and the library's."""
-    for p in params:
-        if p is not None:
-            if p.dtype != torch.float32 and p.dtype != dtype:
-                raise ValueError(f"parameters must be float32 or {dtype}")
-            return p.dtype, _CODES[p.dtype]
-    return dtype, _CODES[dtype]
-
-
-def _element_code(t, name) -> int:
-    if t.dtype not in _CODES:
-        raise ValueError(f"unsupported {name} dtype {t.dtype}")
-    return _CODES[t.dtype]
-
-
-def sar_layer_norm(x, y, weight=None, bias=None, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
-    """y = (x - mean) * rstd * weight + bias for every row of x; mean and rstd
-    (float32, one per row) are written when given."""
-    code, td, dev = _element_code(x, "x"), x.dtype, x.get_device()
-    if x.shape != y.shape:
-        raise ValueError("x and y must have one shape")
-    px, ldx = _matrix(x, "x", td, dev)
-    py, ldy = _matrix(y, "y", td, dev)
-    rows, cols = x.shape
-    wd, wcode = _param_dtype(td, weight, bias)
-    _check(lib.sar_layer_norm(
-        px, ldx, None if weight is None else _vector(weight, "weight", wd, cols, dev),
-        None if bias is None else _vector(bias, "bias", wd, cols, dev), py, ldy,
-        None if mean is None else _vector(mean, "mean", torch.float32, rows, dev),
-        None if rstd is None else _vector(rstd, "rstd", torch.float32, rows, dev),
-        rows, cols, eps, code, wcode, _stream_on(stream, dev)))
+_operators = _load_operators()
+sar_layer_norm = _operators.sar_layer_norm
+sar_layer_norm_backward = _operators.sar_layer_norm_backward
+sar_expert_sort = _operators.sar_expert_sort
+sar_expert_dispatch = _operators.sar_expert_dispatch
+sar_expert_combine = _operators.sar_expert_combine
+sar_expert_combine_backward = _operators.sar_expert_combine_backward
 
 
 def sar_layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    """Bytes of sar_layer_norm_backward's workspace."""
     return int(lib.sar_layer_norm_backward_workspace_bytes(rows, cols))
-
-
-def sar_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None, stream=None) -> None:
-    """The gradients of sar_layer_norm.  dweight and dbias (optional; of
-    weight's type) need a workspace of sar_layer_norm_backward_workspace_bytes:
-    a contiguous tensor of any type, 16-byte aligned."""
-    code, td, dev = _element_code(x, "x"), x.dtype, x.get_device()
-    if x.shape != dy.shape or x.shape != dx.shape:
-        raise ValueError("dy, x and dx must have one shape")
-    pdy, lddy = _matrix(dy, "dy", td, dev)
-    px, ldx = _matrix(x, "x", td, dev)
-    pdx, lddx = _matrix(dx, "dx", td, dev)
-    rows, cols = x.shape
-    wd, wcode = _param_dtype(td, weight, dweight, dbias)
-    pws, nws = None, 0
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.get_device() != dev:
-            raise ValueError("workspace must be a contiguous tensor on the same CUDA device")
-        pws, nws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.sar_layer_norm_backward(
-        pdy, lddy, px, ldx, None if weight is None else _vector(weight, "weight", wd, cols, dev),
-        _vector(mean, "mean", torch.float32, rows, dev), _vector(rstd, "rstd", torch.float32, rows, dev), pdx, lddx,
-        None if dweight is None else _vector(dweight, "dweight", wd, cols, dev),
-        None if dbias is None else _vector(dbias, "dbias", wd, cols, dev),
-        rows, cols, code, wcode, pws, nws, _stream_on(stream, dev)))
 
 
 def sar_expert_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int:
     """Rows that hold every expert's segment whatever the routing."""
     return int(lib.sar_expert_rows(tokens, topk, experts, align))
-
-
-def _positions(position, dev):
-    """Address, tokens and choices per token of a (tokens, topk) int32 tensor."""
-    if position.dim() != 2:
-        raise ValueError("position must have the shape (tokens, topk)")
-    tokens, topk = position.shape
-    return _vector(position, "position", torch.int32, tokens * topk, dev), tokens, topk
-
-
-def _segments(counts, offsets, dev):
-    if counts is None and offsets is None:
-        return None, None, 0
-    if counts is None or offsets is None:
-        raise ValueError("counts and offsets go together")
-    n = counts.numel()
-    return (_vector(counts, "counts", torch.int32, n, dev), _vector(offsets, "offsets", torch.int32, n + 1, dev), n)
-
-
-def sar_expert_sort(ids, counts, offsets, position, source=None, align: int = 1, capacity=None, stream=None) -> None:
-    """Sorts the choices ids (tokens, topk; int32 or int64) by expert: counts
-    (experts), offsets (experts + 1), position (tokens, topk) and, optional,
-    source (capacity), all int32.  Without source, capacity says how many places
-    there are (default: enough for every routing)."""
-    dev = ids.get_device()
-    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous() or dev < 0:
-        raise ValueError("ids must be a contiguous (tokens, topk) int32 or int64 CUDA tensor")
-    tokens, topk = ids.shape
-    experts = counts.numel()
-    if source is not None:
-        if capacity is not None and capacity != source.numel():
-            raise ValueError("capacity must be source's length")
-        capacity = source.numel()
-    elif capacity is None:
-        capacity = sar_expert_rows(tokens, topk, experts, align)
-    _check(lib.sar_expert_sort(
-        ids.data_ptr(), 8 if ids.dtype == torch.int64 else 4, tokens, topk, experts, align, capacity,
-        _vector(counts, "counts", torch.int32, experts, dev),
-        _vector(offsets, "offsets", torch.int32, experts + 1, dev),
-        _vector(position, "position", torch.int32, tokens * topk, dev),
-        None if source is None else _vector(source, "source", torch.int32, capacity, dev), _stream_on(stream, dev)))
-
-
-def sar_expert_dispatch(x, position, rows, counts=None, offsets=None, dtype=None, stream=None) -> None:
-    """rows[position[t, j]] = x[t]; with counts and offsets the segments'
-    padding becomes zero.  dtype: the type of the elements where torch has no
-    type for them ("e4m3b15" in uint8 tensors)."""
-    dev, td = x.get_device(), x.dtype
-    code = _element_code(x, "x") if dtype is None else _dtype_code(dtype)
-    if ESIZE.get(code) != x.element_size():
-        raise ValueError("dtype does not fit the tensors' elements")
-    ppos, tokens, topk = _positions(position, dev)
-    if x.dim() != 2 or rows.dim() != 2 or x.shape[0] != tokens or x.shape[1] != rows.shape[1]:
-        raise ValueError("x must be (tokens, cols) and rows (capacity, cols)")
-    px, ldx = _matrix(x, "x", td, dev)
-    pr, ldr = _matrix(rows, "rows", td, dev)
-    pc, po, experts = _segments(counts, offsets, dev)
-    capacity, cols = rows.shape
-    _check(lib.sar_expert_dispatch(px, ldx, ppos, pc, po, experts, pr, ldr, capacity, tokens, topk, cols, code,
-                                   _stream_on(stream, dev)))
-
-
-def sar_expert_combine(rows, position, out, weights=None, stream=None) -> None:
-    """out[t] = sum over the kept choices j of weights[t, j] * rows[position[t, j]];
-    without weights the plain sum, which is sar_expert_dispatch's gradient."""
-    dev, td = rows.get_device(), rows.dtype
-    code = _element_code(rows, "rows")
-    ppos, tokens, topk = _positions(position, dev)
-    if rows.dim() != 2 or out.dim() != 2 or out.shape[0] != tokens or out.shape[1] != rows.shape[1]:
-        raise ValueError("out must be (tokens, cols) and rows (capacity, cols)")
-    pr, ldr = _matrix(rows, "rows", td, dev)
-    po, ldo = _matrix(out, "out", td, dev)
-    wd, wcode = _param_dtype(td, weights)
-    capacity, cols = rows.shape
-    _check(lib.sar_expert_combine(pr, ldr, capacity, ppos,
-                                  None if weights is None else _vector(weights, "weights", wd, tokens * topk, dev),
-                                  po, ldo, tokens, topk, cols, code, wcode, _stream_on(stream, dev)))
-
-
-def sar_expert_combine_backward(dout, rows, position, weights, drows, dweights=None, counts=None, offsets=None,
-                                stream=None) -> None:
-    """The gradients of sar_expert_combine with weights: drows and, optional,
-    dweights (of weights' type; without it rows may be None).  With counts and
-    offsets the padding rows of drows become zero."""
-    dev, td = dout.get_device(), dout.dtype
-    code = _element_code(dout, "dout")
-    ppos, tokens, topk = _positions(position, dev)
-    if dout.dim() != 2 or drows.dim() != 2 or dout.shape[0] != tokens or dout.shape[1] != drows.shape[1]:
-        raise ValueError("dout must be (tokens, cols) and drows (capacity, cols)")
-    pdo, ldo = _matrix(dout, "dout", td, dev)
-    pdr, lddr = _matrix(drows, "drows", td, dev)
-    pr, ldr = None, 0
-    if dweights is not None:
-        if rows is None or rows.shape != drows.shape:
-            raise ValueError("rows must have the shape of drows")
-        pr, ldr = _matrix(rows, "rows", td, dev)
-    wd, wcode = _param_dtype(td, weights)
-    pc, po, experts = _segments(counts, offsets, dev)
-    capacity, cols = drows.shape
-    _check(lib.sar_expert_combine_backward(
-        pdo, ldo, pr, ldr, capacity, ppos, _vector(weights, "weights", wd, tokens * topk, dev), pc, po, experts, pdr,
-        lddr, None if dweights is None else _vector(dweights, "dweights", wd, tokens * topk, dev), tokens, topk, cols,
-        code, wcode, _stream_on(stream, dev)))

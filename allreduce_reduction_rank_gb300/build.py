@@ -5,7 +5,9 @@ Usage: ``python allreduce_reduction_rank_gb300/build.py [--force] [--verbose-ptx
 Each CUDA translation unit is compiled in parallel into an object file under
 ``_build/`` and the objects are linked into ``_build/libsar.so`` (C ABI,
 declared in ``include/sar.h``; the CUDA runtime is linked statically and its
-symbols are kept private).  Floating point is compiled without fast-math,
+symbols are kept private).  The torch module ``_build/_sar_torch.so``
+(``csrc/torch_binding.cpp``) is compiled at the same time with the host compiler
+against the installed torch.  Floating point is compiled without fast-math,
 flush-to-zero or contraction so that the binary32 adds are exactly IEEE adds
 with gradual underflow.
 
@@ -15,16 +17,19 @@ exists.
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libsar.so")
+TORCH_MODULE = os.path.join(OUT, "_sar_torch.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 # Slowest first, so the parallel build finishes sooner.
@@ -54,6 +59,31 @@ def nvcc_path() -> str:
     return p
 
 
+def torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the binding needs it to build")
+    return list(spec.submodule_search_locations)[0]
+
+
+def compile_binding(force: bool) -> str:
+    """The torch module's object file."""
+    path, obj = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(OUT, "torch_binding.cpp.obj")
+    # Rebuilt with another torch or Python, too: their headers define what it may assume.
+    deps = [path, os.path.join(INCLUDE, "sar.h"), os.path.join(torch_dir(), "version.py")]
+    if force or _stale(obj, deps):
+        cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-I", INCLUDE,
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir(), "include"),
+               "-I", os.path.join(torch_dir(), "include", "torch", "csrc", "api", "include"),
+               "-I", os.path.join(cuda, "include"), "-c", path, "-o", obj + ".tmp"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{res.stdout}\n{res.stderr}")
+        os.replace(obj + ".tmp", obj)
+    return obj
+
+
 def _stale(target: str, deps: list) -> bool:
     if not os.path.exists(target):
         return True
@@ -80,16 +110,27 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             os.replace(obj + ".tmp", obj)
         return obj
 
-    with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(min(len(SOURCES) + 1, (os.cpu_count() or 4) + 1)) as ex:
+        binding = ex.submit(compile_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + [
-            "-Xlinker", "--exclude-libs,ALL", "-Xlinker", "-z,defs"]
+            "-Xlinker", "--exclude-libs,ALL", "-Xlinker", "-z,defs", "-Xlinker", "-soname=libsar.so"]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    if force or _stale(TORCH_MODULE, [binding_obj, LIB]):
+        tmp = TORCH_MODULE + f".tmp{os.getpid()}"
+        lib_dir = os.path.join(torch_dir(), "lib")
+        cmd = ["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L", lib_dir, "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib_dir]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link of the torch module failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, TORCH_MODULE)
     return LIB
 
 

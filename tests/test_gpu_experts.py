@@ -144,7 +144,7 @@ def test_dispatch(sar, plan, cols, dtype):
         else:
             rows, flat = placed(torch.full((src.numel(), cols), MARK, dtype=td, device="cuda"), gap, offset)
         sar.sar_expert_dispatch(x, position, rows, counts if clear else None, offsets if clear else None,
-                                dtype=dtype if dtype == "e4m3b15" else None)
+                                dtype=sar.SAR_FP8_E4M3B15 if dtype == "e4m3b15" else None)
         torch.cuda.synchronize()
         want = torch.full_like(bits(rows), 3) if x.element_size() == 1 else bits(torch.full_like(rows, MARK))
         if clear:

@@ -117,11 +117,23 @@ def test_binding_refuses_what_the_boundary_cannot_see(sar):
                  lambda: sar.sar_layer_norm_backward(x, x, None, f, f, x),
                  lambda: sar.sar_expert_sort(i, f.int(), torch.zeros(5, dtype=torch.int32), i),
                  lambda: sar.sar_expert_dispatch(x, i, x), lambda: sar.sar_expert_dispatch(x, i[0], x),
-                 lambda: sar.sar_expert_dispatch(x, i, x, dtype="bf16"), lambda: sar.sar_expert_combine(x, i, x),
+                 lambda: sar.sar_expert_dispatch(x, i, x, dtype=0), lambda: sar.sar_expert_combine(x, i, x),
                  lambda: sar.sar_expert_combine(x, i, torch.zeros(4, 7)),
                  lambda: sar.sar_expert_combine_backward(x, x, i, f, x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_arguments(sar):
+    import inspect
+    assert list(inspect.signature(sar.sar_layer_norm).parameters) == ["x", "y", "weight", "bias", "mean", "rstd", "eps", "stream"]
+    for call in (lambda: sar.sar_layer_norm(), lambda: sar.sar_layer_norm(torch.zeros(1, 1)),
+                 lambda: sar.sar_layer_norm(1, 2, 3, 4, 5, 6, 7, 8, 9), lambda: sar.sar_layer_norm(1, 2, x=3),
+                 lambda: sar.sar_layer_norm(1, 2, z=3)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        sar.sar_layer_norm(None, None)
 
 
 def test_binding_lists_every_operator(sar):

@@ -7,6 +7,7 @@
 // a time) in flight together.  A token's own row is touched once.
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "sar_device.cuh"
 #include "sar_internal.h"
@@ -90,15 +91,21 @@ __device__ __forceinline__ int place_of(const ExpertArgs& a, size_t t, int j) {
 // each of kBlock / TX tokens; gridDim.y shares a row's granules.
 struct Shape {
     unsigned tx, granules;       // threads, granules per row
-    unsigned token_blocks;       // blocks (x) of tokens; then one per expert
+    unsigned token_blocks;       // blocks (x) of tokens
+    unsigned pad_blocks;         // blocks before them, kPadShares for each expert
 };
 
-// Clears the padding rows of segment e.
-template <int GB> __device__ void clear_padding(const ExpertArgs& a, const Shape& sh, unsigned e, size_t es) {
+// Blocks that clear the padding of a segment.  They come first in the grid, so
+// that theirs is not the last work of a small call.
+constexpr unsigned kPadShares = 4;
+
+// Clears a share of the padding rows of a segment.
+template <int GB> __device__ void clear_padding(const ExpertArgs& a, const Shape& sh, unsigned block, size_t es) {
+    const unsigned e = block / kPadShares;
     const int64_t first = static_cast<int64_t>(a.offsets[e]) + a.counts[e], end = a.offsets[e + 1];
     const int64_t last = end < static_cast<int64_t>(a.capacity) ? end : static_cast<int64_t>(a.capacity);
     Granule<GB> zero = {};
-    for (int64_t p = first; p < last; ++p)
+    for (int64_t p = first + block % kPadShares; p < last; p += kPadShares)
         for (unsigned v = blockIdx.y * kBlock + threadIdx.x; v < sh.granules; v += gridDim.y * kBlock)
             store<GB>(a.out, (static_cast<size_t>(p) * a.ldo) * es + static_cast<size_t>(v) * GB, zero);
 }
@@ -108,11 +115,11 @@ constexpr int kJ = 8;
 template <int GB>
 __global__ void __launch_bounds__(kBlock) dispatch_kernel(ExpertArgs a, Shape sh, unsigned es) {
     pdl_wait();
-    if (blockIdx.x >= sh.token_blocks) {
-        clear_padding<GB>(a, sh, blockIdx.x - sh.token_blocks, es);
+    if (blockIdx.x < sh.pad_blocks) {
+        clear_padding<GB>(a, sh, blockIdx.x, es);
         return;
     }
-    const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
     if (t >= a.tokens) return;
     const unsigned first = blockIdx.y * sh.tx + threadIdx.x % sh.tx, step = gridDim.y * sh.tx;
     for (int j0 = 0; j0 < a.topk; j0 += kJ) {
@@ -128,52 +135,79 @@ __global__ void __launch_bounds__(kBlock) dispatch_kernel(ExpertArgs a, Shape sh
     }
 }
 
-template <int WDT> __device__ __forceinline__ float weight_at(const ExpertArgs& a, size_t slot) {
-    return a.weights != nullptr ? load_elem<WDT>(a.weights, slot) : 1.0f;
-}
+// Sums on pairs of elements (one instruction for two, each half rounded as the
+// scalar one); a granule of one element uses one half.
+template <int DT, int GB> struct Sums {
+    static constexpr int kN = Elements<DT, GB>::kN, kPairs = (kN + 1) / 2;
+    float2 v[kPairs];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) v[p] = make_float2(-0.0f, -0.0f);
+    }
+    // += x, or += w * x by one fused multiply-add.
+    __device__ __forceinline__ void add(const Granule<GB>& g, float w, bool weighted) {
+        float x[2 * kPairs];
+        x[2 * kPairs - 1] = 0.0f;
+        widen<DT, GB>(g, x);
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+            const float2 f = make_float2(x[2 * p], x[2 * p + 1]);
+            v[p] = weighted ? __ffma2_rn(make_float2(w, w), f, v[p]) : __fadd2_rn(v[p], f);
+        }
+    }
+    __device__ __forceinline__ Granule<GB> rounded(bool any) const {
+        float x[2 * kPairs];
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) x[2 * p] = any ? v[p].x : 0.0f, x[2 * p + 1] = any ? v[p].y : 0.0f;
+        return narrow<DT, GB>(x);
+    }
+};
 
 // out = sum of w * row over the kept slots.  The sum starts from -0, the exact
 // identity of the round-to-nearest add, so that one row is copied bit for bit.
-template <int DT, int WDT, int GB>
-__global__ void __launch_bounds__(kBlock) combine_kernel(ExpertArgs a, Shape sh) {
-    constexpr int N = Elements<DT, GB>::kN;
+// kOne: at most kJ slots a token, whose places and weights are read once, and
+// rows within 2^32 granules of the first, so that a row's place is 32 bits.
+template <int DT, int WDT, int GB, bool kOne>
+__global__ void __launch_bounds__(kBlock, 4) combine_kernel(ExpertArgs a, Shape sh) {
+    using Offset = std::conditional_t<kOne, uint32_t, size_t>;          // in granules
+    constexpr Offset kNone = static_cast<Offset>(-1);
     constexpr size_t es = Elem<DT>::kSize;
     pdl_wait();
     const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
     if (t >= a.tokens) return;
     const unsigned first = blockIdx.y * sh.tx + threadIdx.x % sh.tx, step = gridDim.y * sh.tx;
-    for (unsigned v = first; v < sh.granules; v += step) {
-        float acc[N];
+    const bool weighted = a.weights != nullptr;
+    const Offset ld = static_cast<Offset>(a.ldi * es / GB);
+    Offset row[kJ];
+    float w[kJ];
+    auto slots_from = [&](int j0) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = -0.0f;
+        for (int j = 0; j < kJ; ++j) {
+            const int p = place_of(a, t, j0 + j);
+            row[j] = p >= 0 ? static_cast<Offset>(p) * ld : kNone;
+            w[j] = weighted && p >= 0 ? load_elem<WDT>(a.weights, t * a.topk + j0 + j) : 0.0f;
+        }
+    };
+    if (kOne) slots_from(0);
+    for (unsigned v = first; v < sh.granules; v += step) {
+        Sums<DT, GB> sum;
+        sum.clear();
         bool any = false;
-        for (int j0 = 0; j0 < a.topk; j0 += kJ) {
-            int p[kJ];
+        for (int j0 = 0; j0 < (kOne ? 1 : a.topk); j0 += kJ) {
+            if (!kOne) slots_from(j0);
             Granule<GB> g[kJ];
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) p[j] = place_of(a, t, j0 + j);
-#pragma unroll
             for (int j = 0; j < kJ; ++j)
-                if (p[j] >= 0) g[j] = load<GB>(a.rows_in, static_cast<size_t>(p[j]) * a.ldi * es + static_cast<size_t>(v) * GB);
+                if (row[j] != kNone) g[j] = load<GB>(a.rows_in, static_cast<size_t>(static_cast<Offset>(row[j] + v)) * GB);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-                if (p[j] < 0) continue;
+                if (row[j] == kNone) continue;
                 any = true;
-                float x[N];
-                widen<DT, GB>(g[j], x);
-                if (a.weights != nullptr) {
-                    const float w = load_elem<WDT>(a.weights, t * a.topk + j0 + j);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] = __fmaf_rn(w, x[e], acc[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], x[e]);
-                }
+                sum.add(g[j], w[j], weighted);
             }
         }
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = any ? acc[e] : 0.0f;
-        store<GB>(a.out, t * a.ldo * es + static_cast<size_t>(v) * GB, narrow<DT, GB>(acc));
+        store<GB>(a.out, t * a.ldo * es + static_cast<size_t>(v) * GB, sum.rounded(any));
     }
 }
 
@@ -186,19 +220,11 @@ __global__ void __launch_bounds__(kBlock) combine_backward_kernel(ExpertArgs a, 
     constexpr size_t es = Elem<DT>::kSize;
     __shared__ float red[W > 1 ? W : 1][J];
     pdl_wait();
-    if (blockIdx.x >= sh.token_blocks) {
-        if (blockIdx.y == 0) {
-            const unsigned e = blockIdx.x - sh.token_blocks;
-            const int64_t first = static_cast<int64_t>(a.offsets[e]) + a.counts[e], end = a.offsets[e + 1];
-            const int64_t last = end < static_cast<int64_t>(a.capacity) ? end : static_cast<int64_t>(a.capacity);
-            Granule<GB> zero = {};
-            for (int64_t p = first; p < last; ++p)
-                for (unsigned v = threadIdx.x; v < sh.granules; v += kBlock)
-                    store<GB>(a.out, static_cast<size_t>(p) * a.ldo * es + static_cast<size_t>(v) * GB, zero);
-        }
+    if (blockIdx.x < sh.pad_blocks) {
+        clear_padding<GB>(a, sh, blockIdx.x, es);
         return;
     }
-    const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / TX) + threadIdx.x / TX;
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / TX) + threadIdx.x / TX;
     const unsigned x = threadIdx.x % TX;
     if (t >= a.tokens) return;                        // whole warps; with W > 1 never
     for (int j0 = blockIdx.y * J; j0 < a.topk; j0 += gridDim.y * J) {
@@ -271,33 +297,40 @@ unsigned granule_of(std::initializer_list<const void*> ptrs, std::initializer_li
     return g;
 }
 
-// Threads per row: a power of two that covers the row's granules, from `least`
-// to kBlock.  gridDim.y: shares of a row, so that a few tokens still fill the
-// SMs (about four blocks each).
-Shape shape_of(size_t tokens, size_t granules, unsigned least) {
+// Threads per row: a power of two that covers the row's granules, up to kBlock.
+Shape shape_of(const ExpertArgs& a, size_t granules, unsigned least) {
     Shape sh;
     sh.tx = least;
     while (sh.tx < kBlock && sh.tx < granules) sh.tx *= 2;
     sh.granules = static_cast<unsigned>(granules);
     const size_t per = kBlock / sh.tx;
-    sh.token_blocks = static_cast<unsigned>((tokens + per - 1) / per);
+    sh.token_blocks = static_cast<unsigned>((a.tokens + per - 1) / per);
+    sh.pad_blocks = a.counts != nullptr ? kPadShares * a.experts : 0;
     return sh;
 }
 
+// Blocks (y) that share a token's row, one granule a thread, while the grid stays
+// within kSpread blocks.
+constexpr unsigned kSpread = 1216;
 unsigned row_shares(const Shape& sh) {
-    const unsigned most = (sh.granules + sh.tx - 1) / sh.tx, want = 608 / (sh.token_blocks < 608 ? sh.token_blocks : 608);
-    return want < 1 ? 1 : (want < most ? want : most);
+    const unsigned most = (sh.granules + sh.tx - 1) / sh.tx, want = kSpread / std::min(sh.token_blocks, kSpread);
+    return std::max(1u, std::min(want, most));
 }
 
 template <int GB> cudaError_t dispatch(const ExpertArgs& a, size_t es, cudaStream_t s) {
-    const Shape sh = shape_of(a.tokens, a.cols * es / GB, 8);
-    const dim3 grid(sh.token_blocks + (a.counts != nullptr ? a.experts : 0), row_shares(sh));
-    return launch_kernel(dispatch_kernel<GB>, grid, dim3(kBlock), s, a, sh, static_cast<unsigned>(es));
+    const Shape sh = shape_of(a, a.cols * es / GB, 8);
+    return launch_kernel(dispatch_kernel<GB>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(kBlock), s, a, sh,
+                         static_cast<unsigned>(es));
 }
 
 template <int DT, int WDT, int GB> cudaError_t combine(const ExpertArgs& a, cudaStream_t s) {
-    const Shape sh = shape_of(a.tokens, a.cols * Elem<DT>::kSize / GB, 8);
-    return launch_kernel(combine_kernel<DT, WDT, GB>, dim3(sh.token_blocks, row_shares(sh)), dim3(kBlock), s, a, sh);
+    const Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, 8);
+    const dim3 grid(sh.token_blocks, row_shares(sh)), block(kBlock);
+    const size_t ld = a.ldi * Elem<DT>::kSize / GB;
+    const bool near = a.capacity == 0 || ld < 0xFFFFFFFFu / a.capacity;       // a place and the row after it
+    return a.topk <= kJ && near
+               ? launch_kernel(combine_kernel<DT, WDT, GB, true>, grid, block, s, a, sh)
+               : launch_kernel(combine_kernel<DT, WDT, GB, false>, grid, block, s, a, sh);
 }
 
 template <int DT, int WDT> cudaError_t combine_by_granule(const ExpertArgs& a, cudaStream_t s) {
@@ -309,18 +342,21 @@ template <int DT, int WDT> cudaError_t combine_by_granule(const ExpertArgs& a, c
     return combine<DT, WDT, es>(a, s);
 }
 
+// Slots up to which the backward call has a block for each.
+constexpr size_t kFewSlots = 2432;
+
 template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const ExpertArgs& a, cudaStream_t s) {
-    Shape sh = shape_of(a.tokens, a.cols * Elem<DT>::kSize / GB, TX);
+    Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, TX);
     sh.tx = TX;
     sh.token_blocks = static_cast<unsigned>((a.tokens + kBlock / TX - 1) / (kBlock / TX));
-    const dim3 grid(sh.token_blocks + (a.counts != nullptr ? a.experts : 0), std::min((a.topk + J - 1) / J, 65535));
+    const dim3 grid(sh.pad_blocks + sh.token_blocks, std::min((a.topk + J - 1) / J, 65535));
     return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(kBlock), s, a, sh);
 }
 
 template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArgs& a, cudaStream_t s) {
     const bool narrow_rows = a.cols * Elem<DT>::kSize / GB <= 128;
     // Few tokens: a block for each slot.
-    const bool few = a.tokens * a.topk <= 608;
+    const bool few = a.tokens * a.topk <= kFewSlots;
     if (narrow_rows) return few ? backward<DT, WDT, GB, 32, 1>(a, s) : backward<DT, WDT, GB, 32, 4>(a, s);
     return few ? backward<DT, WDT, GB, 256, 1>(a, s) : backward<DT, WDT, GB, 256, 4>(a, s);
 }

@@ -32,19 +32,19 @@ template <typename Id> __device__ __forceinline__ int expert_of(Id id, int exper
     return id >= 0 && id < experts ? static_cast<int>(id) : experts;
 }
 
-// First slot of share b of `blocks`.
-__device__ __forceinline__ uint32_t share_start(uint32_t slots, uint32_t b, uint32_t blocks) {
-    const uint32_t per = slots / blocks, more = slots % blocks;
-    return per * b + (b < more ? b : more);
-}
+// The blocks' shares of the slots: `per` each, the first `more` of them one more.
+struct Shares {
+    uint32_t blocks, per, more;
+    __device__ __forceinline__ uint32_t start(uint32_t b) const { return per * b + (b < more ? b : more); }
+};
 
-template <typename Id> __global__ void __launch_bounds__(kMaxThreads) count_kernel(SortArgs a) {
+template <typename Id> __global__ void __launch_bounds__(kMaxThreads) count_kernel(SortArgs a, Shares shares) {
     __shared__ int hist[SAR_MAX_EXPERTS];
     for (int e = threadIdx.x; e < a.experts; e += kMaxThreads) hist[e] = 0;
     pdl_wait();
     __syncthreads();
     const Id* ids = static_cast<const Id*>(a.ids);
-    const uint32_t begin = share_start(a.slots, blockIdx.x, gridDim.x), end = share_start(a.slots, blockIdx.x + 1, gridDim.x);
+    const uint32_t begin = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
     int e[kRounds];
 #pragma unroll
     for (int u = 0; u < kRounds; ++u) {
@@ -59,36 +59,45 @@ template <typename Id> __global__ void __launch_bounds__(kMaxThreads) count_kern
 }
 
 // 32 experts a block, a warp's lanes; the warps share the blocks' counts.
-__global__ void __launch_bounds__(kMaxThreads) prefix_kernel(SortArgs a, uint32_t blocks) {
+__global__ void __launch_bounds__(kMaxThreads) prefix_kernel(SortArgs a, Shares shares) {
     __shared__ int part[32][32];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
-    const uint32_t per = (blocks + 31) / 32, b0 = per * warp, b1 = b0 + per < blocks ? b0 + per : blocks;
-    int sum = 0;
-    if (e < a.experts) {
-#pragma unroll 4
-        for (uint32_t b = b0; b < b1; ++b) sum += a.position[share_start(a.slots, b, blocks) + e];
+    const uint32_t per = (shares.blocks + 31) / 32, b0 = per * warp, b1 = b0 + per < shares.blocks ? b0 + per : shares.blocks;
+    // Four counts in flight at a time; the last four are still there for the
+    // second walk, which is all of them up to 128 blocks.
+    constexpr int kAhead = 4;
+    int c[kAhead], sum = 0;
+    auto fetch = [&](uint32_t b) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            c[i] = b + i < b1 && e < a.experts ? a.position[shares.start(b + i) + e] : 0;
+    };
+    for (uint32_t b = b0; b < b1; b += kAhead) {
+        fetch(b);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) sum += c[i];
     }
     part[warp][lane] = sum;
     __syncthreads();
     if (warp == 0) {
-        int before = 0;
+        int all = 0;
 #pragma unroll
         for (int w = 0; w < 32; ++w) {
-            const int c = part[w][lane];
-            part[w][lane] = before;
-            before += c;
+            const int k = part[w][lane];
+            part[w][lane] = all;
+            all += k;
         }
-        if (e < a.experts) a.counts[e] = before;
+        if (e < a.experts) a.counts[e] = all;
     }
     __syncthreads();
-    if (e < a.experts) {
-        int before = part[warp][lane];
-        for (uint32_t b = b0; b < b1; ++b) {
-            int* at = a.position + share_start(a.slots, b, blocks) + e;
-            const int c = *at;
-            *at = before;
-            before += c;
+    int before = part[warp][lane];
+    for (uint32_t b = b0; b < b1; b += kAhead) {
+        if (per > kAhead) fetch(b);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (b + i < b1 && e < a.experts) a.position[shares.start(b + i) + e] = before;
+            before += c[i];
         }
     }
 }
@@ -96,7 +105,7 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_kernel(SortArgs a, uint32_
 // Places of one share of the slots; with kSingle the only one, which also
 // counts.
 template <typename Id, bool kSingle>
-__global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, int bits) {
+__global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, Shares shares, int bits) {
     extern __shared__ int smem[];
     const int warps = blockDim.x >> 5, E = a.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* hist = smem;                                 // [warps][E]: counts, then first places
@@ -109,7 +118,7 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, int bits
     pdl_wait();
 
     const Id* ids = static_cast<const Id*>(a.ids);
-    const uint32_t begin = share_start(a.slots, blockIdx.x, gridDim.x), end = share_start(a.slots, blockIdx.x + 1, gridDim.x);
+    const uint32_t begin = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
     const uint32_t rounds = (end - begin + blockDim.x - 1) / blockDim.x;
     const uint32_t first = begin + warp * rounds * 32 + lane;
     const unsigned below = (1u << lane) - 1;
@@ -142,10 +151,15 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, int bits
         int count = 0, before = 0;
         if (x < E) {
             int sum = 0;
-            for (int w = 0; w < warps; ++w) {
-                const int c = hist[w * E + x];
-                hist[w * E + x] = sum;
-                sum += c;
+            for (int w0 = 0; w0 < warps; w0 += 8) {   // eight at a time in flight
+                int c[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? hist[(w0 + w) * E + x] : 0;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    if (w0 + w < warps) hist[(w0 + w) * E + x] = sum;
+                    sum += c[w];
+                }
             }
             count = kSingle ? sum : a.counts[x];
             before = kSingle ? 0 : a.position[begin + x];
@@ -204,7 +218,7 @@ size_t smem_bytes(unsigned warps, int experts) {
     return (static_cast<size_t>(warps) * experts + 2 * static_cast<size_t>(experts) + 32) * sizeof(int);
 }
 
-template <typename Id, bool kSingle> cudaError_t place(const SortArgs& a, unsigned blocks, unsigned threads, cudaStream_t s) {
+template <typename Id, bool kSingle> cudaError_t place(const SortArgs& a, const Shares& shares, unsigned threads, cudaStream_t s) {
     // Shared memory above 48 KiB is allowed explicitly, once per device (only a
     // successful call is remembered).
     static std::atomic<bool> allowed[kDevices];
@@ -212,22 +226,23 @@ template <typename Id, bool kSingle> cudaError_t place(const SortArgs& a, unsign
     if (e != cudaSuccess) return e;
     int bits = 0;
     while (a.experts >> bits) ++bits;                 // of 0 .. experts
-    return launch_kernel_smem(place_kernel<Id, kSingle>, dim3(blocks), dim3(threads), smem_bytes(threads / 32, a.experts), s, a,
-                              bits);
+    return launch_kernel_smem(place_kernel<Id, kSingle>, dim3(shares.blocks), dim3(threads), smem_bytes(threads / 32, a.experts),
+                              s, a, shares, bits);
 }
 
 template <typename Id> cudaError_t sort(const SortArgs& a, cudaStream_t s) {
     if (a.slots < 2 * kTile) {
         unsigned threads = 64;
         while (threads < kMaxThreads && threads < a.slots) threads *= 2;
-        return place<Id, true>(a, 1, threads, s);
+        return place<Id, true>(a, {1, a.slots, 0}, threads, s);
     }
-    const unsigned blocks = a.slots / kTile;
-    cudaError_t e = launch_kernel(count_kernel<Id>, dim3(blocks), dim3(kMaxThreads), s, a);
+    const uint32_t blocks = a.slots / kTile;
+    const Shares shares = {blocks, a.slots / blocks, a.slots % blocks};
+    cudaError_t e = launch_kernel(count_kernel<Id>, dim3(blocks), dim3(kMaxThreads), s, a, shares);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(prefix_kernel, dim3((a.experts + 31) / 32), dim3(kMaxThreads), s, a, static_cast<uint32_t>(blocks));
+    e = launch_kernel(prefix_kernel, dim3((a.experts + 31) / 32), dim3(kMaxThreads), s, a, shares);
     if (e != cudaSuccess) return e;
-    return place<Id, false>(a, blocks, kMaxThreads, s);
+    return place<Id, false>(a, shares, kMaxThreads, s);
 }
 
 }  // namespace

@@ -243,12 +243,12 @@ template <int DT> cudaError_t forward_of(sar_dtype wdt, const NormArgs& a, cudaS
     return norm::forward<DT>(a, wdt == SAR_FP32, vec, s);
 }
 
-// Blocks of the register kernel: enough groups for the rows, at most what the
-// SMs hold at a time.
+// Blocks of the register kernel: groups with two rows or more, since each block
+// leaves a row of sums, at most what the SMs hold at a time.
 template <int DT> unsigned backward_blocks(size_t rows, size_t cols) {
     const int tpr = norm::backward_tpr((cols + Elem<DT>::kVE - 1) / Elem<DT>::kVE);
     const int groups = tpr > 512 ? 1 : 512 / tpr;
-    const size_t need = (rows + groups - 1) / groups, fit = tpr > 512 ? norm::kSMs : 2 * norm::kSMs;
+    const size_t need = (rows + 2 * groups - 1) / (2 * groups), fit = tpr > 512 ? norm::kSMs : 2 * norm::kSMs;
     return static_cast<unsigned>(need < fit ? need : fit);
 }
 

@@ -505,8 +505,8 @@ cudaError_t ring_launch(const Args& a, bool w32, size_t vecs, const Alignment& a
 // `vecs` places a row, at most kRingVecs.
 template <int DT, bool kShift> cudaError_t ring_any(const NormArgs& a, bool w32, size_t vecs, const Alignment& al, cudaStream_t s) {
     switch (ring_vectors(vecs)) {
-    case 1: return ring_launch<DT, 1, 2, 4, kShift>(a, w32, vecs, al, s);
-    case 2: return ring_launch<DT, 2, 2, 4, kShift>(a, w32, vecs, al, s);
+    case 1: return ring_launch<DT, 1, 2, 3, kShift>(a, w32, vecs, al, s);
+    case 2: return ring_launch<DT, 2, 2, 3, kShift>(a, w32, vecs, al, s);
     default: return ring_launch<DT, 4, 1, 6, kShift>(a, w32, vecs, al, s);
     }
 }
@@ -514,9 +514,9 @@ template <int DT, bool kShift> cudaError_t ring_any(const NormArgs& a, bool w32,
 template <int DT, bool kShift>
 cudaError_t ring_any(const NormGradArgs& a, bool w32, size_t vecs, const Alignment& al, cudaStream_t s) {
     switch (ring_vectors(vecs)) {
-    case 1: return ring_launch<DT, 1, 2, 3, kShift>(a, w32, vecs, al, s);
-    case 2: return ring_launch<DT, 2, 2, 3, kShift>(a, w32, vecs, al, s);
-    default: return ring_launch<DT, 4, 1, 3, kShift>(a, w32, vecs, al, s);
+    case 1: return ring_launch<DT, 1, 2, 2, kShift>(a, w32, vecs, al, s);
+    case 2: return ring_launch<DT, 2, 2, 2, kShift>(a, w32, vecs, al, s);
+    default: return ring_launch<DT, 4, 1, 2, kShift>(a, w32, vecs, al, s);
     }
 }
 

@@ -110,8 +110,8 @@ def test_backward(sar, shape, types):
 
 
 # Rows enough to stay in the blocks for long, at every split of a row over threads, whole and partly filled.
-MANY = [(305, 4096), (611, 4090), (330, 8192), (333, 5004), (320, 16384), (306, 12290), (613, 2048), (1217, 1024), (1300, 520),
-        (2434, 512), (2500, 300), (4870, 256), (5001, 132), (9730, 140), (20011, 64)]
+MANY = [(2500, 4096), (2443, 4090), (330, 8192), (333, 5004), (320, 16384), (306, 12290), (4900, 2048), (9800, 1024), (9740, 520),
+        (18300, 512), (18250, 300), (39000, 256), (38950, 132), (20011, 64), (6100, 1150), (305, 4096), (1217, 1024)]
 
 
 @pytest.mark.parametrize("types", TYPES, ids="/".join)
@@ -125,7 +125,7 @@ def test_many_rows(sar, shape, types):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("gap,offset", [(8, 8), (2, 4), (1, 0), (0, 1)])
-@pytest.mark.parametrize("shape", [(610, 1000), (620, 2048), (2440, 400)], ids=str)
+@pytest.mark.parametrize("shape", [(9740, 1000), (4870, 2048), (600, 9000), (18300, 400)], ids=str)
 def test_many_rows_strides_and_alignment(sar, shape, gap, offset, dtype):
     dt = ref.DTYPES[dtype]
     x, dy, w, b = inputs(*shape, dt, dt, seed=1)
@@ -133,7 +133,7 @@ def test_many_rows_strides_and_alignment(sar, shape, gap, offset, dtype):
     check_backward(sar, dy, x, w, dt, gap=gap, offset=offset)
 
 
-@pytest.mark.parametrize("shape", [(700, 4096), (1300, 1021)], ids=str)
+@pytest.mark.parametrize("shape", [(700, 4096), (5000, 1021), (320, 9001)], ids=str)
 def test_many_rows_without_parameters_in_place(sar, shape):
     """No weight or bias, statistics not wanted, y over x and dx over dy; a NaN row stays alone."""
     x, dy, _, _ = inputs(*shape, torch.float32, torch.float32, seed=2)
@@ -302,7 +302,7 @@ def test_gradient_against_differences(sar, cols):
         assert allowed < 0.05 * (abs(truth) + (exact.abs() * d.abs()).sum().item() ** 0.5)     # the check says something
 
 
-@pytest.mark.parametrize("shape", [(8, 4096), (515, 1024), (300, 1021), (70, 12000), (1500, 2048)], ids=str)
+@pytest.mark.parametrize("shape", [(8, 4096), (515, 1024), (300, 1021), (70, 12000), (4900, 2048), (5000, 1021)], ids=str)
 def test_same_bits_on_every_run_and_stream(sar, shape):
     x, dy, w, b = inputs(*shape, torch.bfloat16, torch.float32, seed=9)
     y, mean, rstd = forward(sar, x, w, b)

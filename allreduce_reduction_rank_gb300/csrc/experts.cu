@@ -24,12 +24,12 @@ template <int GB> __device__ __forceinline__ Granule<GB> load(const void* base, 
     const char* p = static_cast<const char*>(base) + byte;
     Granule<GB> g;
     if constexpr (GB == 16) {
-        const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
+        const uint4 v = ld_stream_ordered(reinterpret_cast<const uint4*>(p));
         g.w[0] = v.x, g.w[1] = v.y, g.w[2] = v.z, g.w[3] = v.w;
     } else if constexpr (GB == 8) {
-        asm("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(p));
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(p) : "memory");
     } else if constexpr (GB == 4) {
-        asm("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(g.w[0]) : "l"(p));
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(g.w[0]) : "l"(p) : "memory");
     } else if constexpr (GB == 2) {
         g.w[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
@@ -286,6 +286,202 @@ __global__ void __launch_bounds__(kBlock) combine_backward_kernel(ExpertArgs a, 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Rows that do not start alike.  Where the addresses allow granules of 4 bytes
+// or less (odd row lengths), the written row is taken in chunks of 16 bytes from
+// a 16-byte boundary, and the bytes read for one come from two aligned vectors
+// (the second is a neighbour lane's first, from L1) by funnel shifts.  The
+// vectors may hold bytes of the rows beside the one read, never bytes outside
+// the matrix: windows at its ends, and the chunks at a row's ends, go by
+// element.  Measured against granules (us): dispatch 8192 x 8 x 4097 bf16 117 /
+// 189, 16384 x 8 x 201 26 / 38; combine's gradient 326 / 388, 64 / 97.  The
+// combine itself did not gain (198 / 220 and 47 / 41) and stays with granules.
+// ---------------------------------------------------------------------------
+
+// A matrix that is read; rows start at base + i * pitch bytes.
+struct Source {
+    const char* base;
+    const char* end;             // one past its last element
+    size_t pitch;
+    __device__ __forceinline__ Source(const void* p, size_t rows, size_t ld, size_t cols, size_t es)
+        : base(static_cast<const char*>(p)), end(base + ((rows - 1) * ld + cols) * es), pitch(ld * es) {}
+};
+
+__device__ __forceinline__ uint4 ld_cached(const char* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+template <typename Unit> __device__ __noinline__ uint4 gather16(const char* at) {
+    constexpr int kPerWord = 4 / sizeof(Unit);
+    const Unit* u = reinterpret_cast<const Unit*>(at);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int k = 0; k < kPerWord; ++k) w[i] |= static_cast<uint32_t>(u[i * kPerWord + k]) << (8 * sizeof(Unit) * k);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The vectors around the 16 bytes at `at`, all of them in one row of `src`; at
+// the matrix's ends the bytes themselves.
+struct Window {
+    uint4 a, b;
+    unsigned shift;
+
+    template <typename Unit> __device__ __forceinline__ void load(const Source& src, const char* at) {
+        shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u;
+        const char* low = at - shift;
+        b = make_uint4(0, 0, 0, 0);
+        if (low >= src.base && low + (shift != 0 ? 32 : 16) <= src.end) {
+            a = ld_cached(low);
+            if (shift != 0) b = ld_cached(low + 16);
+        } else {
+            a = gather16<Unit>(at);
+            shift = 0;
+        }
+    }
+    __device__ __forceinline__ uint4 bytes() const {
+        uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (shift & 8u) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
+        }
+        if (shift & 4u) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) x[i] = x[i + 1];
+        }
+        const unsigned bits = (shift & 3u) * 8;
+        return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
+                          __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
+    }
+};
+
+__device__ __forceinline__ Granule<16> granule(const uint4& v) {
+    Granule<16> g;
+    g.w[0] = v.x, g.w[1] = v.y, g.w[2] = v.z, g.w[3] = v.w;
+    return g;
+}
+
+__device__ __forceinline__ unsigned phase_of(const void* p) {
+    return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) & 15u;
+}
+
+// Chunk u of a row written at `row` has the row's bytes u * 16 - phase ... + 15;
+// sh.granules counts chunks, which a row has whatever its phase.
+template <typename Unit>
+__global__ void __launch_bounds__(kBlock) dispatch_shift_kernel(ExpertArgs a, Shape sh) {
+    constexpr size_t es = sizeof(Unit);
+    pdl_wait();
+    if (blockIdx.x < sh.pad_blocks) {
+        Shape by_unit = sh;
+        by_unit.granules = static_cast<unsigned>(a.cols);
+        clear_padding<es>(a, by_unit, blockIdx.x, es);
+        return;
+    }
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    if (t >= a.tokens) return;
+    const Source src(a.tok, a.tokens, a.ldt, a.cols, es);
+    const char* from = src.base + t * src.pitch;
+    const long long bytes = static_cast<long long>(a.cols * es);
+    for (unsigned u = blockIdx.y * sh.tx + threadIdx.x % sh.tx; u < sh.granules; u += gridDim.y * sh.tx) {
+        for (int j = 0; j < a.topk; ++j) {
+            const int p = place_of(a, t, j);
+            if (p < 0) continue;
+            char* row = static_cast<char*>(a.out) + static_cast<size_t>(p) * a.ldo * es;
+            const long long at = static_cast<long long>(u) * 16 - phase_of(row);
+            if (at >= 0 && at + 16 <= bytes) {
+                Window w;
+                w.load<Unit>(src, from + at);
+                st_stream(reinterpret_cast<uint4*>(row + at), w.bytes());
+            } else {
+                for (long long i = at < 0 ? 0 : at; i < at + 16 && i < bytes; i += es)
+                    *reinterpret_cast<Unit*>(row + i) = *reinterpret_cast<const Unit*>(from + i);
+            }
+        }
+    }
+}
+
+// 16-bit elements; the rows read and written start alike (or none are read); dout
+// by windows.
+template <int DT, int WDT, int TX>
+__global__ void __launch_bounds__(kBlock) combine_backward_shift_kernel(ExpertArgs a, Shape sh) {
+    constexpr int N = Elements<DT, 16>::kN, W = TX / 32;
+    constexpr size_t es = Elem<DT>::kSize;
+    __shared__ float red[W > 1 ? W : 1];
+    pdl_wait();
+    if (blockIdx.x < sh.pad_blocks) {
+        Shape by_unit = sh;
+        by_unit.granules = static_cast<unsigned>(a.cols);
+        clear_padding<es>(a, by_unit, blockIdx.x, es);
+        return;
+    }
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / TX) + threadIdx.x / TX;
+    const unsigned x = threadIdx.x % TX;
+    if (t >= a.tokens) return;                        // whole warps; with W > 1 never
+    const Source src(a.tok, a.tokens, a.ldt, a.cols, es);
+    const char* from = src.base + t * src.pitch;
+    const long long bytes = static_cast<long long>(a.cols * es);
+    for (int j = blockIdx.y; j < a.topk; j += gridDim.y) {
+        const size_t slot = t * a.topk + j;
+        const int p = place_of(a, t, j);
+        float dot = 0.0f;
+        if (p >= 0) {
+            const float w = load_elem<WDT>(a.weights, slot);
+            char* to = static_cast<char*>(a.out) + static_cast<size_t>(p) * a.ldo * es;
+            const char* row = static_cast<const char*>(a.rows_in) + static_cast<size_t>(p) * a.ldi * es;
+            const unsigned phase = phase_of(to);
+#pragma unroll 2
+            for (unsigned u = x; u < sh.granules; u += TX) {
+                const long long at = static_cast<long long>(u) * 16 - phase;
+                if (at >= 0 && at + 16 <= bytes) {
+                    Window win;
+                    win.template load<uint16_t>(src, from + at);
+                    float y[N], d[N];
+                    if (a.dweights != nullptr) widen<DT, 16>(load<16>(row, static_cast<size_t>(at)), y);
+                    widen<DT, 16>(granule(win.bytes()), d);
+                    if (a.dweights != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) dot = __fmaf_rn(d[e], y[e], dot);
+                    }
+#pragma unroll
+                    for (int e = 0; e < N; ++e) d[e] = __fmul_rn(w, d[e]);
+                    store<16>(to, static_cast<size_t>(at), narrow<DT, 16>(d));
+                } else {
+                    for (int e = 0; e < N; ++e) {
+                        const long long i = at + e * static_cast<long long>(es);
+                        if (i < 0 || i >= bytes) continue;
+                        const float d = load_elem<DT>(from + i, 0);
+                        if (a.dweights != nullptr) dot = __fmaf_rn(d, load_elem<DT>(row + i, 0), dot);
+                        store_elem<DT>(to + i, 0, __fmul_rn(w, d));
+                    }
+                }
+            }
+        }
+        if (a.dweights == nullptr) continue;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xFFFFFFFFu, dot, k));
+        if (W == 1) {
+            if (x == 0) store_elem<WDT>(a.dweights, slot, dot);
+        } else {
+            if ((x & 31) == 0) red[x / 32] = dot;
+            __syncthreads();
+            if (x == 0) {
+                float s = red[0];
+                for (int k = 1; k < W; ++k) s = __fadd_rn(s, red[k]);
+                store_elem<WDT>(a.dweights, slot, s);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // Largest granule (16, 8, 4, 2 or 1 bytes) that divides every address, leading
 // dimension and the row's length.
 unsigned granule_of(std::initializer_list<const void*> ptrs, std::initializer_list<size_t> lds, size_t cols, size_t es) {
@@ -315,6 +511,19 @@ constexpr unsigned kSpread = 1216;
 unsigned row_shares(const Shape& sh) {
     const unsigned most = (sh.granules + sh.tx - 1) / sh.tx, want = kSpread / std::min(sh.token_blocks, kSpread);
     return std::max(1u, std::min(want, most));
+}
+
+// Rows by shifted windows: granules of 4 bytes or less, and rows long enough that
+// their ends, which go by element, do not matter.
+bool by_windows(unsigned granule, size_t row_bytes) { return granule <= 4 && row_bytes >= 256 && row_bytes < (1u << 30); }
+
+// Chunks of a row wherever it starts.
+size_t chunks(size_t row_bytes) { return row_bytes / 16 + 2; }
+
+template <typename Unit> cudaError_t dispatch_shift(const ExpertArgs& a, cudaStream_t s) {
+    const Shape sh = shape_of(a, chunks(a.cols * sizeof(Unit)), 8);
+    return launch_kernel(dispatch_shift_kernel<Unit>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(kBlock), s, a,
+                         sh);
 }
 
 template <int GB> cudaError_t dispatch(const ExpertArgs& a, size_t es, cudaStream_t s) {
@@ -361,10 +570,25 @@ template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArg
     return few ? backward<DT, WDT, GB, 256, 1>(a, s) : backward<DT, WDT, GB, 256, 4>(a, s);
 }
 
+template <int DT, int WDT, int TX> cudaError_t backward_shift(const ExpertArgs& a, cudaStream_t s) {
+    Shape sh = shape_of(a, chunks(a.cols * Elem<DT>::kSize), TX);
+    sh.tx = TX;
+    sh.token_blocks = static_cast<unsigned>((a.tokens + kBlock / TX - 1) / (kBlock / TX));
+    const dim3 grid(sh.pad_blocks + sh.token_blocks, a.tokens * a.topk <= kFewSlots ? a.topk : 1);
+    return launch_kernel(combine_backward_shift_kernel<DT, WDT, TX>, grid, dim3(kBlock), s, a, sh);
+}
+
 template <int DT, int WDT> cudaError_t backward_by_granule(const ExpertArgs& a, cudaStream_t s) {
     constexpr int es = Elem<DT>::kSize;
+    const bool alike = a.dweights == nullptr ||
+                       (((reinterpret_cast<uintptr_t>(a.rows_in) ^ reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0 &&
+                        (a.ldi * es - a.ldo * es) % 16 == 0);
     const unsigned g = a.dweights != nullptr ? granule_of({a.tok, a.rows_in, a.out}, {a.ldt, a.ldi, a.ldo}, a.cols, es)
                                              : granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es);
+    if constexpr (es == 2) {                          // 4-byte elements are no faster by windows (127 / 124 us)
+        if (alike && by_windows(g, a.cols * es))
+            return a.cols * es <= 2048 ? backward_shift<DT, WDT, 32>(a, s) : backward_shift<DT, WDT, 256>(a, s);
+    }
     if (g == 16) return backward_by_shape<DT, WDT, 16>(a, s);
     if (g == 8) return backward_by_shape<DT, WDT, 8>(a, s);
     return backward_by_shape<DT, WDT, es>(a, s);
@@ -373,7 +597,10 @@ template <int DT, int WDT> cudaError_t backward_by_granule(const ExpertArgs& a, 
 }  // namespace
 
 cudaError_t launch_expert_dispatch(size_t es, const ExpertArgs& a, cudaStream_t s) {
-    switch (granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es)) {
+    const unsigned g = granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es);
+    if (by_windows(g, a.cols * es))
+        return es == 1 ? dispatch_shift<uint8_t>(a, s) : (es == 2 ? dispatch_shift<uint16_t>(a, s) : dispatch_shift<uint32_t>(a, s));
+    switch (g) {
     case 16: return dispatch<16>(a, es, s);
     case 8: return dispatch<8>(a, es, s);
     case 4: return dispatch<4>(a, es, s);

@@ -30,7 +30,7 @@ template <int DT, bool kVec> struct Unit {
 
     static __device__ __forceinline__ void load(const void* base, size_t i, float (&f)[kN]) {
         if constexpr (kVec) {
-            const uint4 v = ld_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(base) + i * Elem<DT>::kSize));
+            const uint4 v = ld_stream_ordered(reinterpret_cast<const uint4*>(static_cast<const char*>(base) + i * Elem<DT>::kSize));
             constexpr int W = PerWord<DT>::kN;
             widen_word<DT>(v.x, f);
             widen_word<DT>(v.y, f + W);

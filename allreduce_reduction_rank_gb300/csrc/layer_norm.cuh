@@ -28,7 +28,7 @@ __device__ __forceinline__ void load_row(Raw<DT, NV>& r, const void* base, size_
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const unsigned k = i * TPR + t;
-            r.v[i] = k * VE < cols ? ld_stream(p + k) : make_uint4(0, 0, 0, 0);
+            r.v[i] = k * VE < cols ? ld_stream_ordered(p + k) : make_uint4(0, 0, 0, 0);
         }
     } else if (Elem<DT>::kSize == 4) {
         const uint32_t* p = static_cast<const uint32_t*>(base) + first;

@@ -41,32 +41,44 @@ template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.
 
 // A thread's place in its group's rows.
 template <int DT, bool kShift> struct Place {
-    static constexpr int VE = Elem<DT>::kVE;
+    static constexpr int VE = Elem<DT>::kVE, es = Elem<DT>::kSize;
     int t, tpr, shift, cols;
+    unsigned flags;              // of vector i, from bit 4 i: some of it is in the row, all is, it has the row's start, end
 
+    __device__ __forceinline__ Place(int t_, int tpr_, int shift_, int cols_, int vectors)
+        : t(t_), tpr(tpr_), shift(shift_), cols(cols_), flags(0) {
+        if (!kShift) return;
+        for (int i = 0; i < vectors; ++i) {
+            const int c = column(i);
+            const bool start = c < 0, end = c < cols && c + VE > cols;
+            flags |= ((c < cols ? 1u : 0u) | (c < cols && !start && !end ? 2u : 0u) | (start ? 4u : 0u) | (end ? 8u : 0u)) << (4 * i);
+        }
+    }
     // First column of vector i; element e of it is column + e.
     __device__ __forceinline__ int column(int i) const { return (i * tpr + t) * VE - (kShift ? shift : 0); }
     __device__ __forceinline__ bool has(int c) const { return c < cols && (!kShift || c >= 0); }
     // Some of the vector's elements are in the row; all are.
-    __device__ __forceinline__ bool some(int i) const { return column(i) < cols; }
-    __device__ __forceinline__ bool whole(int i) const {
-        return kShift ? column(i) >= 0 && column(i) + VE <= cols : column(i) < cols;
+    __device__ __forceinline__ bool some(int i) const {
+        return kShift ? (flags & (1u << (4 * i))) != 0 : column(i) < cols;
     }
+    __device__ __forceinline__ bool whole(int i) const {
+        return kShift ? (flags & (2u << (4 * i))) != 0 : column(i) < cols;
+    }
+    // Its byte in the row; a 16-byte boundary even where it is past the row.
+    __device__ __forceinline__ int byte(int i) const { return (i * tpr + t) * 16 - (kShift ? shift * es : 0); }
 };
 
-// Copies a thread's part of one row into its places.  `edge`: the first (1) or
-// last (2) row of the matrix.
+// Copies a thread's part of one row into its places.  `edge`: the matrix's first
+// row (4), whose start, or its last (8), whose end may have nothing beside it.
 template <int DT, int NV, int BT, bool kShift>
-__device__ __forceinline__ void copy_row(uint4* slots, const void* base, size_t first, const Place<DT, kShift>& at,
-                                         unsigned edge) {
+__device__ __forceinline__ void copy_row(uint4* slots, const char* row, const Place<DT, kShift>& at, unsigned edge) {
     constexpr int VE = Elem<DT>::kVE, es = Elem<DT>::kSize;
-    const char* row = static_cast<const char*>(base) + first * es;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         uint4* slot = slots + i * BT + threadIdx.x;
-        const int c = at.column(i);
-        if (kShift && at.some(i) && ((c < 0 && (edge & 1)) || (c + VE > at.cols && (edge & 2)))) {
-#pragma unroll
+        if (kShift && ((at.flags >> (4 * i)) & edge)) {
+            const int c = at.column(i);
+#pragma unroll 1
             for (int e = 0; e < VE; ++e) {
                 if (es == 2)
                     reinterpret_cast<uint16_t*>(slot)[e] = at.has(c + e) ? reinterpret_cast<const uint16_t*>(row)[c + e] : 0;
@@ -74,38 +86,70 @@ __device__ __forceinline__ void copy_row(uint4* slots, const void* base, size_t 
                     reinterpret_cast<uint32_t*>(slot)[e] = at.has(c + e) ? reinterpret_cast<const uint32_t*>(row)[c + e] : 0u;
             }
         } else {
-            copy_async(slot, row + (at.some(i) ? c * es : 0) - (kShift && !at.some(i) ? at.shift * es : 0), at.some(i));
+            copy_async(slot, row + (at.some(i) ? at.byte(i) : at.byte(0) - at.t * 16), at.some(i));
         }
     }
 }
 
-// Vector i of a row in pairs, zeros where it is past the row's ends.
-template <int DT, int BT, bool kShift>
-__device__ __forceinline__ void read_vec(const uint4* slots, int i, const Place<DT, kShift>& at, float2* x) {
-    widen<DT>(slots[i * BT + threadIdx.x], x);
-    if (kShift && !at.whole(i)) {
+// Which bits of vector i are in the row.
+template <int DT, bool kShift> __device__ __forceinline__ uint4 bits_of(int i, const Place<DT, kShift>& at) {
+    constexpr int N = PerWord<DT>::kN;
+    uint32_t w[4];
 #pragma unroll
-        for (int p = 0; p < Elem<DT>::kVE / 2; ++p) {
-            if (!at.has(at.column(i) + 2 * p)) x[p].x = 0.0f;
-            if (!at.has(at.column(i) + 2 * p + 1)) x[p].y = 0.0f;
-        }
+    for (int k = 0; k < 4; ++k) {
+        const int c = at.column(i) + k * N;
+        w[k] = at.has(c) ? (N == 2 ? 0xFFFFu : 0xFFFFFFFFu) : 0u;
+        if (N == 2 && at.has(c + 1)) w[k] |= 0xFFFF0000u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Vector i of a row in pairs, zeros where it is past the row's ends.  With one
+// vector a thread its bits are kept in registers, else worked out where needed.
+template <int DT, int NV, int BT, bool kShift>
+__device__ __forceinline__ void read_vec(const uint4* slots, int i, const Place<DT, kShift>& at, const uint4& bits, float2* x) {
+    uint4 v = slots[i * BT + threadIdx.x];
+    constexpr bool kAlways = NV == 1 && Elem<DT>::kVE == 8;        // cheaper than the branch
+    if (kShift && (kAlways || !at.whole(i))) {
+        const uint4 m = NV == 1 ? bits : bits_of<DT, kShift>(i, at);
+        v = make_uint4(v.x & m.x, v.y & m.y, v.z & m.z, v.w & m.w);
+    }
+    widen<DT>(v, x);
+}
+
+// Zeros in the pairs of vector i that are past the row's ends.
+template <int DT> __device__ __forceinline__ void clear_outside(const uint4& bits, float2* x) {
+    constexpr int P = Elem<DT>::kVE / 2;
+    const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const uint32_t lo = PerWord<DT>::kN == 2 ? static_cast<uint32_t>(static_cast<int32_t>(w[p % 4] << 16) >> 16) : w[2 * p % 4];
+        const uint32_t hi = PerWord<DT>::kN == 2 ? static_cast<uint32_t>(static_cast<int32_t>(w[p % 4]) >> 16) : w[(2 * p + 1) % 4];
+        x[p].x = __uint_as_float(__float_as_uint(x[p].x) & lo);
+        x[p].y = __uint_as_float(__float_as_uint(x[p].y) & hi);
     }
 }
 
 template <int DT, bool kShift>
-__device__ __forceinline__ void write_vec(void* base, size_t first, int i, const Place<DT, kShift>& at, const float2* x) {
+__device__ __forceinline__ void write_vec(char* row, int i, const Place<DT, kShift>& at, const float2* x) {
     constexpr int VE = Elem<DT>::kVE, N = PerWord<DT>::kN;
     float f[VE];
 #pragma unroll
     for (int p = 0; p < VE / 2; ++p) f[2 * p] = x[p].x, f[2 * p + 1] = x[p].y;
-    const int c = at.column(i);
     if (at.whole(i)) {
-        st_stream(reinterpret_cast<uint4*>(static_cast<char*>(base) + (first + c) * Elem<DT>::kSize),
+        st_stream(reinterpret_cast<uint4*>(row + at.byte(i)),
                   make_uint4(narrow_word<DT>(f), narrow_word<DT>(f + N), narrow_word<DT>(f + 2 * N), narrow_word<DT>(f + 3 * N)));
-    } else if (kShift && at.some(i)) {
+    } else if (kShift && at.some(i)) {                // words where they are whole
+        const int c = at.column(i);
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-            if (at.has(c + e)) store_elem<DT>(base, first + c + e, f[e]);
+        for (int k = 0; k < 4; ++k) {
+            char* to = row + (c + k * N) * Elem<DT>::kSize;
+            const bool first = at.has(c + k * N), last = at.has(c + k * N + N - 1);
+            const uint32_t word = narrow_word<DT>(f + k * N);
+            if (first && last) *reinterpret_cast<uint32_t*>(to) = word;
+            else if (first) *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(word);
+            else if (last) *reinterpret_cast<uint16_t*>(to + 2) = static_cast<uint16_t>(word >> 16);
+        }
     }
 }
 
@@ -152,6 +196,7 @@ template <int N> __device__ __forceinline__ float scatter_sum(float (&v)[N]) {
 // (A row here is longer than 240 bytes, so their number fits 32 bits.)
 struct Rows {
     unsigned residue, begin, end, period;
+    unsigned first, last;        // the i of the matrix's first and last row, where the residue has them
     __device__ __forceinline__ Rows(size_t all, unsigned id, unsigned groups, unsigned period_) : period(period_) {
         const unsigned rows = static_cast<unsigned>(all);
         residue = id % period;
@@ -159,8 +204,12 @@ struct Rows {
         const unsigned n = groups / period, g = id / period, per = mine / n, more = mine % n;
         begin = per * g + (g < more ? g : more);
         end = begin + per + (g < more ? 1 : 0);
+        first = residue == 0 ? 0 : 0xFFFFFFFFu;
+        last = (rows - 1) % period == residue ? (rows - 1) / period : 0xFFFFFFFFu;
     }
     __device__ __forceinline__ size_t row(unsigned i) const { return residue + static_cast<size_t>(i) * period; }
+    // Whether it is the matrix's first (4) or last (8) row.
+    __device__ __forceinline__ unsigned edge(unsigned i) const { return (i == first ? 4u : 0u) | (i == last ? 8u : 0u); }
 };
 
 template <int DT, int NV, int R, int D, bool kShift, int WPG>
@@ -175,18 +224,23 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
     const int g = __shfl_sync(0xFFFFFFFFu, threadIdx.x / (32 * wpg), 0);        // the same for a warp
     const float n = static_cast<float>(a.cols);
     const Rows rows(a.rows, blockIdx.x * G + g, gridDim.x * G, kShift ? al.period : 1);
-    const Place<DT, kShift> at = {static_cast<int>(threadIdx.x) - g * 32 * wpg, 32 * wpg,
-                                       static_cast<int>((al.start + rows.residue * al.step) % VE), static_cast<int>(a.cols)};
+    const Place<DT, kShift> at(static_cast<int>(threadIdx.x) - g * 32 * wpg, 32 * wpg,
+                                       static_cast<int>((al.start + rows.residue * al.step) % VE), static_cast<int>(a.cols), NV);
+    const uint4 bits = bits_of<DT, kShift>(0, at);
     pdl_wait();
-    unsigned ahead = rows.begin;                        // first row of the next batch to copy
+    // Rows are walked by pointers: the products would cost more than the copies.
+    constexpr size_t es = Elem<DT>::kSize;
+    const size_t pitch_x = rows.period * a.ldx * es, pitch_y = rows.period * a.ldy * es;
+    const char* next_x = static_cast<const char*>(a.x) + rows.row(rows.begin) * a.ldx * es;
+    char* now_y = static_cast<char*>(a.y) + rows.row(rows.begin) * a.ldy * es;
+    unsigned ahead = rows.begin;                      // first row of the next batch to copy
     int slot = 0;                                     // its place in the ring
     auto copy_batch = [&] {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (ahead + j >= rows.end) continue;
-            const size_t r = rows.row(ahead + j);
-            copy_row<DT, NV, BT, kShift>(ring + (slot * R + j) * NV * BT, a.x, r * a.ldx, at,
-                                          (r == 0 ? 1u : 0u) | (r + 1 == a.rows ? 2u : 0u));
+            copy_row<DT, NV, BT, kShift>(ring + (slot * R + j) * NV * BT, next_x, at, rows.edge(ahead + j));
+            next_x += pitch_x;
         }
         copy_commit();
         ahead += R;
@@ -220,7 +274,7 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float2 f[P];
-                read_vec<DT, BT, kShift>(from + j * NV * BT, i, at, f);
+                read_vec<DT, NV, BT, kShift>(from + j * NV * BT, i, at, bits, f);
 #pragma unroll
                 for (int p = 0; p < P; ++p) s2 = __fadd2_rn(s2, f[p]);
             }
@@ -239,13 +293,7 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
                 widen<DT>(from[(j * NV + i) * BT + threadIdx.x], f);
 #pragma unroll
                 for (int p = 0; p < P; ++p) f[p] = __fadd2_rn(f[p], pair(-m[j]));
-                if (!whole) {
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        if (!at.has(at.column(i) + 2 * p)) f[p].x = 0.0f;
-                        if (!at.has(at.column(i) + 2 * p + 1)) f[p].y = 0.0f;
-                    }
-                }
+                if (!whole) clear_outside<DT>(NV == 1 ? bits : bits_of<DT, kShift>(i, at), f);
 #pragma unroll
                 for (int p = 0; p < P; ++p) q2 = __ffma2_rn(f[p], f[p], q2);
             }
@@ -284,7 +332,6 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
             const float mj = __shfl_sync(0xFFFFFFFFu, mean, wpg == 1 ? j * L : j);
             const float rj = __shfl_sync(0xFFFFFFFFu, rstd, wpg == 1 ? j * L : j);
             if (r + j >= rows.end) continue;
-            const size_t row = rows.row(r + j);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float2 f[P];
@@ -292,9 +339,11 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     f[p] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[p], pair(-mj)), pair(rj)), w[i * P + p], b[i * P + p]);
-                write_vec<DT, kShift>(a.y, row * a.ldy, i, at, f);
+                write_vec<DT, kShift>(now_y, i, at, f);
             }
+            now_y += pitch_y;
             if (at.t == 0) {
+                const size_t row = rows.row(r + j);
                 if (a.mean != nullptr) a.mean[row] = mj;
                 if (a.rstd != nullptr) a.rstd[row] = rj;
             }
@@ -342,20 +391,26 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
     __shared__ float red[2][BT / 32][2 * R];
     const int g = __shfl_sync(0xFFFFFFFFu, threadIdx.x / (32 * wpg), 0);        // the same for a warp
     const Rows rows(a.rows, blockIdx.x * G + g, gridDim.x * G, kShift ? al.period : 1);
-    const Place<DT, kShift> at = {static_cast<int>(threadIdx.x) - g * 32 * wpg, 32 * wpg,
-                                       static_cast<int>((al.start + rows.residue * al.step) % VE), static_cast<int>(a.cols)};
+    const Place<DT, kShift> at(static_cast<int>(threadIdx.x) - g * 32 * wpg, 32 * wpg,
+                                       static_cast<int>((al.start + rows.residue * al.step) % VE), static_cast<int>(a.cols), NV);
+    const uint4 bits = bits_of<DT, kShift>(0, at);
     pdl_wait();
+    constexpr size_t es = Elem<DT>::kSize;
+    const size_t pitch_x = rows.period * a.ldx * es, pitch_dy = rows.period * a.lddy * es, pitch_dx = rows.period * a.lddx * es;
+    const char* next_x = static_cast<const char*>(a.x) + rows.row(rows.begin) * a.ldx * es;
+    const char* next_dy = static_cast<const char*>(a.dy) + rows.row(rows.begin) * a.lddy * es;
+    char* now_dx = static_cast<char*>(a.dx) + rows.row(rows.begin) * a.lddx * es;
     unsigned ahead = rows.begin;
     int slot = 0;
     auto copy_batch = [&] {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (ahead + j >= rows.end) continue;
-            const size_t r = rows.row(ahead + j);
-            const unsigned edge = (r == 0 ? 1u : 0u) | (r + 1 == a.rows ? 2u : 0u);
+            const unsigned edge = rows.edge(ahead + j);
             uint4* to = ring + (slot * R + j) * 2 * NV * BT;
-            copy_row<DT, NV, BT, kShift>(to, a.x, r * a.ldx, at, edge);
-            copy_row<DT, NV, BT, kShift>(to + NV * BT, a.dy, r * a.lddy, at, edge);
+            copy_row<DT, NV, BT, kShift>(to, next_x, at, edge);
+            copy_row<DT, NV, BT, kShift>(to + NV * BT, next_dy, at, edge);
+            next_x += pitch_x, next_dy += pitch_dy;
         }
         copy_commit();
         ahead += R;
@@ -368,12 +423,15 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
 #pragma unroll
     for (int p = 0; p < NV * P; ++p) dw[p] = db[p] = pair(0.0f);
     float mean[R], rstd[R];
+    const float* next_mean = a.mean + rows.row(rows.begin);
+    const float* next_rstd = a.rstd + rows.row(rows.begin);
     auto statistics = [&](unsigned r) {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            mean[j] = r + j < rows.end ? a.mean[rows.row(r + j)] : 0.0f;
-            rstd[j] = r + j < rows.end ? a.rstd[rows.row(r + j)] : 0.0f;
+            mean[j] = r + j < rows.end ? next_mean[j * rows.period] : 0.0f;
+            rstd[j] = r + j < rows.end ? next_rstd[j * rows.period] : 0.0f;
         }
+        next_mean += R * rows.period, next_rstd += R * rows.period;
     };
     statistics(rows.begin);
     int now = 0;
@@ -392,8 +450,8 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     float2 f[P], d[P];
-                    read_vec<DT, BT, kShift>(from + (j * 2) * NV * BT, i, at, f);
-                    read_vec<DT, BT, kShift>(from + (j * 2 + 1) * NV * BT, i, at, d);
+                    read_vec<DT, NV, BT, kShift>(from + (j * 2) * NV * BT, i, at, bits, f);
+                    read_vec<DT, NV, BT, kShift>(from + (j * 2 + 1) * NV * BT, i, at, bits, d);
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         const int c = i * P + p;
@@ -418,7 +476,6 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
             // dx = rstd g - rstd mean(g) - (x - mean) rstd^2 mean(g h)
             const float c0 = -__fmul_rn(rs[j], __fmul_rn(v[2 * j], inv_n));
             const float c1 = -__fmul_rn(__fmul_rn(rs[j], rs[j]), __fmul_rn(v[2 * j + 1], inv_n));
-            const size_t row = rows.row(r + j);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float2 f[P], d[P];
@@ -434,8 +491,9 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     f[p] = __ffma2_rn(__fmul2_rn(d[p], w[i * P + p]), pair(rs[j]), __ffma2_rn(f[p], pair(c1), pair(c0)));
-                write_vec<DT, kShift>(a.dx, row * a.lddx, i, at, f);
+                write_vec<DT, kShift>(now_dx, i, at, f);
             }
+            now_dx += pitch_dx;
         }
     }
     copy_wait<0>();

@@ -16,7 +16,10 @@
 // take their counts out again, writes the places.  Each place is written by one
 // thread and the only atomics add integers, so the order is that of the slots.
 //
-// Bound by latency: 65536 x 8 slots are 6 MB of traffic, 1 us of HBM time.
+// Bound by latency: 65536 x 8 slots of 256 experts are 6 MB of traffic, 1 us of
+// HBM time, and take 11.3 us (three launches of 2 us at the least; counts 3,
+// prefixes 2.5, places 6); 32 x 8 slots take 1.9 us, one launch.  One cluster of
+// 16 blocks for all of it took 57 us, tiles of 2048 and 6144 slots 15.4 and 15.5.
 #include "sar_device.cuh"
 #include "sar_internal.h"
 
@@ -25,6 +28,7 @@ namespace {
 
 constexpr unsigned kTile = 4096;                      // slots of one block, as many as 8191
 constexpr int kMaxThreads = 1024, kRounds = 8;        // 32-slot rounds of a warp
+static_assert(2 * kTile <= 1 << 13 && SAR_MAX_EXPERTS < 1 << 18, "an expert and a share's slot in one word");
 static_assert(kTile >= SAR_MAX_EXPERTS, "a share's counts fit its part of position[]");
 
 // Expert of a slot; `experts` for a dropped one.
@@ -111,7 +115,9 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, Shares s
     int* hist = smem;                                 // [warps][E]: counts, then first places
     int* start = hist + warps * E;                    // [E]: the segments' starts
     int* filled = start + E;                          // [E]: the ends of their slots
-    int* carry = filled + E;                          // [32]
+    int* local = filled + E;                          // [E]: the segments' starts among this block's slots
+    int* carry = local + E;                           // [2][32]
+    int* sorted = carry + 64;                         // [slots of a share]: expert and slot, sorted
     int* mine = hist + warp * E;
     for (int i = lane; i < E; i += 32) mine[i] = 0;
     __syncwarp();
@@ -145,12 +151,11 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, Shares s
     }
     __syncthreads();
     // Experts in tiles of the block's threads.
-    int done = 0;
+    int done = 0, mine_done = 0;
     for (int e0 = 0; e0 < E; e0 += blockDim.x) {
         const int x = e0 + threadIdx.x;
-        int count = 0, before = 0;
+        int count = 0, before = 0, sum = 0;
         if (x < E) {
-            int sum = 0;
             for (int w0 = 0; w0 < warps; w0 += 8) {   // eight at a time in flight
                 int c[8];
 #pragma unroll
@@ -164,28 +169,30 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, Shares s
             count = kSingle ? sum : a.counts[x];
             before = kSingle ? 0 : a.position[begin + x];
         }
+        // Running sums over the experts: of the padded counts, and of the block's own.
         const int padded = (count + a.align - 1) / a.align * a.align;
-        int up = padded;
+        int up = padded, own = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, up, d);
-            if (lane >= d) up += v;
+            const int v = __shfl_up_sync(0xFFFFFFFFu, up, d), w = __shfl_up_sync(0xFFFFFFFFu, own, d);
+            if (lane >= d) up += v, own += w;
         }
-        if (lane == 31) carry[warp] = up;
+        if (lane == 31) carry[warp] = up, carry[32 + warp] = own;
         __syncthreads();
-        int c = lane < warps ? carry[lane] : 0;       // the warps' sums: before this one, and all
-        const int all = __reduce_add_sync(0xFFFFFFFFu, c);
-        c = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? c : 0);
+        const int c = lane < warps ? carry[lane] : 0, k = lane < warps ? carry[32 + lane] : 0;
+        const int at = done + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? c : 0) + up - padded;
+        const int here = mine_done + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? k : 0) + own - sum;
+        done += __reduce_add_sync(0xFFFFFFFFu, c);
+        mine_done += __reduce_add_sync(0xFFFFFFFFu, k);
         if (x < E) {
-            const int at = done + c + up - padded;
             start[x] = at + before;
             filled[x] = at + count;
+            local[x] = here;
             if (blockIdx.x == 0) {
                 if (kSingle) a.counts[x] = count;
                 a.offsets[x] = at;
             }
         }
-        done += all;
         __syncthreads();
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = done;
@@ -193,10 +200,23 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, Shares s
     for (int u = 0; u < kRounds; ++u) {
         const uint32_t i = first + u * 32;
         if (static_cast<uint32_t>(u) >= rounds || i >= end) break;
-        int place = e[u] < E ? start[e[u]] + mine[e[u]] + rank[u] : -1;
-        if (static_cast<uint32_t>(place) >= a.capacity) place = -1;
-        a.position[i] = place;
-        if (place >= 0 && a.source != nullptr) a.source[place] = static_cast<int>(i);
+        int place = -1;
+        if (e[u] < E) {
+            const int nth = mine[e[u]] + rank[u];     // of the expert's slots in this share
+            place = start[e[u]] + nth;
+            sorted[local[e[u]] + nth] = e[u] << 13 | static_cast<int>(i - begin);
+        }
+        a.position[i] = static_cast<uint32_t>(place) < a.capacity ? place : -1;
+    }
+    if (a.source != nullptr) {
+        // In the order of the places, so that a warp's stores are runs and not 32
+        // sectors each (65536 x 8 slots: 12.0 -> 11.3 us for the sort).
+        __syncthreads();
+        for (int n = threadIdx.x; n < mine_done; n += blockDim.x) {
+            const int v = sorted[n], x = v >> 13;
+            const uint32_t place = static_cast<uint32_t>(start[x] + n - local[x]);
+            if (place < a.capacity) a.source[place] = static_cast<int>(begin + (v & 0x1FFF));
+        }
     }
     if (a.source != nullptr) {                        // places without a slot: padding, and past the segments
         const unsigned runs = gridDim.x * warps;
@@ -214,20 +234,20 @@ __global__ void __launch_bounds__(kMaxThreads) place_kernel(SortArgs a, Shares s
     }
 }
 
-size_t smem_bytes(unsigned warps, int experts) {
-    return (static_cast<size_t>(warps) * experts + 2 * static_cast<size_t>(experts) + 32) * sizeof(int);
+size_t smem_bytes(unsigned warps, int experts, uint32_t slots) {
+    return (static_cast<size_t>(warps) * experts + 3 * static_cast<size_t>(experts) + 64 + slots) * sizeof(int);
 }
 
 template <typename Id, bool kSingle> cudaError_t place(const SortArgs& a, const Shares& shares, unsigned threads, cudaStream_t s) {
     // Shared memory above 48 KiB is allowed explicitly, once per device (only a
     // successful call is remembered).
     static std::atomic<bool> allowed[kDevices];
-    const cudaError_t e = allow_smem(place_kernel<Id, kSingle>, smem_bytes(kMaxThreads / 32, SAR_MAX_EXPERTS), allowed);
+    const cudaError_t e = allow_smem(place_kernel<Id, kSingle>, smem_bytes(kMaxThreads / 32, SAR_MAX_EXPERTS, 2 * kTile), allowed);
     if (e != cudaSuccess) return e;
     int bits = 0;
     while (a.experts >> bits) ++bits;                 // of 0 .. experts
-    return launch_kernel_smem(place_kernel<Id, kSingle>, dim3(shares.blocks), dim3(threads), smem_bytes(threads / 32, a.experts),
-                              s, a, shares, bits);
+    return launch_kernel_smem(place_kernel<Id, kSingle>, dim3(shares.blocks), dim3(threads),
+                              smem_bytes(threads / 32, a.experts, shares.per + 1), s, a, shares, bits);
 }
 
 template <typename Id> cudaError_t sort(const SortArgs& a, cudaStream_t s) {

@@ -5,6 +5,12 @@
 // bound by HBM: whole rows move in granules of up to 16 bytes, a thread owns
 // one granule of a token's row at a time and has the topk rows' accesses (kJ at
 // a time) in flight together.  A token's own row is touched once.
+//
+// Measured (GB300, copy rate 6.78 TB/s), 16384 x 8 x 4096 bf16: dispatch 181 us
+// (98% of the copy rate: it scatters, so that x is read once, where gathering by
+// place would read each row topk times), combine 171 us (104%); combine's
+// gradient 8192 x 4 x 8192 fp16 176 us (101%).  Small: dispatch of 32 x 8 rows of
+// 2048 bf16 2.0 us, combine's gradient 512 x 2 x 1024 fp32 3.0 us.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -167,7 +173,9 @@ template <int DT, int GB> struct Sums {
 // out = sum of w * row over the kept slots.  The sum starts from -0, the exact
 // identity of the round-to-nearest add, so that one row is copied bit for bit.
 // kOne: at most kJ slots a token, whose places and weights are read once, and
-// rows within 2^32 granules of the first, so that a row's place is 32 bits.
+// rows within 2^32 granules of the first, so that a row's place is 32 bits (of
+// 16384 x 8 x 4096 bf16: 192 us -> 171).  Four blocks an SM (64 registers): three
+// take 178 us, five spill and take 193; four rows ahead instead of eight 182.
 template <int DT, int WDT, int GB, bool kOne>
 __global__ void __launch_bounds__(kBlock, 4) combine_kernel(ExpertArgs a, Shape sh) {
     using Offset = std::conditional_t<kOne, uint32_t, size_t>;          // in granules

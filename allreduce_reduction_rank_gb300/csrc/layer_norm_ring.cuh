@@ -11,6 +11,15 @@
 // the sums over the threads and a barrier, is shared by its rows: the sums of R
 // rows travel together, halving their number with each exchange between lanes.
 //
+// Measured (GB300, copy rate 6.78 TB/s): forward 16384 x 8192 bf16 84 us, 94% of
+// the copy rate, bound by HBM; backward 32768 x 4096 fp16 117 us without the
+// parameters' gradients (101%), 122.5 with; 8192 x 4096 37.2 us (80%: launches,
+// the ring's first fill and its last batch are 3 us and the parameters' sums 5).
+// Depth: backward D = 3 41.0 us, D = 2 38.8 (less to fill before the first row
+// and to work off after the last load); forward NV = 2 D = 2 90.1, 3 84.5, 6
+// 88.4.  R = 1 backward 41, and 128 registers with half the threads 42.  The loads
+// alone, from registers with one row ahead, took 61 us backward and 126 forward.
+//
 // Rows need not start on 16-byte boundaries (kShift): where the matrices of a
 // call do so alike, row r starts `shift` elements past a boundary, with a period
 // of 1, 2, 4 or 8 rows.  A group takes rows of one residue only, so its threads
@@ -18,6 +27,7 @@
 // vectors at a row's ends are copied whole, with bytes of the neighbouring row
 // or gap that are masked when they are read; only the first row's start and the
 // last row's end, where there may be no such bytes, are copied by element.
+// 32768 x 1021 fp32 backward 67 us (88%), 16384 x 1021 bf16 34 us (44%; 1024: 22).
 #pragma once
 
 #include "layer_norm.cuh"

@@ -108,7 +108,8 @@ constexpr unsigned kPadShares = 4;
 // Clears a share of the padding rows of a segment.
 template <int GB> __device__ void clear_padding(const ExpertArgs& a, const Shape& sh, unsigned block, size_t es) {
     const unsigned e = block / kPadShares;
-    const int64_t first = static_cast<int64_t>(a.offsets[e]) + a.counts[e], end = a.offsets[e + 1];
+    const int64_t from = static_cast<int64_t>(a.offsets[e]) + a.counts[e], end = a.offsets[e + 1];
+    const int64_t first = from < 0 ? 0 : from;        // stays in the matrix whatever the arrays hold
     const int64_t last = end < static_cast<int64_t>(a.capacity) ? end : static_cast<int64_t>(a.capacity);
     Granule<GB> zero = {};
     for (int64_t p = first + block % kPadShares; p < last; p += kPadShares)

@@ -451,7 +451,10 @@ SAR_API sar_status sar_fp8_convert(const void* src, sar_dtype src_dtype, void* d
  *    leading dimension ld* (elements from one row to the next) is at least
  *    `cols`.  Element offsets are 64-bit.  Rows that all start on 16-byte
  *    boundaries (base address and ld * element size) move as 16-byte vectors;
- *    other layouts run slower kernels with the same results to rounding.
+ *    other layouts run slower kernels with the same results to rounding.  The
+ *    kernels read whole 16-byte blocks that hold elements of a row, so bytes
+ *    between the rows may be read (never those before the first or after the
+ *    last); only elements of the matrix are written.
  *  - Elements are widened exactly to binary32; sums, statistics and products
  *    are held in binary32; every output element is rounded once.  Sums run in
  *    an order that depends on the sizes and the alignment only: no atomics, so

@@ -319,7 +319,7 @@ backward_kernel(NormGradArgs a, bool w32, float inv_n) {
     constexpr int VE = Elem<DT>::kVE, P = VE / 2, BT = BackwardShape<TPR>::kThreads, G = BT / TPR;
     constexpr int WPG = TPR > 32 ? TPR / 32 : 1;
     __shared__ float2 red[2][G][WPG];
-    extern __shared__ float sums[];                   // [G][TPR * VE], groups of at least a warp
+    extern __shared__ __align__(16) float sums[];                   // [G][TPR * VE], groups of at least a warp
     pdl_wait();
     const unsigned t = threadIdx.x % TPR, cols = static_cast<unsigned>(a.cols);
     const int g = threadIdx.x / TPR;
@@ -396,11 +396,18 @@ backward_kernel(NormGradArgs a, bool w32, float inv_n) {
     for (int half = 0; half < 2; ++half) {
         if (half == 1) __syncthreads();
         if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
+            if (kVec) {                               // four columns at a time: single ones would meet in the banks
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const unsigned c = kVec ? t * VE + e : e * TPR + t;
-                const float2 v = half == 0 ? dw[e / 2] : db[e / 2];
-                sums[slot * C + c] = e % 2 ? v.y : v.x;
+                for (int p = 0; p < P; p += 2) {
+                    const float2 u = half == 0 ? dw[p] : db[p], v = half == 0 ? dw[p + 1] : db[p + 1];
+                    *reinterpret_cast<float4*>(sums + slot * C + t * VE + 2 * p) = make_float4(u.x, u.y, v.x, v.y);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float2 v = half == 0 ? dw[e / 2] : db[e / 2];
+                    sums[slot * C + e * TPR + t] = e % 2 ? v.y : v.x;
+                }
             }
         }
         __syncthreads();

@@ -13,8 +13,8 @@
 //
 // Measured (GB300, copy rate 6.78 TB/s): forward 16384 x 8192 bf16 84 us, 94% of
 // the copy rate, bound by HBM; backward 32768 x 4096 fp16 117 us without the
-// parameters' gradients (101%), 122.5 with; 8192 x 4096 37.2 us (80%: launches,
-// the ring's first fill and its last batch are 3 us and the parameters' sums 5).
+// parameters' gradients (101%), 121.6 with; 8192 x 4096 36.0 us (82%: launches,
+// the ring's first fill and its last batch are 3 us and the parameters' sums 4).
 // Depth: backward D = 3 41.0 us, D = 2 38.8 (less to fill before the first row
 // and to work off after the last load); forward NV = 2 D = 2 90.1, 3 84.5, 6
 // 88.4.  R = 1 backward 41, and 128 registers with half the threads 42.  The loads
@@ -514,12 +514,23 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
     float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * cols;
     float* sums = reinterpret_cast<float*>(ring);     // [G][2][cols]
     __syncthreads();
+    if (kShift) {
 #pragma unroll
-    for (int e = 0; e < NV * VE; ++e) {
-        const int c = at.column(e / VE) + e % VE;
-        if (at.has(c)) {
-            sums[g * 2 * cols + c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
-            sums[(g * 2 + 1) * cols + c] = e % 2 ? db[e / 2].y : db[e / 2].x;
+        for (int e = 0; e < NV * VE; ++e) {
+            const int c = at.column(e / VE) + e % VE;
+            if (at.has(c)) {
+                sums[g * 2 * cols + c] = e % 2 ? dw[e / 2].y : dw[e / 2].x;
+                sums[(g * 2 + 1) * cols + c] = e % 2 ? db[e / 2].y : db[e / 2].x;
+            }
+        }
+    } else {                                          // four columns at a time: single ones would meet in the banks
+#pragma unroll
+        for (int p = 0; p < NV * P; p += 2) {
+            const int c = at.column(2 * p / VE) + 2 * p % VE;
+            if (at.some(2 * p / VE)) {
+                *reinterpret_cast<float4*>(sums + g * 2 * cols + c) = make_float4(dw[p].x, dw[p].y, dw[p + 1].x, dw[p + 1].y);
+                *reinterpret_cast<float4*>(sums + (g * 2 + 1) * cols + c) = make_float4(db[p].x, db[p].y, db[p + 1].x, db[p + 1].y);
+            }
         }
     }
     __syncthreads();

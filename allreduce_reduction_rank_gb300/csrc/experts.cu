@@ -113,7 +113,7 @@ template <int GB> __device__ void clear_padding(const ExpertArgs& a, const Shape
     const int64_t last = end < static_cast<int64_t>(a.capacity) ? end : static_cast<int64_t>(a.capacity);
     Granule<GB> zero = {};
     for (int64_t p = first + block % kPadShares; p < last; p += kPadShares)
-        for (unsigned v = blockIdx.y * kBlock + threadIdx.x; v < sh.granules; v += gridDim.y * kBlock)
+        for (unsigned v = blockIdx.y * blockDim.x + threadIdx.x; v < sh.granules; v += gridDim.y * blockDim.x)
             store<GB>(a.out, (static_cast<size_t>(p) * a.ldo) * es + static_cast<size_t>(v) * GB, zero);
 }
 
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kBlock) dispatch_kernel(ExpertArgs a, Shape sh
         clear_padding<GB>(a, sh, blockIdx.x, es);
         return;
     }
-    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (blockDim.x / sh.tx) + threadIdx.x / sh.tx;
     if (t >= a.tokens) return;
     const unsigned first = blockIdx.y * sh.tx + threadIdx.x % sh.tx, step = gridDim.y * sh.tx;
     for (int j0 = 0; j0 < a.topk; j0 += kJ) {
@@ -175,15 +175,17 @@ template <int DT, int GB> struct Sums {
 // identity of the round-to-nearest add, so that one row is copied bit for bit.
 // kOne: at most kJ slots a token, whose places and weights are read once, and
 // rows within 2^32 granules of the first, so that a row's place is 32 bits (of
-// 16384 x 8 x 4096 bf16: 192 us -> 171).  Four blocks an SM (64 registers): three
-// take 178 us, five spill and take 193; four rows ahead instead of eight 182.
+// 16384 x 8 x 4096 bf16: 192 us -> 171).  1024 threads an SM (64 registers): 768
+// take 178 us, 1280 spill and take 193; four rows ahead instead of eight 182.
+// Blocks of 128 leave less of the last round empty: 1003 x 6 x 1500 fp16 6.3 -> 5.0.
+constexpr int kCombineBlock = 128;
 template <int DT, int WDT, int GB, bool kOne>
-__global__ void __launch_bounds__(kBlock, 4) combine_kernel(ExpertArgs a, Shape sh) {
+__global__ void __launch_bounds__(kCombineBlock, 8) combine_kernel(ExpertArgs a, Shape sh) {
     using Offset = std::conditional_t<kOne, uint32_t, size_t>;          // in granules
     constexpr Offset kNone = static_cast<Offset>(-1);
     constexpr size_t es = Elem<DT>::kSize;
     pdl_wait();
-    const size_t t = static_cast<size_t>(blockIdx.x) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    const size_t t = static_cast<size_t>(blockIdx.x) * (blockDim.x / sh.tx) + threadIdx.x / sh.tx;
     if (t >= a.tokens) return;
     const unsigned first = blockIdx.y * sh.tx + threadIdx.x % sh.tx, step = gridDim.y * sh.tx;
     const bool weighted = a.weights != nullptr;
@@ -220,11 +222,14 @@ __global__ void __launch_bounds__(kBlock, 4) combine_kernel(ExpertArgs a, Shape 
     }
 }
 
+// A block of the backward kernels: a token's TX threads, or eight tokens' warps.
+template <int TX> constexpr int kTokenBlock = TX == 128 ? 128 : kBlock;
+
 // drows = w * dout, dweights = <dout, row>.  TX threads (whole warps) have a
 // token's row; gridDim.y shares the slots, J at a time.  The dot products are
 // summed over the threads in a fixed order.
 template <int DT, int WDT, int GB, int TX, int J>
-__global__ void __launch_bounds__(kBlock) combine_backward_kernel(ExpertArgs a, Shape sh) {
+__global__ void __launch_bounds__(kTokenBlock<TX>) combine_backward_kernel(ExpertArgs a, Shape sh) {
     constexpr int N = Elements<DT, GB>::kN, W = TX / 32;
     constexpr size_t es = Elem<DT>::kSize;
     __shared__ float red[W > 1 ? W : 1][J];
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kBlock) combine_backward_kernel(ExpertArgs a, 
         clear_padding<GB>(a, sh, blockIdx.x, es);
         return;
     }
-    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / TX) + threadIdx.x / TX;
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kTokenBlock<TX> / TX) + threadIdx.x / TX;
     const unsigned x = threadIdx.x % TX;
     if (t >= a.tokens) return;                        // whole warps; with W > 1 never
     for (int j0 = blockIdx.y * J; j0 < a.topk; j0 += gridDim.y * J) {
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kBlock) dispatch_shift_kernel(ExpertArgs a, Sh
         clear_padding<es>(a, by_unit, blockIdx.x, es);
         return;
     }
-    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / sh.tx) + threadIdx.x / sh.tx;
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (blockDim.x / sh.tx) + threadIdx.x / sh.tx;
     if (t >= a.tokens) return;
     const Source src(a.tok, a.tokens, a.ldt, a.cols, es);
     const char* from = src.base + t * src.pitch;
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kBlock) dispatch_shift_kernel(ExpertArgs a, Sh
 // 16-bit elements; the rows read and written start alike (or none are read); dout
 // by windows.
 template <int DT, int WDT, int TX>
-__global__ void __launch_bounds__(kBlock) combine_backward_shift_kernel(ExpertArgs a, Shape sh) {
+__global__ void __launch_bounds__(kTokenBlock<TX>) combine_backward_shift_kernel(ExpertArgs a, Shape sh) {
     constexpr int N = Elements<DT, 16>::kN, W = TX / 32;
     constexpr size_t es = Elem<DT>::kSize;
     __shared__ float red[W > 1 ? W : 1];
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kBlock) combine_backward_shift_kernel(ExpertAr
         clear_padding<es>(a, by_unit, blockIdx.x, es);
         return;
     }
-    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kBlock / TX) + threadIdx.x / TX;
+    const size_t t = static_cast<size_t>(blockIdx.x - sh.pad_blocks) * (kTokenBlock<TX> / TX) + threadIdx.x / TX;
     const unsigned x = threadIdx.x % TX;
     if (t >= a.tokens) return;                        // whole warps; with W > 1 never
     const Source src(a.tok, a.tokens, a.ldt, a.cols, es);
@@ -502,13 +507,13 @@ unsigned granule_of(std::initializer_list<const void*> ptrs, std::initializer_li
     return g;
 }
 
-// Threads per row: a power of two that covers the row's granules, up to kBlock.
-Shape shape_of(const ExpertArgs& a, size_t granules, unsigned least) {
+// Threads per row: a power of two that covers the row's granules, up to the block.
+Shape shape_of(const ExpertArgs& a, size_t granules, unsigned least, unsigned block) {
     Shape sh;
     sh.tx = least;
-    while (sh.tx < kBlock && sh.tx < granules) sh.tx *= 2;
+    while (sh.tx < block && sh.tx < granules) sh.tx *= 2;
     sh.granules = static_cast<unsigned>(granules);
-    const size_t per = kBlock / sh.tx;
+    const size_t per = block / sh.tx;
     sh.token_blocks = static_cast<unsigned>((a.tokens + per - 1) / per);
     sh.pad_blocks = a.counts != nullptr ? kPadShares * a.experts : 0;
     return sh;
@@ -529,21 +534,27 @@ bool by_windows(unsigned granule, size_t row_bytes) { return granule <= 4 && row
 // Chunks of a row wherever it starts.
 size_t chunks(size_t row_bytes) { return row_bytes / 16 + 2; }
 
+// Threads of a dispatch block: 128 for few tokens (32 x 8 x 2048 bf16 1.9 us, 2.05
+// with 256), else 256 (16384 x 8 x 4096 181 us, 184 with 128).
+unsigned dispatch_block(const ExpertArgs& a) { return a.tokens <= 608 ? 128 : kBlock; }
+
 template <typename Unit> cudaError_t dispatch_shift(const ExpertArgs& a, cudaStream_t s) {
-    const Shape sh = shape_of(a, chunks(a.cols * sizeof(Unit)), 8);
-    return launch_kernel(dispatch_shift_kernel<Unit>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(kBlock), s, a,
+    const unsigned block = dispatch_block(a);
+    const Shape sh = shape_of(a, chunks(a.cols * sizeof(Unit)), 8, block);
+    return launch_kernel(dispatch_shift_kernel<Unit>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(block), s, a,
                          sh);
 }
 
 template <int GB> cudaError_t dispatch(const ExpertArgs& a, size_t es, cudaStream_t s) {
-    const Shape sh = shape_of(a, a.cols * es / GB, 8);
-    return launch_kernel(dispatch_kernel<GB>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(kBlock), s, a, sh,
+    const unsigned block = dispatch_block(a);
+    const Shape sh = shape_of(a, a.cols * es / GB, 8, block);
+    return launch_kernel(dispatch_kernel<GB>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(block), s, a, sh,
                          static_cast<unsigned>(es));
 }
 
 template <int DT, int WDT, int GB> cudaError_t combine(const ExpertArgs& a, cudaStream_t s) {
-    const Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, 8);
-    const dim3 grid(sh.token_blocks, row_shares(sh)), block(kBlock);
+    const Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, 8, kCombineBlock);
+    const dim3 grid(sh.token_blocks, row_shares(sh)), block(kCombineBlock);
     const size_t ld = a.ldi * Elem<DT>::kSize / GB;
     const bool near = a.capacity == 0 || ld < 0xFFFFFFFFu / a.capacity;       // a place and the row after it
     return a.topk <= kJ && near
@@ -564,27 +575,30 @@ template <int DT, int WDT> cudaError_t combine_by_granule(const ExpertArgs& a, c
 constexpr size_t kFewSlots = 2432;
 
 template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const ExpertArgs& a, cudaStream_t s) {
-    Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, TX);
+    constexpr int block = kTokenBlock<TX>;
+    Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, TX, block);
     sh.tx = TX;
-    sh.token_blocks = static_cast<unsigned>((a.tokens + kBlock / TX - 1) / (kBlock / TX));
+    sh.token_blocks = static_cast<unsigned>((a.tokens + block / TX - 1) / (block / TX));
     const dim3 grid(sh.pad_blocks + sh.token_blocks, std::min((a.topk + J - 1) / J, 65535));
-    return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(kBlock), s, a, sh);
+    return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(block), s, a, sh);
 }
 
 template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArgs& a, cudaStream_t s) {
     const bool narrow_rows = a.cols * Elem<DT>::kSize / GB <= 128;
-    // Few tokens: a block for each slot.
+    // Few tokens: a block for each slot (512 x 2 x 1024 fp32: 2.7 us; 3.0 with 256
+    // threads, 8.1 with all slots of a token in one block).
     const bool few = a.tokens * a.topk <= kFewSlots;
     if (narrow_rows) return few ? backward<DT, WDT, GB, 32, 1>(a, s) : backward<DT, WDT, GB, 32, 4>(a, s);
-    return few ? backward<DT, WDT, GB, 256, 1>(a, s) : backward<DT, WDT, GB, 256, 4>(a, s);
+    return few ? backward<DT, WDT, GB, 128, 1>(a, s) : backward<DT, WDT, GB, 256, 4>(a, s);
 }
 
 template <int DT, int WDT, int TX> cudaError_t backward_shift(const ExpertArgs& a, cudaStream_t s) {
-    Shape sh = shape_of(a, chunks(a.cols * Elem<DT>::kSize), TX);
+    constexpr int block = kTokenBlock<TX>;
+    Shape sh = shape_of(a, chunks(a.cols * Elem<DT>::kSize), TX, block);
     sh.tx = TX;
-    sh.token_blocks = static_cast<unsigned>((a.tokens + kBlock / TX - 1) / (kBlock / TX));
+    sh.token_blocks = static_cast<unsigned>((a.tokens + block / TX - 1) / (block / TX));
     const dim3 grid(sh.pad_blocks + sh.token_blocks, a.tokens * a.topk <= kFewSlots ? a.topk : 1);
-    return launch_kernel(combine_backward_shift_kernel<DT, WDT, TX>, grid, dim3(kBlock), s, a, sh);
+    return launch_kernel(combine_backward_shift_kernel<DT, WDT, TX>, grid, dim3(block), s, a, sh);
 }
 
 template <int DT, int WDT> cudaError_t backward_by_granule(const ExpertArgs& a, cudaStream_t s) {

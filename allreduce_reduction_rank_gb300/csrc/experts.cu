@@ -201,24 +201,36 @@ __global__ void __launch_bounds__(kCombineBlock, 8) combine_kernel(ExpertArgs a,
         }
     };
     if (kOne) slots_from(0);
-    for (unsigned v = first; v < sh.granules; v += step) {
-        Sums<DT, GB> sum;
-        sum.clear();
+    // Small granules take two places at a time, for as many bytes in flight
+    // (8192 x 8 x 4097 bf16 226 -> 144 us, 4098 111 -> 102; four spill).
+    constexpr int kPlaces = kOne && GB <= 4 ? 2 : 1;
+    for (unsigned v = first; v < sh.granules; v += kPlaces * step) {
+        Sums<DT, GB> sum[kPlaces];
+#pragma unroll
+        for (int i = 0; i < kPlaces; ++i) sum[i].clear();
         bool any = false;
         for (int j0 = 0; j0 < (kOne ? 1 : a.topk); j0 += kJ) {
             if (!kOne) slots_from(j0);
-            Granule<GB> g[kJ];
+            Granule<GB> g[kPlaces][kJ];
 #pragma unroll
-            for (int j = 0; j < kJ; ++j)
-                if (row[j] != kNone) g[j] = load<GB>(a.rows_in, static_cast<size_t>(static_cast<Offset>(row[j] + v)) * GB);
+            for (int i = 0; i < kPlaces; ++i)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+                    if (row[j] != kNone && (i == 0 || v + i * step < sh.granules))
+                        g[i][j] = load<GB>(a.rows_in, static_cast<size_t>(static_cast<Offset>(row[j] + v + i * step)) * GB);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
                 if (row[j] == kNone) continue;
                 any = true;
-                sum.add(g[j], w[j], weighted);
+#pragma unroll
+                for (int i = 0; i < kPlaces; ++i)
+                    if (i == 0 || v + i * step < sh.granules) sum[i].add(g[i][j], w[j], weighted);
             }
         }
-        store<GB>(a.out, t * a.ldo * es + static_cast<size_t>(v) * GB, sum.rounded(any));
+#pragma unroll
+        for (int i = 0; i < kPlaces; ++i)
+            if (i == 0 || v + i * step < sh.granules)
+                store<GB>(a.out, t * a.ldo * es + static_cast<size_t>(v + i * step) * GB, sum[i].rounded(any));
     }
 }
 
@@ -309,7 +321,7 @@ __global__ void __launch_bounds__(kTokenBlock<TX>) combine_backward_kernel(Exper
 // the matrix: windows at its ends, and the chunks at a row's ends, go by
 // element.  Measured against granules (us): dispatch 8192 x 8 x 4097 bf16 117 /
 // 189, 16384 x 8 x 201 26 / 38; combine's gradient 326 / 388, 64 / 97.  The
-// combine itself did not gain (198 / 220 and 47 / 41) and stays with granules.
+// combine itself did not gain (198 / 144 and 47 / 28) and stays with granules.
 // ---------------------------------------------------------------------------
 
 // A matrix that is read; rows start at base + i * pitch bytes.

@@ -532,16 +532,22 @@ Shape shape_of(const ExpertArgs& a, size_t granules, unsigned least, unsigned bl
 }
 
 // Blocks (y) that share a token's row, one granule a thread, while the grid stays
-// within kSpread blocks.
+// within kSpread blocks.  Combine, bf16 (us, kSpread 304 / 1216 / 4864): 300 x 4 x
+// 4096 3.6 / 3.1 / 3.1, 600 x 4 x 4096 4.3 / 4.1 / 4.8, 1200 x 4 x 4096 7.1 / 7.2 / 9.1.
 constexpr unsigned kSpread = 1216;
 unsigned row_shares(const Shape& sh) {
     const unsigned most = (sh.granules + sh.tx - 1) / sh.tx, want = kSpread / std::min(sh.token_blocks, kSpread);
     return std::max(1u, std::min(want, most));
 }
 
-// Rows by shifted windows: granules of 4 bytes or less, and rows long enough that
-// their ends, which go by element, do not matter.
-bool by_windows(unsigned granule, size_t row_bytes) { return granule <= 4 && row_bytes >= 256 && row_bytes < (1u << 30); }
+// Rows by shifted windows: granules of 2 bytes or less from `least` bytes a row
+// on, of 4 bytes from `least4` on (the rows' ends go by element).  Dispatch, us,
+// windows / granules: 8192 x 8 rows of 131 bf16 14.7 / 16.4, 251 18.5 / 18.9; 4
+// bytes: 130 bf16 13.9 / 10.4, 250 17.7 / 12.8, 151 fp32 20 / 20, 4098 bf16 116 /
+// 140.  Combine's gradient: 130 bf16 29.8 / 38.6, 4098 322 / 387.
+bool by_windows(unsigned granule, size_t row_bytes, size_t least, size_t least4) {
+    return granule <= 4 && row_bytes >= (granule == 4 ? least4 : least);
+}
 
 // Chunks of a row wherever it starts.
 size_t chunks(size_t row_bytes) { return row_bytes / 16 + 2; }
@@ -583,8 +589,12 @@ template <int DT, int WDT> cudaError_t combine_by_granule(const ExpertArgs& a, c
     return combine<DT, WDT, es>(a, s);
 }
 
-// Slots up to which the backward call has a block for each.
-constexpr size_t kFewSlots = 2432;
+// Whether the backward call has a block for each slot (else for four of a
+// token's): while all threads are on the SMs together, about.  Measured (us, so /
+// not): 512 x 2 x 1024 fp32 2.7 / 3.4, 600 x 4 x 1024 bf16 3.2 / 4.1, 1200 x 4 x
+// 1024 4.0 / 4.3, 512 x 8 x 2048 7.0 / 6.4; longer rows 4 x 8 x 4096 2.7 / 2.9, 64
+// x 8 x 4096 3.3 / 3.1, 600 x 4 x 4096 7.8 / 5.5.
+bool slot_blocks(size_t slots, size_t granules) { return granules <= 256 ? slots * granules <= 640000 : slots <= 64; }
 
 template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const ExpertArgs& a, cudaStream_t s) {
     constexpr int block = kTokenBlock<TX>;
@@ -595,13 +605,17 @@ template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const Exp
     return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(block), s, a, sh);
 }
 
+// A warp has a token's row up to 128 granules, and up to 511 where a block would
+// have idle threads (us, warp / block: 8192 x 8 x 600 fp32, 150 granules, 58 / 78;
+// 8192 x 8 x 1000 fp32, 250, 94 / 102; 4096 x 8 x 1500 bf16, 375, 42 / 49; 4096 x
+// 8 x 2048 bf16, 256, 51 / 48).
 template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArgs& a, cudaStream_t s) {
-    const bool narrow_rows = a.cols * Elem<DT>::kSize / GB <= 128;
-    // Few tokens: a block for each slot (512 x 2 x 1024 fp32: 2.7 us; 3.0 with 256
-    // threads, 8.1 with all slots of a token in one block).
-    const bool few = a.tokens * a.topk <= kFewSlots;
-    if (narrow_rows) return few ? backward<DT, WDT, GB, 32, 1>(a, s) : backward<DT, WDT, GB, 32, 4>(a, s);
-    return few ? backward<DT, WDT, GB, 128, 1>(a, s) : backward<DT, WDT, GB, 256, 4>(a, s);
+    const size_t granules = a.cols * Elem<DT>::kSize / GB;
+    const bool few = slot_blocks(a.tokens * a.topk, granules);
+    if (granules <= 128 && few) return backward<DT, WDT, GB, 32, 1>(a, s);
+    if (few) return backward<DT, WDT, GB, 128, 1>(a, s);
+    if (granules <= 128 || (granules < 512 && granules != 256)) return backward<DT, WDT, GB, 32, 4>(a, s);
+    return backward<DT, WDT, GB, 256, 4>(a, s);
 }
 
 template <int DT, int WDT, int TX> cudaError_t backward_shift(const ExpertArgs& a, cudaStream_t s) {
@@ -609,7 +623,7 @@ template <int DT, int WDT, int TX> cudaError_t backward_shift(const ExpertArgs& 
     Shape sh = shape_of(a, chunks(a.cols * Elem<DT>::kSize), TX, block);
     sh.tx = TX;
     sh.token_blocks = static_cast<unsigned>((a.tokens + block / TX - 1) / (block / TX));
-    const dim3 grid(sh.pad_blocks + sh.token_blocks, a.tokens * a.topk <= kFewSlots ? a.topk : 1);
+    const dim3 grid(sh.pad_blocks + sh.token_blocks, slot_blocks(a.tokens * a.topk, sh.granules) ? std::min(a.topk, 65535) : 1);
     return launch_kernel(combine_backward_shift_kernel<DT, WDT, TX>, grid, dim3(block), s, a, sh);
 }
 
@@ -621,7 +635,7 @@ template <int DT, int WDT> cudaError_t backward_by_granule(const ExpertArgs& a, 
     const unsigned g = a.dweights != nullptr ? granule_of({a.tok, a.rows_in, a.out}, {a.ldt, a.ldi, a.ldo}, a.cols, es)
                                              : granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es);
     if constexpr (es == 2) {                          // 4-byte elements are no faster by windows (127 / 124 us)
-        if (alike && by_windows(g, a.cols * es))
+        if (alike && by_windows(g, a.cols * es, 256, 256))
             return a.cols * es <= 2048 ? backward_shift<DT, WDT, 32>(a, s) : backward_shift<DT, WDT, 256>(a, s);
     }
     if (g == 16) return backward_by_shape<DT, WDT, 16>(a, s);
@@ -633,7 +647,7 @@ template <int DT, int WDT> cudaError_t backward_by_granule(const ExpertArgs& a, 
 
 cudaError_t launch_expert_dispatch(size_t es, const ExpertArgs& a, cudaStream_t s) {
     const unsigned g = granule_of({a.tok, a.out}, {a.ldt, a.ldo}, a.cols, es);
-    if (by_windows(g, a.cols * es))
+    if (by_windows(g, a.cols * es, 256, 1024))
         return es == 1 ? dispatch_shift<uint8_t>(a, s) : (es == 2 ? dispatch_shift<uint16_t>(a, s) : dispatch_shift<uint32_t>(a, s));
     switch (g) {
     case 16: return dispatch<16>(a, es, s);

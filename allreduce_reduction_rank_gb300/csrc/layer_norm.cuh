@@ -468,17 +468,23 @@ cudaError_t backward_launch(const NormGradArgs& a, bool w32, bool vec, unsigned 
                : launch_kernel_smem(backward_kernel<DT, TPR, false>, dim3(blocks), dim3(BT), smem, s, a, w32, inv_n);
 }
 
-// Rows up to which a call is a matter of latency: one vector a thread.
-constexpr size_t kFewRows = 2 * kSMs;
+// Threads up to which one vector a thread, with its parameters loaded at once, is
+// faster: while all rows are on the SMs together.  Measured (us, so / several
+// vectors a thread): 8 x 4096 bf16 1.9 / 2.5, 300 x 4096 2.5 / 2.9, 600 x 4096
+// 4.2 / 3.3, 1000 x 1024 2.3 / 2.9, 300 x 8192 4.6 / 3.75.
+constexpr size_t kEarlyThreads = static_cast<size_t>(kSMs) * 1024;
 
 // Definitions for one element type (layer_norm_<type>.cu).
 template <int DT> cudaError_t forward_any(const NormArgs& a, bool w32, bool vec, cudaStream_t s) {
     const size_t vecs = (a.cols + Elem<DT>::kVE - 1) / Elem<DT>::kVE;
-    if (a.rows <= kFewRows && vecs > 32 && vecs <= 1024) {
-        if (vecs <= 128) return forward_launch<DT, 128, 1, true>(a, w32, vec, s);
-        if (vecs <= 256) return forward_launch<DT, 256, 1, true>(a, w32, vec, s);
-        if (vecs <= 512) return forward_launch<DT, 512, 1, true>(a, w32, vec, s);
-        return forward_launch<DT, 1024, 1, true>(a, w32, vec, s);
+    if (vecs > 32 && vecs <= 1024) {
+        const size_t tpr = vecs <= 128 ? 128 : (vecs <= 256 ? 256 : (vecs <= 512 ? 512 : 1024));
+        if (a.rows * tpr <= kEarlyThreads) {
+            if (tpr == 128) return forward_launch<DT, 128, 1, true>(a, w32, vec, s);
+            if (tpr == 256) return forward_launch<DT, 256, 1, true>(a, w32, vec, s);
+            if (tpr == 512) return forward_launch<DT, 512, 1, true>(a, w32, vec, s);
+            return forward_launch<DT, 1024, 1, true>(a, w32, vec, s);
+        }
     }
     if (vecs <= 8) return forward_launch<DT, 8, 1>(a, w32, vec, s);
     if (vecs <= 32) return forward_launch<DT, 32, 1>(a, w32, vec, s);

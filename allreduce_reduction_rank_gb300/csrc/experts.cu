@@ -519,11 +519,17 @@ unsigned granule_of(std::initializer_list<const void*> ptrs, std::initializer_li
     return g;
 }
 
-// Threads per row: a power of two that covers the row's granules, up to the block.
-Shape shape_of(const ExpertArgs& a, size_t granules, unsigned least, unsigned block) {
+// Threads per row: a power of two that covers the row's granules, up to the block;
+// with `fit` a smaller one where that leaves less than 7/8 of the places (granules
+// below 16 bytes, which are not bound by HBM: dispatch 8192 x 8 x 151 fp32 21.3 ->
+// 13.5 us, 4096 x 8 x 1500 bf16 24.0 -> 22.3, but 600 fp32, 16 bytes, 28.6 -> 33.4).
+Shape shape_of(const ExpertArgs& a, size_t granules, unsigned least, unsigned block, bool fit) {
     Shape sh;
     sh.tx = least;
     while (sh.tx < block && sh.tx < granules) sh.tx *= 2;
+    const auto places = [&](size_t tx) { return (granules + tx - 1) / tx * tx; };
+    for (unsigned tx = sh.tx / 2; fit && tx >= 32 && tx >= least; tx /= 2)
+        if (8 * places(tx) < 7 * places(sh.tx)) sh.tx = tx;
     sh.granules = static_cast<unsigned>(granules);
     const size_t per = block / sh.tx;
     sh.token_blocks = static_cast<unsigned>((a.tokens + per - 1) / per);
@@ -558,20 +564,20 @@ unsigned dispatch_block(const ExpertArgs& a) { return a.tokens <= 608 ? 128 : kB
 
 template <typename Unit> cudaError_t dispatch_shift(const ExpertArgs& a, cudaStream_t s) {
     const unsigned block = dispatch_block(a);
-    const Shape sh = shape_of(a, chunks(a.cols * sizeof(Unit)), 8, block);
+    const Shape sh = shape_of(a, chunks(a.cols * sizeof(Unit)), 8, block, false);
     return launch_kernel(dispatch_shift_kernel<Unit>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(block), s, a,
                          sh);
 }
 
 template <int GB> cudaError_t dispatch(const ExpertArgs& a, size_t es, cudaStream_t s) {
     const unsigned block = dispatch_block(a);
-    const Shape sh = shape_of(a, a.cols * es / GB, 8, block);
+    const Shape sh = shape_of(a, a.cols * es / GB, 8, block, GB < 16);
     return launch_kernel(dispatch_kernel<GB>, dim3(sh.pad_blocks + sh.token_blocks, row_shares(sh)), dim3(block), s, a, sh,
                          static_cast<unsigned>(es));
 }
 
 template <int DT, int WDT, int GB> cudaError_t combine(const ExpertArgs& a, cudaStream_t s) {
-    const Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, 8, kCombineBlock);
+    const Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, 8, kCombineBlock, GB < 16);
     const dim3 grid(sh.token_blocks, row_shares(sh)), block(kCombineBlock);
     const size_t ld = a.ldi * Elem<DT>::kSize / GB;
     const bool near = a.capacity == 0 || ld < 0xFFFFFFFFu / a.capacity;       // a place and the row after it
@@ -594,33 +600,35 @@ template <int DT, int WDT> cudaError_t combine_by_granule(const ExpertArgs& a, c
 // not): 512 x 2 x 1024 fp32 2.7 / 3.4, 600 x 4 x 1024 bf16 3.2 / 4.1, 1200 x 4 x
 // 1024 4.0 / 4.3, 512 x 8 x 2048 7.0 / 6.4; longer rows 4 x 8 x 4096 2.7 / 2.9, 64
 // x 8 x 4096 3.3 / 3.1, 600 x 4 x 4096 7.8 / 5.5.
-bool slot_blocks(size_t slots, size_t granules) { return granules <= 256 ? slots * granules <= 640000 : slots <= 64; }
+bool slot_blocks(size_t slots, size_t granules) { return slots * granules <= (granules <= 256 ? 640000 : 160000); }
 
 template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const ExpertArgs& a, cudaStream_t s) {
     constexpr int block = kTokenBlock<TX>;
-    Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, TX, block);
+    Shape sh = shape_of(a, a.cols * Elem<DT>::kSize / GB, TX, block, false);
     sh.tx = TX;
     sh.token_blocks = static_cast<unsigned>((a.tokens + block / TX - 1) / (block / TX));
     const dim3 grid(sh.pad_blocks + sh.token_blocks, std::min((a.topk + J - 1) / J, 65535));
     return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(block), s, a, sh);
 }
 
+constexpr size_t kWarpTokens = 2048;
+
 // A warp has a token's row up to 128 granules, and up to 511 where a block would
 // have idle threads (us, warp / block: 8192 x 8 x 600 fp32, 150 granules, 58 / 78;
 // 8192 x 8 x 1000 fp32, 250, 94 / 102; 4096 x 8 x 1500 bf16, 375, 42 / 49; 4096 x
-// 8 x 2048 bf16, 256, 51 / 48).
+// 8 x 2048 bf16, 256, 51 / 48), if there are warps enough.
 template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArgs& a, cudaStream_t s) {
     const size_t granules = a.cols * Elem<DT>::kSize / GB;
     const bool few = slot_blocks(a.tokens * a.topk, granules);
     if (granules <= 128 && few) return backward<DT, WDT, GB, 32, 1>(a, s);
     if (few) return backward<DT, WDT, GB, 128, 1>(a, s);
-    if (granules <= 128 || (granules < 512 && granules != 256)) return backward<DT, WDT, GB, 32, 4>(a, s);
+    if (granules <= 128 || (granules < 512 && granules != 256 && a.tokens >= kWarpTokens)) return backward<DT, WDT, GB, 32, 4>(a, s);
     return backward<DT, WDT, GB, 256, 4>(a, s);
 }
 
 template <int DT, int WDT, int TX> cudaError_t backward_shift(const ExpertArgs& a, cudaStream_t s) {
     constexpr int block = kTokenBlock<TX>;
-    Shape sh = shape_of(a, chunks(a.cols * Elem<DT>::kSize), TX, block);
+    Shape sh = shape_of(a, chunks(a.cols * Elem<DT>::kSize), TX, block, false);
     sh.tx = TX;
     sh.token_blocks = static_cast<unsigned>((a.tokens + block / TX - 1) / (block / TX));
     const dim3 grid(sh.pad_blocks + sh.token_blocks, slot_blocks(a.tokens * a.topk, sh.granules) ? std::min(a.topk, 65535) : 1);

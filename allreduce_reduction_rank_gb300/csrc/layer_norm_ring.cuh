@@ -140,25 +140,26 @@ template <int DT> __device__ __forceinline__ void clear_outside(const uint4& bit
     }
 }
 
-template <int DT, bool kShift>
-__device__ __forceinline__ void write_vec(char* row, int i, const Place<DT, kShift>& at, const float2* x) {
+template <int DT, int NV, bool kShift>
+__device__ __forceinline__ void write_vec(char* row, int i, const Place<DT, kShift>& at, const uint4& bits, const float2* x) {
     constexpr int VE = Elem<DT>::kVE, N = PerWord<DT>::kN;
     float f[VE];
 #pragma unroll
     for (int p = 0; p < VE / 2; ++p) f[2 * p] = x[p].x, f[2 * p + 1] = x[p].y;
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = narrow_word<DT>(f + k * N);
+    char* to = row + at.byte(i);
     if (at.whole(i)) {
-        st_stream(reinterpret_cast<uint4*>(row + at.byte(i)),
-                  make_uint4(narrow_word<DT>(f), narrow_word<DT>(f + N), narrow_word<DT>(f + 2 * N), narrow_word<DT>(f + 3 * N)));
+        st_stream(reinterpret_cast<uint4*>(to), make_uint4(u[0], u[1], u[2], u[3]));
     } else if (kShift && at.some(i)) {                // words where they are whole
-        const int c = at.column(i);
+        const uint4 m = NV == 1 ? bits : bits_of<DT, kShift>(i, at);
+        const uint32_t have[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            char* to = row + (c + k * N) * Elem<DT>::kSize;
-            const bool first = at.has(c + k * N), last = at.has(c + k * N + N - 1);
-            const uint32_t word = narrow_word<DT>(f + k * N);
-            if (first && last) *reinterpret_cast<uint32_t*>(to) = word;
-            else if (first) *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(word);
-            else if (last) *reinterpret_cast<uint16_t*>(to + 2) = static_cast<uint16_t>(word >> 16);
+            if (have[k] == 0xFFFFFFFFu) reinterpret_cast<uint32_t*>(to)[k] = u[k];
+            else if (have[k] == 0x0000FFFFu) reinterpret_cast<uint16_t*>(to)[2 * k] = static_cast<uint16_t>(u[k]);
+            else if (have[k] == 0xFFFF0000u) reinterpret_cast<uint16_t*>(to)[2 * k + 1] = static_cast<uint16_t>(u[k] >> 16);
         }
     }
 }
@@ -349,7 +350,7 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     f[p] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[p], pair(-mj)), pair(rj)), w[i * P + p], b[i * P + p]);
-                write_vec<DT, kShift>(now_y, i, at, f);
+                write_vec<DT, NV, kShift>(now_y, i, at, bits, f);
             }
             now_y += pitch_y;
             if (at.t == 0) {
@@ -501,7 +502,7 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     f[p] = __ffma2_rn(__fmul2_rn(d[p], w[i * P + p]), pair(rs[j]), __ffma2_rn(f[p], pair(c1), pair(c0)));
-                write_vec<DT, kShift>(now_dx, i, at, f);
+                write_vec<DT, NV, kShift>(now_dx, i, at, bits, f);
             }
             now_dx += pitch_dx;
         }

@@ -27,7 +27,10 @@
 // vectors at a row's ends are copied whole, with bytes of the neighbouring row
 // or gap that are masked when they are read; only the first row's start and the
 // last row's end, where there may be no such bytes, are copied by element.
-// 32768 x 1021 fp32 backward 67 us (88%), 16384 x 1021 bf16 34 us (44%; 1024: 22).
+// That is done when the row is read, in a function of its own: inside the copies
+// it held registers (8192 x 4085 bf16 backward 50.2 -> 45.3 us, 4096 x 12001 90.7
+// -> 82.7, 16384 x 1021 34.0 -> 33.0; 32768 x 1021 fp32 67 -> 69).
+// 32768 x 1021 fp32 backward 69 us (86%), 16384 x 1021 bf16 33 us (45%; 1024: 20.6).
 #pragma once
 
 #include "layer_norm.cuh"
@@ -79,24 +82,30 @@ template <int DT, bool kShift> struct Place {
 };
 
 // Copies a thread's part of one row into its places.  `edge`: the matrix's first
-// row (4), whose start, or its last (8), whose end may have nothing beside it.
+// row (4), whose start, or its last (8), whose end may have nothing beside it;
+// those vectors become zeros here and are left to patch_row.
 template <int DT, int NV, int BT, bool kShift>
 __device__ __forceinline__ void copy_row(uint4* slots, const char* row, const Place<DT, kShift>& at, unsigned edge) {
-    constexpr int VE = Elem<DT>::kVE, es = Elem<DT>::kSize;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        const bool have = at.some(i) && !(kShift && ((at.flags >> (4 * i)) & edge));
+        copy_async(slots + i * BT + threadIdx.x, row + (at.some(i) ? at.byte(i) : at.byte(0) - at.t * 16), have);
+    }
+}
+
+// Copies what copy_row left, element by element, once the thread's own copies
+// of the batch have ended.
+template <int DT, int NV, int BT, bool kShift>
+__device__ __noinline__ void patch_row(uint4* slots, const char* row, const Place<DT, kShift>& at, unsigned edge) {
+    constexpr int VE = Elem<DT>::kVE, es = Elem<DT>::kSize;
+    for (int i = 0; i < NV; ++i) {
+        if (!((at.flags >> (4 * i)) & edge)) continue;
         uint4* slot = slots + i * BT + threadIdx.x;
-        if (kShift && ((at.flags >> (4 * i)) & edge)) {
-            const int c = at.column(i);
-#pragma unroll 1
-            for (int e = 0; e < VE; ++e) {
-                if (es == 2)
-                    reinterpret_cast<uint16_t*>(slot)[e] = at.has(c + e) ? reinterpret_cast<const uint16_t*>(row)[c + e] : 0;
-                else
-                    reinterpret_cast<uint32_t*>(slot)[e] = at.has(c + e) ? reinterpret_cast<const uint32_t*>(row)[c + e] : 0u;
-            }
-        } else {
-            copy_async(slot, row + (at.some(i) ? at.byte(i) : at.byte(0) - at.t * 16), at.some(i));
+        const int c = at.column(i);
+        for (int e = 0; e < VE; ++e) {
+            if (!at.has(c + e)) continue;
+            if (es == 2) reinterpret_cast<uint16_t*>(slot)[e] = reinterpret_cast<const uint16_t*>(row)[c + e];
+            else reinterpret_cast<uint32_t*>(slot)[e] = reinterpret_cast<const uint32_t*>(row)[c + e];
         }
     }
 }
@@ -146,13 +155,19 @@ __device__ __forceinline__ void write_vec(char* row, int i, const Place<DT, kShi
     float f[VE];
 #pragma unroll
     for (int p = 0; p < VE / 2; ++p) f[2 * p] = x[p].x, f[2 * p + 1] = x[p].y;
+    char* to = row + at.byte(i);
+    if (!kShift) {                                    // packed inside the branch: 36.0 us, before it 36.8 (backward 8192 x 4096)
+        if (at.whole(i))
+            st_stream(reinterpret_cast<uint4*>(to),
+                      make_uint4(narrow_word<DT>(f), narrow_word<DT>(f + N), narrow_word<DT>(f + 2 * N), narrow_word<DT>(f + 3 * N)));
+        return;
+    }
     uint32_t u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) u[k] = narrow_word<DT>(f + k * N);
-    char* to = row + at.byte(i);
     if (at.whole(i)) {
         st_stream(reinterpret_cast<uint4*>(to), make_uint4(u[0], u[1], u[2], u[3]));
-    } else if (kShift && at.some(i)) {                // words where they are whole
+    } else if (at.some(i)) {                          // words where they are whole
         const uint4 m = NV == 1 ? bits : bits_of<DT, kShift>(i, at);
         const uint32_t have[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
@@ -276,8 +291,16 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
     for (unsigned r = rows.begin, k = 0; r < rows.end; r += R, ++k) {
         copy_wait<D - 2>();
         copy_batch();                                 // into the place of the batch before this one
-        const uint4* from = ring + now * R * NV * BT;
+        uint4* from = ring + now * R * NV * BT;
         now = now + 1 == D ? 0 : now + 1;
+        if (kShift) {
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                if (r + j < rows.end && rows.edge(r + j) != 0)
+                    patch_row<DT, NV, BT, kShift>(from + j * NV * BT,
+                                                  static_cast<const char*>(a.x) + rows.row(r + j) * a.ldx * es, at,
+                                                  rows.edge(r + j));
+        }
         float s[R], m[R], q[R];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
@@ -449,8 +472,19 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
     for (unsigned r = rows.begin, k = 0; r < rows.end; r += R, ++k) {
         copy_wait<D - 2>();
         copy_batch();                                 // into the place of the batch before this one
-        const uint4* from = ring + now * R * 2 * NV * BT;
+        uint4* from = ring + now * R * 2 * NV * BT;
         now = now + 1 == D ? 0 : now + 1;
+        if (kShift) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const unsigned edge = r + j < rows.end ? rows.edge(r + j) : 0u;
+                if (edge == 0) continue;
+                const size_t row = rows.row(r + j);
+                patch_row<DT, NV, BT, kShift>(from + 2 * j * NV * BT, static_cast<const char*>(a.x) + row * a.ldx * es, at, edge);
+                patch_row<DT, NV, BT, kShift>(from + (2 * j + 1) * NV * BT, static_cast<const char*>(a.dy) + row * a.lddy * es,
+                                              at, edge);
+            }
+        }
         float v[2 * R], rs[R], mj[R];
         float2 dev[R][HP], up[R][HP];
 #pragma unroll

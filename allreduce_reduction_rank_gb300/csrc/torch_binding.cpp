@@ -11,6 +11,7 @@
 // SarError.
 #include <Python.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -111,12 +112,16 @@ sar_dtype element_code(const at::Tensor& t, const char* name) {
     return static_cast<sar_dtype>(code);
 }
 
-// A call's device and stream: those of its first tensor.
+// A call's device, that of its first tensor, and its stream.  The device is the
+// current one from here until the call returns or raises: the library launches
+// on the current device, and the default stream's handle is every device's.
 struct Where {
     c10::DeviceIndex device;
+    c10::cuda::OptionalCUDAGuard current;
     explicit Where(const at::Tensor& t, const char* name) : device(-1) {
         if (!t.is_cuda()) value_error("%s must be a CUDA tensor", name);
         device = t.get_device();
+        current.set_index(device);
     }
     void same(const at::Tensor& t, const char* name) const {
         if (!t.is_cuda() || t.get_device() != device) value_error("%s must be on the same CUDA device as the others", name);
@@ -127,6 +132,15 @@ struct Where {
             void* p = PyLong_AsVoidPtr(o);
             if (PyErr_Occurred()) throw Raised{};
             return reinterpret_cast<sar_stream_t>(p);
+        }
+        PyObject* index = PyObject_GetAttrString(o, "device_index");        // torch's streams have one
+        if (index == nullptr) {
+            PyErr_Clear();
+        } else {
+            const long long of = PyLong_AsLongLong(index);
+            Py_DECREF(index);
+            if (of == -1 && PyErr_Occurred()) throw Raised{};
+            if (of != device) value_error("stream must be on the tensors' device");
         }
         PyObject* handle = PyObject_GetAttrString(o, "cuda_stream");
         if (handle == nullptr) throw Raised{};

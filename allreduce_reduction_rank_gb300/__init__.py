@@ -5,7 +5,9 @@ torch tensors (or raw device addresses) into pointer arrays and sizes, calls
 the library, and raises :class:`SarError` on a non-OK status.  Every step of
 the computation runs in the library's CUDA kernels; there is no fallback.
 Importing this package fails if ``_build/libsar.so`` has not been built
-(``python allreduce_reduction_rank_gb300/build.py``).
+(``python allreduce_reduction_rank_gb300/build.py``).  The operators around the
+allreduce are in ``_build/_sar_torch.so``, which is loaded with the first of
+them; it raises ImportError if that module is missing.
 
 Function names follow the C ABI: :func:`sar_allreduce`,
 :func:`sar_allreduce_accum`, :func:`sar_reduce_scatter`, :func:`sar_all_gather`,
@@ -328,13 +330,16 @@ def sar_read_device_status(status, stream=None) -> int:
     return int(lib.sar_read_device_status(_addr(status), _stream(stream)))
 
 
-
 # ---------------------------------------------------------------------------
 # Operators around the allreduce (see include/sar.h).  They take torch tensors
 # and live in a compiled module beside the library (csrc/torch_binding.cpp),
 # which checks shapes, types and devices (ValueError), since the C ABI sees
 # addresses only.
 # ---------------------------------------------------------------------------
+_OPERATORS = ("sar_layer_norm", "sar_layer_norm_backward", "sar_expert_sort", "sar_expert_dispatch",
+              "sar_expert_combine", "sar_expert_combine_backward")
+
+
 def _load_operators():
     path = os.path.join(_HERE, "_build", "_sar_torch.so")
     if not os.path.exists(path):
@@ -347,13 +352,18 @@ def _load_operators():
     return module
 
 
-_operators = _load_operators()
-sar_layer_norm = _operators.sar_layer_norm
-sar_layer_norm_backward = _operators.sar_layer_norm_backward
-sar_expert_sort = _operators.sar_expert_sort
-sar_expert_dispatch = _operators.sar_expert_dispatch
-sar_expert_combine = _operators.sar_expert_combine
-sar_expert_combine_backward = _operators.sar_expert_combine_backward
+def __getattr__(name: str):
+    # The module is loaded with the first of its calls: one that is missing or was
+    # built for another torch costs the operators, not the rest of the package.
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = _load_operators()
+    globals().update((n, getattr(module, n)) for n in _OPERATORS)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_OPERATORS))
 
 
 def sar_layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:

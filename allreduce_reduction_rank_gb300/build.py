@@ -7,7 +7,8 @@ Each CUDA translation unit is compiled in parallel into an object file under
 declared in ``include/sar.h``; the CUDA runtime is linked statically and its
 symbols are kept private).  The torch module ``_build/_sar_torch.so``
 (``csrc/torch_binding.cpp``) is compiled at the same time with the host compiler
-against the installed torch.  Floating point is compiled without fast-math,
+against the installed torch; the library does not need it, and where torch or
+Python's headers are missing it is left out with a note on stderr.  Floating point is compiled without fast-math,
 flush-to-zero or contraction so that the binary32 adds are exactly IEEE adds
 with gradual underflow.
 
@@ -60,10 +61,20 @@ def nvcc_path() -> str:
 
 
 def torch_dir() -> str:
+    """The installed torch's directory; empty without one."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: the binding needs it to build")
-    return list(spec.submodule_search_locations)[0]
+    return list(spec.submodule_search_locations)[0] if spec is not None and spec.submodule_search_locations else ""
+
+
+def binding_lacks() -> str:
+    """What the torch module needs to be built and is not here; empty where nothing is missing."""
+    if not torch_dir():
+        return "torch"
+    if not os.path.exists(os.path.join(torch_dir(), "include", "c10", "cuda", "CUDAGuard.h")):
+        return "torch's CUDA headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return "" if shutil.which("g++") else "g++"
 
 
 def compile_binding(force: bool) -> str:
@@ -111,9 +122,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(min(len(SOURCES) + 1, (os.cpu_count() or 4) + 1)) as ex:
-        binding = ex.submit(compile_binding, force)
+        lacks = binding_lacks()
+        binding = None if lacks else ex.submit(compile_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + [
@@ -122,6 +133,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    if lacks:
+        sys.stderr.write(f"build.py: the torch module is left out: no {lacks}\n")
+        return LIB
+    binding_obj = binding.result()
     if force or _stale(TORCH_MODULE, [binding_obj, LIB]):
         tmp = TORCH_MODULE + f".tmp{os.getpid()}"
         lib_dir = os.path.join(torch_dir(), "lib")

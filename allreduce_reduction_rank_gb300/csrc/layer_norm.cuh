@@ -173,6 +173,9 @@ __device__ __forceinline__ float around(const float4& p, float mean) {
     return __fmaf_rn(__fmaf_rn(p.w, d, __fmul_rn(2.0f, off)), d, p.y);
 }
 
+// A joined sum of squares; NaN stays (fmaxf would drop it).
+__device__ __forceinline__ float not_below_zero(float q) { return q < 0.0f ? 0.0f : q; }
+
 // A barrier among the TPR threads of group g of the block.
 template <int TPR, int BT> __device__ __forceinline__ void group_sync(int g) {
     if (TPR == BT) __syncthreads();
@@ -183,7 +186,9 @@ template <int TPR, int BT> __device__ __forceinline__ void group_sync(int g) {
 // Forward.  Statistics in one exchange between the warps of a group: each warp
 // takes its own mean m_w and the deviations' squares q_w around it, and
 //   mean = sum s_w / n,   sum (x - mean)^2 = sum (q_w + n_w (m_w - mean)^2),
-// which keeps the digits that sum x^2 - n mean^2 would lose.
+// which keeps the digits that sum x^2 - n mean^2 would lose.  s_w is rounded, so
+// for a row far from zero and all but constant the sum can come out below zero,
+// by about what the mean's own rounding is worth: not_below_zero.
 // ---------------------------------------------------------------------------
 // The parameters are loaded after the statistics, except with kEarly (one vector
 // a thread, for calls of few rows, where the loads' latency counts).
@@ -274,6 +279,7 @@ forward_kernel(NormArgs a, bool w32, float inv_n) {
 #pragma unroll
                 for (int d = WPG / 2; d > 0; d >>= 1) q = __fadd_rn(q, __shfl_xor_sync(0xFFFFFFFFu, q, d));
             }
+            q = not_below_zero(q);
         }
         const float rstd = rsqrtf(__fmaf_rn(q, inv_n, a.eps));
 #pragma unroll

@@ -242,6 +242,7 @@ template <int DT, int NV, int R, int D, bool kShift, int WPG>
 __global__ void __launch_bounds__(kRingThreads<NV>, 1)
 ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any) {
     const int wpg = WPG != 0 ? WPG : wpg_any;
+    const bool alone = NV == 1 && wpg == 1;           // a row to a warp: at most 32 vectors
     constexpr int VE = Elem<DT>::kVE, P = VE / 2, BT = kRingThreads<NV>, L = 32 / R;
     const int G = blockDim.x / (32 * wpg);            // groups, of wpg warps each
     extern __shared__ uint4 ring[];                   // [D][R][NV][threads]
@@ -315,7 +316,8 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
             s[j] = __fadd_rn(s2.x, s2.y);
         }
         const float total = scatter_sum<R>(s);
-        const float near = __fmul_rn(total, inv_have);
+        // One warp takes the deviations around the row's mean, several each around one near their own.
+        const float near = alone ? quotient(total, n, inv_n) : __fmul_rn(total, inv_have);
 #pragma unroll
         for (int j = 0; j < R; ++j) m[j] = __shfl_sync(0xFFFFFFFFu, near, j * L);
 #pragma unroll
@@ -335,10 +337,9 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
         }
         const float squares = scatter_sum<R>(q);
         float mean, rstd;                             // of row lane % R, or lane / L with one warp
-        if (wpg == 1) {
-            mean = quotient(total, n, inv_n);
-            const float4 p = make_float4(total, squares, near, have);
-            rstd = rsqrtf(__fmaf_rn(around(p, mean), inv_n, a.eps));
+        if (alone) {
+            mean = near;
+            rstd = rsqrtf(__fmaf_rn(squares, inv_n, a.eps));
         } else {
             float4(&all)[BT / 32][R] = red[k & 1];
             if (lane % L == 0) all[threadIdx.x / 32][lane / L] = make_float4(total, squares, near, have);
@@ -359,12 +360,12 @@ ring_forward_kernel(NormArgs a, bool w32, float inv_n, Alignment al, int wpg_any
             for (int i = 0; i < T; ++i) sq = __fadd_rn(sq, around(p[i], mean));
 #pragma unroll
             for (int d = R; d < 32; d <<= 1) sq = __fadd_rn(sq, __shfl_xor_sync(0xFFFFFFFFu, sq, d));
-            rstd = rsqrtf(__fmaf_rn(sq, inv_n, a.eps));
+            rstd = rsqrtf(__fmaf_rn(not_below_zero(sq), inv_n, a.eps));
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            const float mj = __shfl_sync(0xFFFFFFFFu, mean, wpg == 1 ? j * L : j);
-            const float rj = __shfl_sync(0xFFFFFFFFu, rstd, wpg == 1 ? j * L : j);
+            const float mj = __shfl_sync(0xFFFFFFFFu, mean, alone ? j * L : j);
+            const float rj = __shfl_sync(0xFFFFFFFFu, rstd, alone ? j * L : j);
             if (r + j >= rows.end) continue;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {

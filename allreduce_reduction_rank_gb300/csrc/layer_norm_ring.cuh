@@ -519,9 +519,9 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (r + j >= rows.end) continue;
-            // dx = rstd g - rstd mean(g) - (x - mean) rstd^2 mean(g h)
-            const float c0 = -__fmul_rn(rs[j], __fmul_rn(v[2 * j], inv_n));
-            const float c1 = -__fmul_rn(__fmul_rn(rs[j], rs[j]), __fmul_rn(v[2 * j + 1], inv_n));
+            // dx = rstd (g - mean(g) - (x - mean) (rstd mean(g h))); rstd^2 could leave binary32's range.
+            const float c0 = -__fmul_rn(v[2 * j], inv_n);
+            const float c1 = -__fmul_rn(rs[j], __fmul_rn(v[2 * j + 1], inv_n));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float2 f[P], d[P];
@@ -536,7 +536,7 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
                 }
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    f[p] = __ffma2_rn(__fmul2_rn(d[p], w[i * P + p]), pair(rs[j]), __ffma2_rn(f[p], pair(c1), pair(c0)));
+                    f[p] = __fmul2_rn(__ffma2_rn(f[p], pair(c1), __ffma2_rn(d[p], w[i * P + p], pair(c0))), pair(rs[j]));
                 write_vec<DT, NV, kShift>(now_dx, i, at, bits, f);
             }
             now_dx += pitch_dx;

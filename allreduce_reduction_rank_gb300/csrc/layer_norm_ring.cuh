@@ -412,6 +412,26 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[N], int g
     for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, s, i);
 }
 
+// A thread's sum of g h over its places in the row, from the ring (x, then dy;
+// its first place is column c0) and the parameter.
+template <int DT, int NV, int BT>
+__device__ __noinline__ float sum_in_row(const uint4* slots, const void* weight, bool w32, int c0, int tpr, int cols,
+                                         float minus_mean, float rstd) {
+    constexpr int VE = Elem<DT>::kVE;
+    float q = 0.0f;
+    for (int i = 0; i < NV; ++i) {
+        for (int e = 0; e < VE; ++e) {
+            const int c = c0 + i * tpr * VE + e;
+            if (c < 0 || c >= cols) continue;
+            const float h = __fmul_rn(__fadd_rn(load_elem<DT>(slots + i * BT + threadIdx.x, e), minus_mean), rstd);
+            const float dh = __fmul_rn(load_elem<DT>(slots + (NV + i) * BT + threadIdx.x, e), h);
+            const float w = weight == nullptr ? 1.0f : (w32 ? static_cast<const float*>(weight)[c] : load_elem<DT>(weight, c));
+            q = __fmaf_rn(dh, w, q);
+        }
+    }
+    return q;
+}
+
 template <int DT, int NV, int R, int D, bool kShift, int WPG>
 __global__ void __launch_bounds__(kRingThreads<NV>, 1)
 ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wpg_any) {
@@ -498,10 +518,11 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
                     float2 f[P], d[P];
                     read_vec<DT, NV, BT, kShift>(from + (j * 2) * NV * BT, i, at, bits, f);
                     read_vec<DT, NV, BT, kShift>(from + (j * 2 + 1) * NV * BT, i, at, bits, d);
+                    const float m = kShift || at.some(i) ? mj[j] : 0.0f;        // whole vectors past the end: 0 - 0
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         const int c = i * P + p;
-                        f[p] = __fadd2_rn(f[p], pair(mj[j]));
+                        f[p] = __fadd2_rn(f[p], pair(m));
                         if (kHold) dev[j][p % HP] = f[p], up[j][p % HP] = d[p];
                         const float2 dh = __fmul2_rn(d[p], __fmul2_rn(f[p], pair(rs[j])));     // dy h
                         dw[c] = __fadd2_rn(dw[c], dh);
@@ -513,6 +534,8 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
             }
             v[2 * j] = __fadd_rn(s2.x, s2.y);
             v[2 * j + 1] = __fadd_rn(q2.x, q2.y);
+            if (kShift && past_range<DT>(mj[j], rs[j]))
+                v[2 * j + 1] = sum_in_row<DT, NV, BT>(from + j * 2 * NV * BT, a.weight, w32, at.column(0), at.tpr, at.cols, mj[j], rs[j]);
         }
         statistics(r + R);
         group_sums<BT, 2 * R>(v, red[k & 1], g, wpg);

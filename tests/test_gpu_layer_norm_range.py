@@ -51,3 +51,17 @@ def test_rows_of_huge_spread(sar, shape, dtype):
     w = 1 + 0.2 * torch.randn(shape[1], generator=g, device="cuda")
     d = x.double() - x.double().mean(1, keepdim=True)
     check(sar, dy, x, w, x.double().mean(1).float(), (d * d).mean(1).rsqrt().float())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("gap,offset", [(0, 0), (8, 0), (3, 1)])
+@pytest.mark.parametrize("shape", [(5, 37), (7, 100), (9, 136), (40, 250), (3, 1021), (3, 1500), (24400, 100), (24400, 136),
+                                   (39000, 250), (3100, 1020), (7300, 1021), (330, 5000), (330, 5003)], ids=str)
+def test_constant_rows_of_a_great_value(sar, shape, gap, offset, dtype):
+    """Rows of 2^110 throughout with eps = 1e-12: h is 0 and dx = rstd (g - mean(g)) with rstd = 1e6.  A place past the
+    row's end, which holds 0, would have (0 - mean) rstd = -infinity."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.full(shape, 2.0 ** 110, device="cuda", dtype=ref.DTYPES[dtype])
+    dy = torch.randn(*shape, generator=g, device="cuda").to(x.dtype)
+    mean = torch.full(shape[:1], 2.0 ** 110, device="cuda")
+    check(sar, dy, x, None, mean, torch.full_like(mean, 1e6), gap, offset)

@@ -413,12 +413,12 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[N], int g
 }
 
 // A thread's sum of g h over its places in the row, from the ring (x, then dy;
-// its first place is column c0) and the parameter.
+// its first place is column c0) and the parameter, in the order of the pairs.
 template <int DT, int NV, int BT>
 __device__ __noinline__ float sum_in_row(const uint4* slots, const void* weight, bool w32, int c0, int tpr, int cols,
                                          float minus_mean, float rstd) {
     constexpr int VE = Elem<DT>::kVE;
-    float q = 0.0f;
+    float even = 0.0f, odd = 0.0f;
     for (int i = 0; i < NV; ++i) {
         for (int e = 0; e < VE; ++e) {
             const int c = c0 + i * tpr * VE + e;
@@ -426,10 +426,11 @@ __device__ __noinline__ float sum_in_row(const uint4* slots, const void* weight,
             const float h = __fmul_rn(__fadd_rn(load_elem<DT>(slots + i * BT + threadIdx.x, e), minus_mean), rstd);
             const float dh = __fmul_rn(load_elem<DT>(slots + (NV + i) * BT + threadIdx.x, e), h);
             const float w = weight == nullptr ? 1.0f : (w32 ? static_cast<const float*>(weight)[c] : load_elem<DT>(weight, c));
-            q = __fmaf_rn(dh, w, q);
+            if (e % 2 == 0) even = __fmaf_rn(dh, w, even);
+            else odd = __fmaf_rn(dh, w, odd);
         }
     }
-    return q;
+    return __fadd_rn(even, odd);
 }
 
 template <int DT, int NV, int R, int D, bool kShift, int WPG>

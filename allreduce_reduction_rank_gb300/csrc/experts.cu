@@ -4,13 +4,15 @@
 // All three read or write topk scattered rows for each token's row, and are
 // bound by HBM: whole rows move in granules of up to 16 bytes, a thread owns
 // one granule of a token's row at a time and has the topk rows' accesses (kJ at
-// a time) in flight together.  A token's own row is touched once.
+// a time) in flight together.  A token's own row is read once for every eight
+// choices by the dispatch and for every four by the gradient; the kernels that
+// take one choice at a time read it for each, from L1 or L2 after the first.
 //
 // Measured (GB300, copy rate 6.78 TB/s), 16384 x 8 x 4096 bf16: dispatch 181 us
 // (98% of the copy rate: it scatters, so that x is read once, where gathering by
 // place would read each row topk times), combine 171 us (104%); combine's
 // gradient 8192 x 4 x 8192 fp16 176 us (101%).  Small: dispatch of 32 x 8 rows of
-// 2048 bf16 2.0 us, combine's gradient 512 x 2 x 1024 fp32 3.0 us.
+// 2048 bf16 2.0 us, combine's gradient 512 x 2 x 1024 fp32 2.7 us.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -611,18 +613,29 @@ template <int DT, int WDT, int GB, int TX, int J> cudaError_t backward(const Exp
     return launch_kernel(combine_backward_kernel<DT, WDT, GB, TX, J>, grid, dim3(block), s, a, sh);
 }
 
+// Whether a warp has a token's row rather than a block of 256: up to 128 granules,
+// and up to 511 if there are warps enough, unless the row fills 15/16 of the
+// block's places (from 257 granules on, or granules of eight elements; a block does
+// not pay for 256 of fewer).  Measured (us, warp / block): bf16
+// 4096 x 8 rows of 160 granules 32.5 / 37.0, 230 49.2 / 46.7, 250 51.5 / 48.9, 255
+// 52.8 / 50.0, 256 50.7 / 47.6, 257 54.6 / 53.7, 300 61.5 / 63.1, 375 80.1 / 76.5,
+// 500 102.9 / 92.1, 511 107 / 95.5; 8192 x 8 rows 224 83 / 87, 240 90.8 / 90.6, 255
+// 100 / 99, 256 97 / 94, 511 195 / 184.  fp32 8192 x 8 rows of 230 90 / 100, 255 99 /
+// 107, 256 94 / 99, 375 143 / 157, 511 192 / 193; 4096 x 8 rows of 255 52.2 / 53.8,
+// 511 100 / 95.5; but 4096 x 4 rows of 256 29.3 / 26.5.
 constexpr size_t kWarpTokens = 2048;
+bool warp_rows(size_t tokens, size_t granules, int elements) {
+    const size_t places = (granules + kBlock - 1) / kBlock * kBlock;
+    const bool filled = 16 * granules >= 15 * places && (granules > kBlock || elements == 8);
+    return granules <= 128 || (granules < 2 * kBlock && tokens >= kWarpTokens && !filled);
+}
 
-// A warp has a token's row up to 128 granules, and up to 511 where a block would
-// have idle threads (us, warp / block: 8192 x 8 x 600 fp32, 150 granules, 58 / 78;
-// 8192 x 8 x 1000 fp32, 250, 94 / 102; 4096 x 8 x 1500 bf16, 375, 42 / 49; 4096 x
-// 8 x 2048 bf16, 256, 51 / 48), if there are warps enough.
 template <int DT, int WDT, int GB> cudaError_t backward_by_shape(const ExpertArgs& a, cudaStream_t s) {
     const size_t granules = a.cols * Elem<DT>::kSize / GB;
     const bool few = slot_blocks(a.tokens * a.topk, granules);
     if (granules <= 128 && few) return backward<DT, WDT, GB, 32, 1>(a, s);
     if (few) return backward<DT, WDT, GB, 128, 1>(a, s);
-    if (granules <= 128 || (granules < 512 && granules != 256 && a.tokens >= kWarpTokens)) return backward<DT, WDT, GB, 32, 4>(a, s);
+    if (warp_rows(a.tokens, granules, Elements<DT, GB>::kN)) return backward<DT, WDT, GB, 32, 4>(a, s);
     return backward<DT, WDT, GB, 256, 4>(a, s);
 }
 

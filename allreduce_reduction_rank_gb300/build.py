@@ -77,12 +77,21 @@ def binding_lacks() -> str:
     return "" if shutil.which("g++") else "g++"
 
 
+def binding_key() -> str:
+    """The interpreter and torch whose headers define what the torch module may assume."""
+    with open(os.path.join(torch_dir(), "version.py")) as f:
+        return "\n".join([sysconfig.get_config_var("SOABI") or sys.version, torch_dir(), f.read()])
+
+
 def compile_binding(force: bool) -> str:
-    """The torch module's object file."""
+    """The torch module's object file; built again for another interpreter or torch."""
     path, obj = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(OUT, "torch_binding.cpp.obj")
-    # Rebuilt with another torch or Python, too: their headers define what it may assume.
-    deps = [path, os.path.join(INCLUDE, "sar.h"), os.path.join(torch_dir(), "version.py")]
-    if force or _stale(obj, deps):
+    key_path, key = os.path.join(OUT, "torch_binding.key"), binding_key()
+    built_for = ""
+    if os.path.exists(key_path):
+        with open(key_path) as f:
+            built_for = f.read()
+    if force or built_for != key or _stale(obj, [path, os.path.join(INCLUDE, "sar.h")]):
         cuda = os.path.dirname(os.path.dirname(nvcc_path()))
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-I", INCLUDE,
                "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir(), "include"),
@@ -92,6 +101,8 @@ def compile_binding(force: bool) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{res.stdout}\n{res.stderr}")
         os.replace(obj + ".tmp", obj)
+        with open(key_path, "w") as f:
+            f.write(key)
     return obj
 
 

@@ -56,3 +56,18 @@ def test_the_package_imports_without_its_torch_module(tmp_path, broken):
             "assert not hasattr(sar, 'sar_nothing')\n")
     run = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
     assert run.returncode == 0, run.stderr + run.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no g++")
+def test_the_module_is_rebuilt_for_another_torch_or_interpreter(tmp_path):
+    """Their files may be older than the module, so times do not tell."""
+    out = copy(tmp_path, ())
+    build = [sys.executable, str(tmp_path / PACKAGE / "build.py")]
+    assert subprocess.run(build, capture_output=True).returncode == 0
+    obj, module, key = out / "torch_binding.cpp.obj", out / "_sar_torch.so", out / "torch_binding.key"
+    first = [f.stat().st_mtime_ns for f in (obj, module)]
+    assert subprocess.run(build, capture_output=True).returncode == 0
+    assert [f.stat().st_mtime_ns for f in (obj, module)] == first
+    key.write_text(key.read_text().replace("cpython", "another"))
+    assert subprocess.run(build, capture_output=True).returncode == 0
+    assert all(f.stat().st_mtime_ns > t for f, t in zip((obj, module), first))

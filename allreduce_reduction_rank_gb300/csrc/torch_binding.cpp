@@ -11,6 +11,7 @@
 // SarError.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -121,7 +122,7 @@ struct Where {
     explicit Where(const at::Tensor& t, const char* name) : device(-1) {
         if (!t.is_cuda()) value_error("%s must be a CUDA tensor", name);
         device = t.get_device();
-        current.set_index(device);
+        if (c10::cuda::current_device() != device) current.set_index(device);
     }
     void same(const at::Tensor& t, const char* name) const {
         if (!t.is_cuda() || t.get_device() != device) value_error("%s must be on the same CUDA device as the others", name);

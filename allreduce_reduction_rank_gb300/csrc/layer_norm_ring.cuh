@@ -513,6 +513,9 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
         for (int j = 0; j < R; ++j) {
             float2 s2 = pair(0.0f), q2 = pair(0.0f);
             rs[j] = rstd[j], mj[j] = -mean[j];
+            // One vector a thread: its bits are at hand to mask with.  With more, which
+            // have no registers for it, the thread's sum is taken again.
+            const bool past = kShift && past_range<DT>(mj[j], rs[j]);
             if (r + j < rows.end) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -521,9 +524,11 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
                     read_vec<DT, NV, BT, kShift>(from + (j * 2 + 1) * NV * BT, i, at, bits, d);
                     const float m = kShift || at.some(i) ? mj[j] : 0.0f;        // whole vectors past the end: 0 - 0
 #pragma unroll
+                    for (int p = 0; p < P; ++p) f[p] = __fadd2_rn(f[p], pair(m));
+                    if (NV == 1 && past) clear_outside<DT>(bits, f);
+#pragma unroll
                     for (int p = 0; p < P; ++p) {
                         const int c = i * P + p;
-                        f[p] = __fadd2_rn(f[p], pair(m));
                         if (kHold) dev[j][p % HP] = f[p], up[j][p % HP] = d[p];
                         const float2 dh = __fmul2_rn(d[p], __fmul2_rn(f[p], pair(rs[j])));     // dy h
                         dw[c] = __fadd2_rn(dw[c], dh);
@@ -535,7 +540,7 @@ ring_backward_kernel(NormGradArgs a, bool w32, float inv_n, Alignment al, int wp
             }
             v[2 * j] = __fadd_rn(s2.x, s2.y);
             v[2 * j + 1] = __fadd_rn(q2.x, q2.y);
-            if (kShift && past_range<DT>(mj[j], rs[j]))
+            if (NV > 1 && past)
                 v[2 * j + 1] = sum_in_row<DT, NV, BT>(from + j * 2 * NV * BT, a.weight, w32, at.column(0), at.tpr, at.cols, mj[j], rs[j]);
         }
         statistics(r + R);

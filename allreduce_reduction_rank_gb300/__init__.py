@@ -17,9 +17,10 @@ Function names follow the C ABI: :func:`sar_allreduce`,
 :func:`sar_allreduce_ll_noalloc`, :func:`sar_allreduce_ll_cluster`,
 :func:`sar_fp8_convert`, :func:`sar_read_device_status`,
 :func:`sar_status_string`; around the allreduce, :func:`sar_layer_norm`,
-:func:`sar_layer_norm_backward`, :func:`sar_expert_rows`, :func:`sar_expert_sort`,
-:func:`sar_expert_dispatch`, :func:`sar_expert_combine` and
-:func:`sar_expert_combine_backward`, which take torch tensors.
+:func:`sar_layer_norm_backward` (and :func:`sar_layer_norm_backward_workspace_bytes`),
+:func:`sar_expert_sort` (and :func:`sar_expert_rows`), :func:`sar_expert_dispatch`,
+:func:`sar_expert_combine` and :func:`sar_expert_combine_backward`, which take torch
+tensors.
 """
 from __future__ import annotations
 

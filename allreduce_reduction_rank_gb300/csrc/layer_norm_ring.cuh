@@ -3,9 +3,9 @@
 // One block on each SM stays for many rows.  A row belongs to a group of whole
 // warps, as few as cover it, which has a range of the rows and works on R of
 // them at a time (a batch).  Thread t of the group's `tpr` has NV vectors of
-// each row, vector i at 16-byte place i * tpr + t; it copies them into its own places of a ring of D batches
-// in shared memory with cp.async, D - 1 batches ahead, and only itself reads
-// them again.  So the copies need no barrier, 100 KB and more are in flight on
+// each row, vector i at 16-byte place i * tpr + t; it copies them into its own
+// places of a ring of D batches in shared memory with cp.async, D - 1 batches
+// ahead, and only itself reads them again.  So the copies need no barrier, 100 KB and more are in flight on
 // each SM whatever the registers hold, and the parameters and the sums for
 // their gradients stay in registers.  What a batch costs beside its elements,
 // the sums over the threads and a barrier, is shared by its rows: the sums of R
@@ -13,8 +13,12 @@
 //
 // Measured (GB300, copy rate 6.78 TB/s): forward 16384 x 8192 bf16 84 us, 94% of
 // the copy rate, bound by HBM; backward 32768 x 4096 fp16 117 us without the
-// parameters' gradients (101%), 121.6 with; 8192 x 4096 36.0 us (82%: launches,
+// parameters' gradients (101%), 121 with; 8192 x 4096 36.0 us (82%: launches,
 // the ring's first fill and its last batch are 3 us and the parameters' sums 4).
+// Whole warps and groups leave lanes of a block idle at other widths, 8192 rows of
+// bf16, forward / backward: 2880 columns (70% of the lanes) 64 / 67% of the copy
+// rate, 4608 (56%) 67 / 72, 5120 (62%) 73 / 77, 6144 (75%) 82 / 83, 7168 (88%) 86 /
+// 87, 8192 (all) 91 / 91, 12288 (75%) 82 / 84.
 // Depth: backward D = 3 41.0 us, D = 2 38.8 (less to fill before the first row
 // and to work off after the last load); forward NV = 2 D = 2 90.1, 3 84.5, 6
 // 88.4.  R = 1 backward 41, and 128 registers with half the threads 42.  The loads
@@ -30,7 +34,9 @@
 // That is done when the row is read, in a function of its own: inside the copies
 // it held registers (8192 x 4085 bf16 backward 50.2 -> 45.3 us, 4096 x 12001 90.7
 // -> 82.7, 16384 x 1021 34.0 -> 33.0; 32768 x 1021 fp32 67 -> 69).
-// 32768 x 1021 fp32 backward 69 us (86%), 16384 x 1021 bf16 33 us (45%; 1024: 20.6).
+// 32768 x 1021 fp32 backward 68 us (87%); bf16, forward / backward: 16384 x 1021 41 /
+// 45% (1024: 71 / 73%), 65536 x 130 27 / 28%, 32768 x 321 28 / 30%, 8192 x 4099 36 /
+// 48%, 8192 x 4085 58 / 64%, 4096 x 12001 47 / 52%.
 #pragma once
 
 #include "layer_norm.cuh"

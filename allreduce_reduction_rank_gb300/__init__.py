@@ -19,8 +19,11 @@ Function names follow the C ABI: :func:`sar_allreduce`,
 :func:`sar_status_string`; around the allreduce, :func:`sar_layer_norm`,
 :func:`sar_layer_norm_backward` (and :func:`sar_layer_norm_backward_workspace_bytes`),
 :func:`sar_expert_sort` (and :func:`sar_expert_rows`), :func:`sar_expert_dispatch`,
-:func:`sar_expert_combine` and :func:`sar_expert_combine_backward`, which take torch
-tensors.
+:func:`sar_expert_combine` and :func:`sar_expert_combine_backward`, the router
+:func:`sar_expert_route` and :func:`sar_expert_route_backward`, the expert layer of a few
+tokens :func:`sar_expert_layer` (and :func:`sar_expert_layer_workspace_bytes`), and the update
+of a matrix :func:`sar_orthogonalize` (and :func:`sar_orthogonalize_workspace_bytes`), which
+take torch tensors.
 """
 from __future__ import annotations
 
@@ -51,6 +54,13 @@ SAR_MAX_RANKS = 32
 SAR_LL_NOALLOC_SCRATCH_BYTES = 16 << 20
 SAR_LL_CLUSTER_MAX_RANKS = 16
 SAR_MAX_EXPERTS = 1024
+SAR_MAX_TOPK = 32
+SAR_EXPERT_LAYER_MAX_SLOTS = 1024
+SAR_ORTHOGONALIZE_MAX_SIDE = 65536
+# sar_softmax
+SAR_SOFTMAX_CHOSEN, SAR_SOFTMAX_ALL = 0, 1
+# sar_activation
+SAR_ACT_SILU, SAR_ACT_GELU, SAR_ACT_RELU = 0, 1, 2
 
 DTYPE_CODES = {"bf16": SAR_BF16, "fp16": SAR_FP16, "fp32": SAR_FP32, "e4m3fn": SAR_FP8_E4M3FN,
                "e4m3b15": SAR_FP8_E4M3B15}
@@ -91,6 +101,16 @@ lib.sar_expert_dispatch.argtypes = [_vp, _sz, _vp, _vp, _vp, _i32, _vp, _sz, _sz
 lib.sar_expert_combine.argtypes = [_vp, _sz, _sz, _vp, _vp, _vp, _sz, _sz, _i32, _sz, _i32, _i32, _vp]
 lib.sar_expert_combine_backward.argtypes = [_vp, _sz, _vp, _sz, _sz, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp, _sz, _i32,
                                             _sz, _i32, _i32, _vp]
+lib.sar_expert_route.argtypes = [_vp, _sz, _vp, _i32, _vp, _sz, _i32, _i32, _i32, _i32, _i32, _vp]
+lib.sar_expert_route_backward.argtypes = [_vp, _vp, _sz, _vp, _i32, _vp, _sz, _sz, _i32, _i32, _i32, _i32, _i32, _vp]
+lib.sar_expert_layer_workspace_bytes.argtypes = [_sz, _i32, _i32, _sz, _sz]
+lib.sar_expert_layer_workspace_bytes.restype = _sz
+lib.sar_expert_layer.argtypes = [_vp, _sz, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _sz, _i32, _i32, _sz, _sz, _i32, _i32, _i32,
+                                 _i32, _vp, _sz, _vp]
+lib.sar_orthogonalize_workspace_bytes.argtypes = [_sz, _sz, _sz]
+lib.sar_orthogonalize_workspace_bytes.restype = _sz
+lib.sar_orthogonalize.argtypes = [_vp, _sz, _sz, _vp, _sz, _sz, _sz, _sz, _sz, _i32, _f32, _f32, _f32, _f32, _f32, _i32, _vp,
+                                  _sz, _vp]
 lib.sar_read_device_status.argtypes = [_vp, _vp]
 lib.sar_status_string.argtypes = [_i32]
 lib.sar_status_string.restype = ctypes.c_char_p
@@ -98,7 +118,8 @@ for _f in ("sar_allreduce", "sar_allreduce_accum", "sar_allreduce_ll_fused", "sa
            "sar_reduce_scatter", "sar_all_gather", "sar_ll_pack", "sar_ll_unpack_reduce",
            "sar_allreduce_ll", "sar_allreduce_ll_double", "sar_allreduce_ll_noalloc", "sar_allreduce_ll_cluster",
            "sar_fp8_convert", "sar_layer_norm", "sar_layer_norm_backward", "sar_expert_sort", "sar_expert_dispatch",
-           "sar_expert_combine", "sar_expert_combine_backward",
+           "sar_expert_combine", "sar_expert_combine_backward", "sar_expert_route", "sar_expert_route_backward",
+           "sar_expert_layer", "sar_orthogonalize",
            "sar_read_device_status"):
     getattr(lib, _f).restype = _i32
 
@@ -333,12 +354,13 @@ def sar_read_device_status(status, stream=None) -> int:
 
 # ---------------------------------------------------------------------------
 # Operators around the allreduce (see include/sar.h).  They take torch tensors
-# and live in a compiled module beside the library (csrc/torch_binding.cpp),
+# and live in a compiled module beside the library (csrc/torch_binding*.cpp),
 # which checks shapes, types and devices (ValueError), since the C ABI sees
 # addresses only.
 # ---------------------------------------------------------------------------
 _OPERATORS = ("sar_layer_norm", "sar_layer_norm_backward", "sar_expert_sort", "sar_expert_dispatch",
-              "sar_expert_combine", "sar_expert_combine_backward")
+              "sar_expert_combine", "sar_expert_combine_backward", "sar_expert_route", "sar_expert_route_backward",
+              "sar_expert_layer", "sar_orthogonalize")
 
 
 def _load_operators():
@@ -375,3 +397,13 @@ def sar_layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
 def sar_expert_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int:
     """Rows that hold every expert's segment whatever the routing."""
     return int(lib.sar_expert_rows(tokens, topk, experts, align))
+
+
+def sar_expert_layer_workspace_bytes(tokens: int, topk: int, experts: int, cols: int, hidden: int) -> int:
+    """Bytes of sar_expert_layer's workspace."""
+    return int(lib.sar_expert_layer_workspace_bytes(tokens, topk, experts, cols, hidden))
+
+
+def sar_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    """Bytes of sar_orthogonalize's workspace."""
+    return int(lib.sar_orthogonalize_workspace_bytes(batch, rows, cols))

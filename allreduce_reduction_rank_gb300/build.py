@@ -6,7 +6,7 @@ Each CUDA translation unit is compiled in parallel into an object file under
 ``_build/`` and the objects are linked into ``_build/libsar.so`` (C ABI,
 declared in ``include/sar.h``; the CUDA runtime is linked statically and its
 symbols are kept private).  The torch module ``_build/_sar_torch.so``
-(``csrc/torch_binding.cpp``) is compiled at the same time with the host compiler
+(``csrc/torch_binding*.cpp``) is compiled at the same time with the host compiler
 against the installed torch; the library does not need it, and where torch or
 Python's headers are missing it is left out with a note on stderr.  Floating point is compiled without fast-math,
 flush-to-zero or contraction so that the binary32 adds are exactly IEEE adds
@@ -37,8 +37,10 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["ll_writeback.cu", "ll_fused.cu", "ll_cluster.cu", "ll_cta.cu", "rsag_e4m3b15.cu", "rsag_e4m3b15_acc.cu",
            "ll.cu", "rsag_e4m3fn_acc.cu", "rsag_e4m3fn.cu", "rsag_bf16_acc.cu", "rsag_fp16_acc.cu", "rsag_fp32_acc.cu", "rsag_fp16.cu",
            "rsag_bf16.cu", "rsag_fp32.cu", "layer_norm_bf16.cu", "layer_norm_fp16.cu", "layer_norm_fp32.cu",
-           "layer_norm.cu", "experts.cu", "expert_sort.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
+           "orthogonalize.cu", "expert_layer.cu", "layer_norm.cu", "experts.cu", "route.cu", "expert_sort.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
            "noalloc.cu"]
+# The torch module's; all are compiled again for another interpreter or torch.
+BINDING_SOURCES = ["torch_binding.cpp", "torch_binding_block.cpp"]
 HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh", "layer_norm_ring.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -83,27 +85,34 @@ def binding_key() -> str:
         return "\n".join([sysconfig.get_config_var("SOABI") or sys.version, torch_dir(), f.read()])
 
 
-def compile_binding(force: bool) -> str:
-    """The torch module's object file; built again for another interpreter or torch."""
-    path, obj = os.path.join(CSRC, "torch_binding.cpp"), os.path.join(OUT, "torch_binding.cpp.obj")
+def compile_binding(force: bool) -> list:
+    """The torch module's object files; built again for another interpreter or torch."""
     key_path, key = os.path.join(OUT, "torch_binding.key"), binding_key()
     built_for = ""
     if os.path.exists(key_path):
         with open(key_path) as f:
             built_for = f.read()
-    if force or built_for != key or _stale(obj, [path, os.path.join(INCLUDE, "sar.h")]):
-        cuda = os.path.dirname(os.path.dirname(nvcc_path()))
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-I", INCLUDE,
-               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir(), "include"),
-               "-I", os.path.join(torch_dir(), "include", "torch", "csrc", "api", "include"),
-               "-I", os.path.join(cuda, "include"), "-c", path, "-o", obj + ".tmp"]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{res.stdout}\n{res.stderr}")
-        os.replace(obj + ".tmp", obj)
-        with open(key_path, "w") as f:
-            f.write(key)
-    return obj
+    headers = [os.path.join(CSRC, "torch_binding.h"), os.path.join(INCLUDE, "sar.h")]
+
+    def compile_one(src: str) -> str:
+        path, obj = os.path.join(CSRC, src), os.path.join(OUT, src + ".obj")
+        if force or built_for != key or _stale(obj, [path] + headers):
+            cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+            cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-I", INCLUDE,
+                   "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir(), "include"),
+                   "-I", os.path.join(torch_dir(), "include", "torch", "csrc", "api", "include"),
+                   "-I", os.path.join(cuda, "include"), "-c", path, "-o", obj + ".tmp"]
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            if res.returncode != 0:
+                raise RuntimeError(f"g++ failed on {src}:\n{res.stdout}\n{res.stderr}")
+            os.replace(obj + ".tmp", obj)
+        return obj
+
+    with ThreadPoolExecutor(len(BINDING_SOURCES)) as ex:
+        objs = list(ex.map(compile_one, BINDING_SOURCES))
+    with open(key_path, "w") as f:
+        f.write(key)
+    return objs
 
 
 def _stale(target: str, deps: list) -> bool:
@@ -147,11 +156,11 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if lacks:
         sys.stderr.write(f"build.py: the torch module is left out: no {lacks}\n")
         return LIB
-    binding_obj = binding.result()
-    if force or _stale(TORCH_MODULE, [binding_obj, LIB]):
+    binding_objs = binding.result()
+    if force or _stale(TORCH_MODULE, binding_objs + [LIB]):
         tmp = TORCH_MODULE + f".tmp{os.getpid()}"
         lib_dir = os.path.join(torch_dir(), "lib")
-        cmd = ["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L", lib_dir, "-ltorch_python", "-ltorch_cpu", "-lc10",
+        cmd = ["g++", "-shared", "-o", tmp] + binding_objs + [LIB, "-L", lib_dir, "-ltorch_python", "-ltorch_cpu", "-lc10",
                "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib_dir]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:

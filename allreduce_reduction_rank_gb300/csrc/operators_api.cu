@@ -55,6 +55,46 @@ sar_status check_segments(const int32_t* counts, const int32_t* offsets, int exp
     return aligned(counts, 4) && aligned(offsets, 4) ? SAR_OK : SAR_ERR_MISALIGNED;
 }
 
+bool route_ok(int id_bytes, size_t tokens, int topk, int experts, int softmax) {
+    return (id_bytes == 4 || id_bytes == 8) && topk <= SAR_MAX_TOPK && topk <= experts && experts_ok(experts) &&
+           slots_fit(tokens, topk) && (softmax == SAR_SOFTMAX_CHOSEN || softmax == SAR_SOFTMAX_ALL);
+}
+
+constexpr size_t kMaxLayerSide = size_t(1) << 20;
+
+bool layer_sizes_ok(size_t tokens, int topk, int experts, size_t cols, size_t hidden) {
+    return topk >= 1 && tokens <= static_cast<size_t>(SAR_EXPERT_LAYER_MAX_SLOTS) / static_cast<size_t>(topk) &&
+           experts_ok(experts) && cols <= kMaxLayerSide && hidden <= kMaxLayerSide;
+}
+
+bool orthogonalize_sizes_ok(size_t batch, size_t rows, size_t cols) {
+    return batch <= 65535 && rows <= SAR_ORTHOGONALIZE_MAX_SIDE && cols <= SAR_ORTHOGONALIZE_MAX_SIDE;
+}
+
+// The largest |p(s)|, p(s) = a s + b s^3 + c s^5, of `steps` steps that begin in
+// 0 .. 1: over [0, top] it is at an end or where p'(s) = a + 3 b s^2 + 5 c s^4 = 0.
+// NaN or infinity for coefficients that are not finite.
+double newton_schulz_bound(double a, double b, double c, int steps) {
+    const auto p = [=](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+    double top = 1.0, grown = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        double next = p(top);
+        double roots[3] = {-1.0, -1.0, -1.0};
+        const double d = 9 * b * b - 20 * a * c;
+        if (c != 0.0 && d >= 0.0) {
+            roots[0] = (-3 * b + std::sqrt(d)) / (10 * c);
+            roots[1] = (-3 * b - std::sqrt(d)) / (10 * c);
+        }
+        if (b != 0.0) roots[2] = -a / (3 * b);                       // c = 0, or next to it
+        for (double r : roots)
+            if (r > 0.0 && r < top * top) next = std::fmax(next, p(std::sqrt(r)));
+        if (!(next <= 1e6)) return next * INFINITY;
+        grown = std::fmax(grown, next);
+        top = std::fmax(next, 1e-30);
+    }
+    return grown;
+}
+
 sar_status first_error(std::initializer_list<sar_status> all) {
     for (sar_status s : all)
         if (s != SAR_OK) return s;
@@ -201,6 +241,97 @@ SAR_API sar_status sar_expert_combine_backward(const void* dout, size_t ldo, con
     a.counts = counts, a.offsets = offsets, a.weights = weights, a.dweights = dweights, a.experts = experts;
     a.topk = topk, a.capacity = static_cast<uint32_t>(capacity), a.tokens = tokens, a.cols = cols;
     return to_status(launch_expert_combine_backward(dtype, wdtype, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+SAR_API sar_status sar_expert_route(const void* logits, size_t ldl, void* ids, int id_bytes, void* weights,
+                                    size_t tokens, int topk, int experts, sar_softmax softmax, sar_dtype dtype,
+                                    sar_dtype wdtype, sar_stream_t stream) {
+    if (!dtypes_ok(dtype, wdtype)) return SAR_ERR_UNSUPPORTED_DTYPE;
+    const size_t es = esize_of(dtype);
+    if (!route_ok(id_bytes, tokens, topk, experts, softmax) || !extent_fits(tokens, static_cast<size_t>(experts), ldl, es))
+        return SAR_ERR_INVALID_ARG;
+    if (tokens == 0) return SAR_OK;
+    const sar_status st = first_error({check_ptr(logits, es), check_ptr(ids, static_cast<size_t>(id_bytes)),
+                                       check_ptr(weights, esize_of(wdtype))});
+    if (st != SAR_OK) return st;
+    const RouteArgs a = {logits, ldl, ids, weights, nullptr, 0, tokens, topk, experts, softmax};
+    return to_status(launch_expert_route(dtype, wdtype, id_bytes, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+SAR_API sar_status sar_expert_route_backward(const void* dweights, const void* logits, size_t ldl, const void* ids,
+                                             int id_bytes, void* dlogits, size_t ldd, size_t tokens, int topk,
+                                             int experts, sar_softmax softmax, sar_dtype dtype, sar_dtype wdtype,
+                                             sar_stream_t stream) {
+    if (!dtypes_ok(dtype, wdtype)) return SAR_ERR_UNSUPPORTED_DTYPE;
+    const size_t es = esize_of(dtype);
+    if (!route_ok(id_bytes, tokens, topk, experts, softmax) || !extent_fits(tokens, static_cast<size_t>(experts), ldl, es) ||
+        !extent_fits(tokens, static_cast<size_t>(experts), ldd, es))
+        return SAR_ERR_INVALID_ARG;
+    if (tokens == 0) return SAR_OK;
+    const sar_status st = first_error({check_ptr(dweights, esize_of(wdtype)), check_ptr(logits, es),
+                                       check_ptr(ids, static_cast<size_t>(id_bytes)), check_ptr(dlogits, es)});
+    if (st != SAR_OK) return st;
+    const RouteArgs a = {logits,  ldl, const_cast<void*>(ids), const_cast<void*>(dweights), dlogits, ldd, tokens, topk,
+                         experts, softmax};
+    return to_status(launch_expert_route_backward(dtype, wdtype, id_bytes, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+SAR_API size_t sar_expert_layer_workspace_bytes(size_t tokens, int topk, int experts, size_t cols, size_t hidden) {
+    if (!layer_sizes_ok(tokens, topk, experts, cols, hidden)) return 0;
+    return expert_layer_workspace_bytes(tokens * static_cast<size_t>(topk), cols, hidden);
+}
+
+SAR_API sar_status sar_expert_layer(const void* x, size_t ldx, const void* ids, int id_bytes, const void* weights,
+                                    const void* w_in, const void* w_out, void* out, size_t ldo, size_t tokens,
+                                    int topk, int experts, size_t cols, size_t hidden, int gated,
+                                    sar_activation activation, sar_dtype dtype, sar_dtype wdtype, void* workspace,
+                                    size_t workspace_bytes, sar_stream_t stream) {
+    if (!dtypes_ok(dtype, wdtype)) return SAR_ERR_UNSUPPORTED_DTYPE;
+    const size_t es = esize_of(dtype);
+    if ((id_bytes != 4 && id_bytes != 8) || !layer_sizes_ok(tokens, topk, experts, cols, hidden) ||
+        activation < SAR_ACT_SILU || activation > SAR_ACT_RELU || !extent_fits(tokens, cols, ldx, es) ||
+        !extent_fits(tokens, cols, ldo, es))
+        return SAR_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0) return SAR_OK;
+    sar_status st = first_error({check_ptr(x, es), check_ptr(ids, static_cast<size_t>(id_bytes)),
+                                 check_optional(weights, esize_of(wdtype)), check_ptr(out, es)});
+    if (st == SAR_OK && hidden != 0) st = first_error({check_ptr(w_in, es), check_ptr(w_out, es)});
+    if (st != SAR_OK) return st;
+    if (workspace == nullptr || workspace_bytes < sar_expert_layer_workspace_bytes(tokens, topk, experts, cols, hidden))
+        return SAR_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return SAR_ERR_MISALIGNED;
+    const LayerArgs a = {x,    ldx,     ids, weights, w_in, w_out, out, ldo, static_cast<int>(tokens), topk, experts,
+                         static_cast<int>(cols), static_cast<int>(hidden), gated != 0, activation, workspace};
+    return to_status(launch_expert_layer(dtype, wdtype, id_bytes, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+SAR_API size_t sar_orthogonalize_workspace_bytes(size_t batch, size_t rows, size_t cols) {
+    if (!orthogonalize_sizes_ok(batch, rows, cols)) return 0;
+    return orthogonalize_workspace_bytes(batch, rows, cols);
+}
+
+SAR_API sar_status sar_orthogonalize(const void* g, size_t ldg, size_t gstride, void* out, size_t ldo,
+                                     size_t ostride, size_t batch, size_t rows, size_t cols, int steps, float a,
+                                     float b, float c, float eps, float scale, sar_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, sar_stream_t stream) {
+    if (!wide_dtype(dtype)) return SAR_ERR_UNSUPPORTED_DTYPE;
+    const size_t es = esize_of(dtype);
+    if (!orthogonalize_sizes_ok(batch, rows, cols) || steps < 1 || steps > 64 || !(eps >= 0.0f) || std::isinf(eps) ||
+        !std::isfinite(scale) || !extent_fits(rows, cols, ldg, es) || !extent_fits(rows, cols, ldo, es))
+        return SAR_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0 || cols == 0) return SAR_OK;
+    const size_t last = (rows - 1) * ldo + cols;
+    if (batch > 1 && (ostride < last || !extent_fits(batch, 0, ostride, es) || !extent_fits(batch, 0, gstride, es)))
+        return SAR_ERR_INVALID_ARG;
+    const double grown = newton_schulz_bound(a, b, c, steps);
+    if (!(grown <= 4.0)) return SAR_ERR_INVALID_ARG;
+    const sar_status st = first_error({check_ptr(g, es), check_ptr(out, es)});
+    if (st != SAR_OK) return st;
+    if (workspace == nullptr || workspace_bytes < orthogonalize_workspace_bytes(batch, rows, cols)) return SAR_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return SAR_ERR_MISALIGNED;
+    const OrthogonalizeArgs o = {g, ldg, gstride, out, ldo, ostride, batch, rows, cols, steps, a, b, c, eps, scale,
+                                 static_cast<float>(grown), workspace};
+    return to_status(launch_orthogonalize(dtype, o, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

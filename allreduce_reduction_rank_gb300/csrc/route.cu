@@ -1,0 +1,196 @@
+// route.cu -- the router: each token's best experts by their logits, the
+// weights' softmax, and the logits' gradient.
+//
+// A warp takes a token.  Lane l holds the logits l, l + 32, ...: a row is read
+// once, in whole lines.  The topk largest are taken out one after another; a
+// logit is compared as the whole number of the same order (route_key), so that
+// infinities, NaN and -0 need no cases of their own.
+#include <type_traits>
+
+#include "sar_device.cuh"
+#include "sar_internal.h"
+
+namespace sar {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr uint32_t kMasked = 0x007FFFFFu;      // the key of minus infinity
+
+// Ascending with the value; -0 as +0, NaN above all.
+__device__ __forceinline__ uint32_t route_key(float x) {
+    if (x != x) return 0xFFFFFFFFu;
+    const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float route_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? (key == 0xFFFFFFFFu ? 0x7FFFFFFFu : key & 0x7FFFFFFFu) : ~key);
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+    return x;
+}
+
+template <int DT, int WDT, typename Id, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
+    pdl_wait();
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const size_t t = static_cast<size_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (t >= a.tokens) return;
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < a.experts ? route_key(load_elem<DT>(a.logits, t * a.ldl + static_cast<size_t>(e))) : 0u;
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    const uint32_t top_key = __reduce_max_sync(0xFFFFFFFFu, best);
+    const float top = top_key > kMasked ? route_value(top_key) : 0.0f;
+    float total = 0.0f;
+    if (a.softmax == SAR_SOFTMAX_ALL) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > kMasked) total = __fadd_rn(total, expf(__fsub_rn(route_value(key[i]), top)));
+        total = warp_sum(total);
+    }
+    float mine = 0.0f;                         // lane j: the j-th choice
+    int id = -1;
+    for (int j = 0; j < a.topk; ++j) {
+        uint32_t local = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > local) local = key[i], at = i;
+        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, local);
+        if (most <= kMasked) break;
+        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, local == most ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == static_cast<uint32_t>(i * 32 + lane)) key[i] = 0;
+        if (lane == j) id = static_cast<int>(e), mine = expf(__fsub_rn(route_value(most), top));
+    }
+    if (a.softmax == SAR_SOFTMAX_CHOSEN) total = warp_sum(mine);
+    if (lane < a.topk) {
+        const size_t s = t * static_cast<size_t>(a.topk) + static_cast<size_t>(lane);
+        static_cast<Id*>(a.ids)[s] = id;
+        store_elem<WDT>(a.weights, s, id >= 0 ? __fdiv_rn(mine, total) : 0.0f);
+    }
+}
+
+template <int DT, int WDT, typename Id, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteArgs a) {
+    pdl_wait();
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const size_t t = static_cast<size_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (t >= a.tokens) return;
+    // lane j: the j-th choice; the first of those with one id stands for all
+    int id = -1;
+    float dw = 0.0f;
+    if (lane < a.topk) {
+        const size_t s = t * static_cast<size_t>(a.topk) + static_cast<size_t>(lane);
+        const Id given = static_cast<const Id*>(a.ids)[s];
+        if (given >= 0 && given < static_cast<Id>(a.experts)) {
+            id = static_cast<int>(given);
+            dw = load_elem<WDT>(a.weights, s);
+        }
+    }
+    bool first = id >= 0;
+    float given = 0.0f;
+    for (int j = 0; j < a.topk; ++j) {
+        const int other = __shfl_sync(0xFFFFFFFFu, id, j);
+        const float g = __shfl_sync(0xFFFFFFFFu, dw, j);
+        if (other == id) {
+            given = __fadd_rn(given, g);
+            if (j < lane) first = false;
+        }
+    }
+    float x[V];
+    float top = -INFINITY;
+    bool nan = false;
+    const float chosen = first ? load_elem<DT>(a.logits, t * a.ldl + static_cast<size_t>(id)) : -INFINITY;
+    if (a.softmax == SAR_SOFTMAX_ALL) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = i * 32 + lane;
+            x[i] = e < a.experts ? load_elem<DT>(a.logits, t * a.ldl + static_cast<size_t>(e)) : -INFINITY;
+            top = fmaxf(top, x[i]);
+            nan |= x[i] != x[i];
+        }
+    } else {
+        top = chosen;
+        nan = chosen != chosen;
+    }
+    nan = __any_sync(0xFFFFFFFFu, nan);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (nan) top = __uint_as_float(0x7FFFFFFFu);
+    const bool empty = top == -INFINITY;
+    const float p0 = first && !empty ? expf(__fsub_rn(chosen, top)) : 0.0f;
+    float total = p0;
+    if (a.softmax == SAR_SOFTMAX_ALL) {
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = empty || i * 32 + lane >= a.experts ? 0.0f : expf(__fsub_rn(x[i], top));
+            total = __fadd_rn(total, x[i]);
+        }
+    }
+    total = warp_sum(total);
+    const float scale = empty ? 0.0f : __fdiv_rn(1.0f, total);
+    const float p = __fmul_rn(p0, scale);
+    const float down = warp_sum(first ? __fmul_rn(p, given) : 0.0f);
+    const size_t row = t * a.ldd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        if (e < a.experts)
+            store_elem<DT>(a.dlogits, row + static_cast<size_t>(e),
+                           a.softmax == SAR_SOFTMAX_ALL ? __fmul_rn(__fmul_rn(x[i], scale), -down) : 0.0f);
+    }
+    __syncwarp();                              // the chosen ones again, after the row
+    if (first) store_elem<DT>(a.dlogits, row + static_cast<size_t>(id), __fmul_rn(p, __fsub_rn(given, down)));
+}
+
+template <int DT, int WDT, typename Id>
+cudaError_t launch(bool backward, const RouteArgs& a, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>((a.tokens + kWarps - 1) / kWarps)), block(kWarps * 32);
+    const auto run = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        return backward ? launch_kernel(route_backward_kernel<DT, WDT, Id, V>, grid, block, s, a)
+                        : launch_kernel(route_kernel<DT, WDT, Id, V>, grid, block, s, a);
+    };
+    if (a.experts <= 64) return run(std::integral_constant<int, 2>());
+    if (a.experts <= 128) return run(std::integral_constant<int, 4>());
+    if (a.experts <= 256) return run(std::integral_constant<int, 8>());
+    if (a.experts <= 512) return run(std::integral_constant<int, 16>());
+    return run(std::integral_constant<int, 32>());
+}
+
+template <int DT> cudaError_t launch(sar_dtype wdt, int id_bytes, bool backward, const RouteArgs& a, cudaStream_t s) {
+    if (wdt == SAR_FP32)
+        return id_bytes == 8 ? launch<DT, SAR_FP32, int64_t>(backward, a, s) : launch<DT, SAR_FP32, int32_t>(backward, a, s);
+    return id_bytes == 8 ? launch<DT, DT, int64_t>(backward, a, s) : launch<DT, DT, int32_t>(backward, a, s);
+}
+
+cudaError_t launch(sar_dtype dt, sar_dtype wdt, int id_bytes, bool backward, const RouteArgs& a, cudaStream_t s) {
+    switch (dt) {
+    case SAR_BF16: return launch<SAR_BF16>(wdt, id_bytes, backward, a, s);
+    case SAR_FP16: return launch<SAR_FP16>(wdt, id_bytes, backward, a, s);
+    default: return launch<SAR_FP32>(wdt, id_bytes, backward, a, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_expert_route(sar_dtype dt, sar_dtype wdt, int id_bytes, const RouteArgs& a, cudaStream_t s) {
+    return launch(dt, wdt, id_bytes, false, a, s);
+}
+
+cudaError_t launch_expert_route_backward(sar_dtype dt, sar_dtype wdt, int id_bytes, const RouteArgs& a, cudaStream_t s) {
+    return launch(dt, wdt, id_bytes, true, a, s);
+}
+
+}  // namespace sar

@@ -209,4 +209,53 @@ cudaError_t launch_expert_dispatch(size_t esize, const ExpertArgs& a, cudaStream
 cudaError_t launch_expert_combine(sar_dtype dt, sar_dtype wdt, const ExpertArgs& a, cudaStream_t stream);
 cudaError_t launch_expert_combine_backward(sar_dtype dt, sar_dtype wdt, const ExpertArgs& a, cudaStream_t stream);
 
+
+// The router (route.cu).
+struct RouteArgs {
+    const void* logits;
+    size_t ldl;
+    void* ids;               // read by the backward call
+    void* weights;           // dweights of the backward call
+    void* dlogits;           // backward call only
+    size_t ldd;
+    size_t tokens;
+    int topk, experts;
+    sar_softmax softmax;
+};
+cudaError_t launch_expert_route(sar_dtype dt, sar_dtype wdt, int id_bytes, const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_expert_route_backward(sar_dtype dt, sar_dtype wdt, int id_bytes, const RouteArgs& a, cudaStream_t stream);
+
+// The expert layer of a few tokens (expert_layer.cu).
+struct LayerArgs {
+    const void* x;
+    size_t ldx;
+    const void* ids;
+    const void* weights;     // null: every weight is 1
+    const void* w_in;
+    const void* w_out;
+    void* out;
+    size_t ldo;
+    int tokens, topk, experts, cols, hidden;
+    bool gated;
+    sar_activation activation;
+    void* workspace;
+};
+size_t expert_layer_workspace_bytes(size_t slots, size_t cols, size_t hidden);
+cudaError_t launch_expert_layer(sar_dtype dt, sar_dtype wdt, int id_bytes, const LayerArgs& a, cudaStream_t stream);
+
+// Newton-Schulz iteration (orthogonalize.cu).
+struct OrthogonalizeArgs {
+    const void* g;
+    size_t ldg, gstride;
+    void* out;
+    size_t ldo, ostride;
+    size_t batch, rows, cols;
+    int steps;
+    float a, b, c, eps, scale;
+    float grown;             // no singular value of an iterate is above
+    void* workspace;
+};
+size_t orthogonalize_workspace_bytes(size_t batch, size_t rows, size_t cols);
+cudaError_t launch_orthogonalize(sar_dtype dt, const OrthogonalizeArgs& a, cudaStream_t stream);
+
 }  // namespace sar

@@ -606,6 +606,155 @@ SAR_API sar_status sar_expert_combine_backward(const void* dout, size_t ldo, con
                                                sar_stream_t stream);
 
 /*
+ * The router in front of sar_expert_sort and sar_expert_layer, the whole
+ * expert layer of a few tokens, and the update of a matrix from its summed
+ * gradient.  The conventions of the operators above hold.
+ */
+
+/* Largest topk of the sar_expert_route calls. */
+#define SAR_MAX_TOPK 32
+
+/* Whose softmax the weights of sar_expert_route are. */
+typedef enum {
+    SAR_SOFTMAX_CHOSEN = 0,  /* over the token's chosen logits: the weights' sum is 1 */
+    SAR_SOFTMAX_ALL = 1      /* over all of the token's logits */
+} sar_softmax;
+
+/*
+ * sar_expert_route -- for every token the topk largest of its `experts`
+ * logits, in descending order, the lower id first where logits are equal
+ * (-0 equals 0), and their softmax:
+ *   ids[t * topk + j]     = the j-th choice
+ *   weights[t * topk + j] = R(exp(l_j - max) / sum exp(l - max))
+ * with the sum over the chosen logits or over all of them.  A logit of minus
+ * infinity (a masked expert) is never chosen: where fewer than topk others are
+ * left, the rest of the ids are -1 and their weights 0, which the sar_expert_*
+ * calls take as dropped.  A NaN counts as larger than every number; a row with
+ * a NaN (SAR_SOFTMAX_CHOSEN: with a chosen one) or plus infinity has NaN for
+ * the formula's weights.
+ *
+ * logits  : tokens x experts of type dtype, leading dimension ldl.
+ * ids     : tokens * topk signed integers of id_bytes (4 or 8) bytes.
+ * weights : tokens * topk values of type wdtype.
+ * 1 <= topk <= SAR_MAX_TOPK, topk <= experts <= SAR_MAX_EXPERTS, and tokens *
+ * topk at most 2^31 - 1, else SAR_ERR_INVALID_ARG.
+ */
+SAR_API sar_status sar_expert_route(const void* logits, size_t ldl, void* ids, int id_bytes, void* weights,
+                                    size_t tokens, int topk, int experts, sar_softmax softmax, sar_dtype dtype,
+                                    sar_dtype wdtype, sar_stream_t stream);
+
+/*
+ * sar_expert_route_backward -- the gradient of sar_expert_route's weights with
+ * respect to the logits, the choice held fixed.  With p the softmax (computed
+ * again from the logits), g[e] the sum of dweights over the token's slots that
+ * chose e, and s the sum of p[e] * g[e] over the chosen experts:
+ *   dlogits[t][e] = R(p[e] * (g[e] - s))      SAR_SOFTMAX_ALL: for every e;
+ * SAR_SOFTMAX_CHOSEN: for the chosen ones, 0 for the others.  Slots whose id is
+ * not in 0 .. experts - 1 count for nothing, also in the softmax over the
+ * chosen; an id that a token has twice is one expert, whose gradients add up.
+ * A token without a chosen expert, or with minus infinity for all of its
+ * logits, gets zeros.  dweights of dropped slots are not read.
+ *
+ * dlogits may be logits (same ld).  SAR_SOFTMAX_CHOSEN reads the chosen logits
+ * only.
+ */
+SAR_API sar_status sar_expert_route_backward(const void* dweights, const void* logits, size_t ldl, const void* ids,
+                                             int id_bytes, void* dlogits, size_t ldd, size_t tokens, int topk,
+                                             int experts, sar_softmax softmax, sar_dtype dtype, sar_dtype wdtype,
+                                             sar_stream_t stream);
+
+/* Largest tokens * topk of sar_expert_layer. */
+#define SAR_EXPERT_LAYER_MAX_SLOTS 1024
+
+typedef enum {
+    SAR_ACT_SILU = 0,  /* z / (1 + exp(-z)) */
+    SAR_ACT_GELU = 1,  /* z / 2 * (1 + erf(z / sqrt(2))) */
+    SAR_ACT_RELU = 2   /* z where z > 0, 0 elsewhere (NaN stays NaN) */
+} sar_activation;
+
+/*
+ * sar_expert_layer_workspace_bytes -- bytes of the workspace that
+ * sar_expert_layer needs (0 for arguments that it refuses; never 0 otherwise).
+ */
+SAR_API size_t sar_expert_layer_workspace_bytes(size_t tokens, int topk, int experts, size_t cols, size_t hidden);
+
+/*
+ * sar_expert_layer -- the whole expert layer of a few tokens, for serving: for
+ * every token, with e = ids[t * topk + j],
+ *   z      = w_in[e] . x[t]                                 (each row's product)
+ *   h[i]   = act(z[i]) * z[hidden + i]        (gated != 0; otherwise act(z[i]))
+ *   out[t] = R(sum_j weights[t * topk + j] * (w_out[e] . h))
+ * over the kept choices j in ascending order.  An id outside 0 .. experts - 1
+ * drops its slot: its weight is not read.  A token without a kept slot gets
+ * zeros.  An expert's matrices are read once whatever the number of its
+ * tokens (up to 32; once more for every further 32), and those of experts
+ * without a token not at all.
+ *
+ * x       : tokens x cols, leading dimension ldx.
+ * weights : optional (NULL: 1), tokens * topk values of type wdtype.
+ * w_in    : experts x (gated ? 2 * hidden : hidden) x cols, dense.
+ * w_out   : experts x cols x hidden, dense.
+ * out     : tokens x cols, leading dimension ldo.
+ * workspace : 16-byte aligned, of sar_expert_layer_workspace_bytes bytes; its
+ *           contents do not matter before and after.  A smaller
+ *           workspace_bytes returns SAR_ERR_INVALID_ARG.
+ * z and h are kept in binary32 precision (h as two numbers of the weights'
+ * type where those have 16 bits).
+ * tokens * topk at most SAR_EXPERT_LAYER_MAX_SLOTS, topk >= 1, 1 <= experts <=
+ * SAR_MAX_EXPERTS, cols and hidden at most 2^20, else SAR_ERR_INVALID_ARG;
+ * longer batches go through sar_expert_sort, sar_expert_dispatch, a matrix
+ * product for each segment and sar_expert_combine.  hidden == 0 gives zeros.
+ */
+SAR_API sar_status sar_expert_layer(const void* x, size_t ldx, const void* ids, int id_bytes, const void* weights,
+                                    const void* w_in, const void* w_out, void* out, size_t ldo, size_t tokens,
+                                    int topk, int experts, size_t cols, size_t hidden, int gated,
+                                    sar_activation activation, sar_dtype dtype, sar_dtype wdtype, void* workspace,
+                                    size_t workspace_bytes, sar_stream_t stream);
+
+/* Largest rows and cols of sar_orthogonalize. */
+#define SAR_ORTHOGONALIZE_MAX_SIDE 65536
+
+/*
+ * sar_orthogonalize_workspace_bytes -- bytes of the workspace that
+ * sar_orthogonalize needs (0 for sizes that it refuses; never 0 otherwise).
+ */
+SAR_API size_t sar_orthogonalize_workspace_bytes(size_t batch, size_t rows, size_t cols);
+
+/*
+ * sar_orthogonalize -- Newton-Schulz iteration towards the nearest
+ * (semi-)orthogonal matrix, for each of `batch` matrices:
+ *   X = g / (sqrt(sum g^2) + eps)
+ *   steps times:  A = X X^T,  X = a X + (b A + c A A) X
+ *   out = R(scale * X)
+ * (with X^T X on the right for rows > cols, which is the same in exact
+ * arithmetic).  It is what the Muon optimiser applies to a matrix in place of
+ * its momentum, here of a gradient that the allreduce has summed; a matrix of
+ * zeros gives zeros, one with an infinity or NaN gives NaN throughout.
+ *
+ * Products are held to binary32's precision whatever the type of g: the steps
+ * multiply small singular values, and the errors in their directions, by a
+ * each (485 times in five steps of 3.4445).
+ *
+ * g, out  : matrix i starts at i * gstride (ostride) elements; leading
+ *           dimensions ldg, ldo.  out may be g (same ld and stride).  The
+ *           matrices of out must not overlap: ostride at least (rows - 1) *
+ *           ldo + cols if batch > 1.
+ * steps   : 1 .. 64.
+ * a, b, c : finite, such that no singular value grows past 4: |a s + b s^3 +
+ *           c s^5| <= 4 for every s that the steps can reach from 0 .. 1.
+ * eps     : not negative and finite.  scale: finite.
+ * rows, cols at most SAR_ORTHOGONALIZE_MAX_SIDE, batch at most 65535.  Others
+ * return SAR_ERR_INVALID_ARG.
+ * workspace : 16-byte aligned, of sar_orthogonalize_workspace_bytes bytes; its
+ *           contents do not matter before and after.  A smaller
+ *           workspace_bytes returns SAR_ERR_INVALID_ARG.
+ */
+SAR_API sar_status sar_orthogonalize(const void* g, size_t ldg, size_t gstride, void* out, size_t ldo,
+                                     size_t ostride, size_t batch, size_t rows, size_t cols, int steps, float a,
+                                     float b, float c, float eps, float scale, sar_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, sar_stream_t stream);
+
+/*
  * sar_read_device_status -- synchronises `stream`, reads *d_status and returns
  * it as a sar_status (SAR_OK or SAR_ERR_TIMEOUT), or SAR_ERR_CUDA if the copy
  * fails.  Not for use inside a CUDA graph capture.

@@ -41,7 +41,7 @@ SOURCES = ["ll_writeback.cu", "ll_fused.cu", "ll_cluster.cu", "ll_cta.cu", "rsag
            "noalloc.cu"]
 # The torch module's; all are compiled again for another interpreter or torch.
 BINDING_SOURCES = ["torch_binding.cpp", "torch_binding_block.cpp"]
-HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh", "layer_norm_ring.cuh"]
+HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh", "layer_norm_ring.cuh", "tensor_core.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-std=c++17", "-lineinfo",

@@ -324,7 +324,7 @@ SAR_API sar_status sar_orthogonalize(const void* g, size_t ldg, size_t gstride, 
     if (batch > 1 && (ostride < last || !extent_fits(batch, 0, ostride, es) || !extent_fits(batch, 0, gstride, es)))
         return SAR_ERR_INVALID_ARG;
     const double grown = newton_schulz_bound(a, b, c, steps);
-    if (!(grown <= 4.0)) return SAR_ERR_INVALID_ARG;
+    if (!(grown <= 4.0) || !(std::fabs(a) >= 1.0f)) return SAR_ERR_INVALID_ARG;
     const sar_status st = first_error({check_ptr(g, es), check_ptr(out, es)});
     if (st != SAR_OK) return st;
     if (workspace == nullptr || workspace_bytes < orthogonalize_workspace_bytes(batch, rows, cols)) return SAR_ERR_INVALID_ARG;

@@ -733,15 +733,17 @@ SAR_API size_t sar_orthogonalize_workspace_bytes(size_t batch, size_t rows, size
  *
  * Products are held to binary32's precision whatever the type of g: the steps
  * multiply small singular values, and the errors in their directions, by a
- * each (485 times in five steps of 3.4445).
+ * each (485 times in five steps of 3.4445).  Errors are relative to the norm of
+ * a step's X: elements and singular values below 2^-30 of it may be lost.
  *
  * g, out  : matrix i starts at i * gstride (ostride) elements; leading
  *           dimensions ldg, ldo.  out may be g (same ld and stride).  The
  *           matrices of out must not overlap: ostride at least (rows - 1) *
  *           ldo + cols if batch > 1.
  * steps   : 1 .. 64.
- * a, b, c : finite, such that no singular value grows past 4: |a s + b s^3 +
- *           c s^5| <= 4 for every s that the steps can reach from 0 .. 1.
+ * a, b, c : finite, |a| at least 1, and such that no singular value grows past
+ *           4: |a s + b s^3 + c s^5| <= 4 for every s that the steps can reach
+ *           from 0 .. 1.
  * eps     : not negative and finite.  scale: finite.
  * rows, cols at most SAR_ORTHOGONALIZE_MAX_SIDE, batch at most 65535.  Others
  * return SAR_ERR_INVALID_ARG.

@@ -93,7 +93,7 @@ def test_orthogonalize_refusals(sar):
     for kw in (dict(g=None), dict(out=None), dict(ws=None), dict(n=need - 1), dict(ldg=47), dict(ldo=47), dict(os=63 * 48 + 47),
                dict(gs=HUGE), dict(os=HUGE), dict(batch=65536), dict(rows=65537), dict(cols=65537, ldg=65537, ldo=65537),
                dict(steps=0), dict(steps=65), dict(eps=-1e-9), dict(eps=nan), dict(eps=inf), dict(scale=nan), dict(scale=inf),
-               dict(a=nan), dict(b=inf), dict(c=nan), dict(a=4.1), dict(a=2.0, b=0.0, c=0.0), dict(a=0.0, b=0.0, c=5.0),
+               dict(a=nan), dict(b=inf), dict(c=nan), dict(a=0.99), dict(a=0.0, b=1.0, c=0.0), dict(a=4.1), dict(a=2.0, b=0.0, c=0.0), dict(a=0.0, b=0.0, c=5.0),
                dict(a=1.0, b=8.0, c=-8.5)):
         assert call(**kw) == sar.SAR_ERR_INVALID_ARG, kw
     for kw in (dict(g=A + 1), dict(out=B + 1), dict(ws=E + 8)):

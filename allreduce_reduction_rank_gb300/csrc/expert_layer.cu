@@ -1,78 +1,503 @@
-// expert_layer.cu -- the whole expert layer of a few tokens.
+// expert_layer.cu -- the whole expert layer of a few tokens, in two kernels:
+//   in_kernel    h = act(w_in[e] . x) (* the second half)   for every slot
+//   out_kernel   out = sum_j weight_j * (w_out[e] . h_j)     for every token
+//
+// A slot is one choice of one token.  The time is that of reading the chosen
+// experts' weights once: 2 to 4 operations for a byte of them, so the tensor
+// cores are not what matters, but how many bytes are on their way.  Warps load
+// 16-byte pieces of the weights straight into registers, which are the left
+// operand of mma.sync (16 rows of weights by 8 slots): a lane's piece holds
+// consecutive k, and as the order of k within a product does not matter, the
+// pieces are taken as they come, with the slots' values at the same k.  (On the
+// 5th-generation tensor cores the weights would have to pass through shared
+// memory for 128 rows at a time, too coarse to spread few experts evenly.)
+//
+// Both kernels first sort the slots by expert into items of up to 8, 16 or 32
+// slots of one expert, each block for itself.  The sort is stable, so that every
+// block has the same items.
+//
+// Precision: x and 16-bit weights are multiplied as they are, sums in binary32.
+// h is not rounded to the type: bf16 weights meet it as two bf16 numbers (16
+// bits), fp16 ones (whose range it may leave) as two tf32 numbers (21 bits) with
+// the weights widened exactly; binary32 values on both sides are two tf32
+// numbers each, all four products.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
 #include "sar_device.cuh"
 #include "sar_internal.h"
 
 namespace sar {
 namespace {
 
-constexpr int kWarps = 8;
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-    return x;
-}
+constexpr int kSMs = 152;
+constexpr int kMaxSlots = SAR_EXPERT_LAYER_MAX_SLOTS;
 
 __device__ __forceinline__ float activate(float z, sar_activation act) {
     if (act == SAR_ACT_SILU) return __fdiv_rn(z, __fadd_rn(1.0f, expf(-z)));
+    // erfc keeps its digits where 1 + erf would cancel
     if (act == SAR_ACT_GELU) return __fmul_rn(__fmul_rn(0.5f, z), erfcf(__fmul_rn(z, -0.70710678f)));
     return z <= 0.0f ? 0.0f : z;
 }
 
-template <int DT> __device__ float dot(const void* w, size_t at, const void* x, size_t xat, int n, int lane) {
-    float s = 0.0f;
-    for (int k = lane; k < n; k += 32) s = __fmaf_rn(load_elem<DT>(w, at + k), load_elem<DT>(x, xat + k), s);
-    return warp_sum(s);
+// ---------------------------------------------------------------------------
+// The slots by expert.
+// ---------------------------------------------------------------------------
+struct Items {
+    int count;
+    int16_t expert[kMaxSlots], first[kMaxSlots], slots[kMaxSlots];   // of an item: its slots are sorted[first ..]
+    int16_t sorted[kMaxSlots];
+    int16_t of[kMaxSlots], rank[kMaxSlots];                          // a slot's expert, and its place among that one's
+    int tally[SAR_MAX_EXPERTS];                                      // an expert's slots, then where they start
+};
+
+__device__ __forceinline__ int expert_of(const LayerArgs& a, int id_bytes, int slot) {
+    const int64_t e = id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[slot] : static_cast<const int32_t*>(a.ids)[slot];
+    return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
 }
 
-__device__ __forceinline__ int expert_of(const void* ids, int id_bytes, int slot, int experts) {
-    const int64_t e = id_bytes == 8 ? static_cast<const int64_t*>(ids)[slot] : static_cast<const int32_t*>(ids)[slot];
-    return e >= 0 && e < experts ? static_cast<int>(e) : -1;
-}
-
-template <int DT> __global__ void in_kernel(LayerArgs a, int id_bytes) {
-    pdl_wait();
-    const int lane = threadIdx.x & 31, i = blockIdx.x * kWarps + (threadIdx.x >> 5), slot = blockIdx.y;
-    const int e = expert_of(a.ids, id_bytes, slot, a.experts);
-    if (i >= a.hidden || e < 0) return;
-    const size_t rows = static_cast<size_t>(a.gated ? 2 : 1) * a.hidden, k = a.cols, xat = (slot / a.topk) * a.ldx;
-    const float z = dot<DT>(a.w_in, (e * rows + i) * k, a.x, xat, a.cols, lane);
-    float h = activate(z, a.activation);
-    if (a.gated) h = __fmul_rn(h, dot<DT>(a.w_in, (e * rows + a.hidden + i) * k, a.x, xat, a.cols, lane));
-    if (lane == 0) static_cast<float*>(a.workspace)[static_cast<size_t>(slot) * a.hidden + i] = h;
-}
-
-template <int DT, int WDT> __global__ void out_kernel(LayerArgs a, int id_bytes) {
-    pdl_wait();
-    const int lane = threadIdx.x & 31, c = blockIdx.x * kWarps + (threadIdx.x >> 5), t = blockIdx.y;
-    if (c >= a.cols) return;
-    float total = 0.0f;
-    for (int j = 0; j < a.topk; ++j) {
-        const int slot = t * a.topk + j, e = expert_of(a.ids, id_bytes, slot, a.experts);
-        if (e < 0) continue;
-        float s = 0.0f;
-        const float* h = static_cast<const float*>(a.workspace) + static_cast<size_t>(slot) * a.hidden;
-        for (int k = lane; k < a.hidden; k += 32)
-            s = __fmaf_rn(load_elem<DT>(a.w_out, (static_cast<size_t>(e) * a.cols + c) * a.hidden + k), h[k], s);
-        s = warp_sum(s);
-        total = __fmaf_rn(a.weights != nullptr ? load_elem<WDT>(a.weights, slot) : 1.0f, s, total);
+// The items of `have` slots at `start`, up to `per` slots each, from item `at` on.
+__device__ __forceinline__ void write_items(Items& it, int expert, int start, int have, int at, int per) {
+    for (int done = 0; done < have; done += per, ++at) {
+        it.expert[at] = static_cast<int16_t>(expert);
+        it.first[at] = static_cast<int16_t>(start + done);
+        it.slots[at] = static_cast<int16_t>(min(per, have - done));
     }
-    if (lane == 0) store_elem<DT>(a.out, t * a.ldo + c, total);
+}
+
+__device__ __forceinline__ int scan_before(int v, int lane) {        // sum over the lanes below
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int other = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += other;
+    }
+    return s - v;
+}
+
+// All threads of the block.
+__device__ void sort_slots(Items& it, const LayerArgs& a, int id_bytes, int per) {
+    const int slots = a.tokens * a.topk, t = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x), lane = t & 31;
+    if (slots <= 32) {                                               // one warp, without a count for each expert
+        if (t < 32) {
+            const int e = lane < slots ? expert_of(a, id_bytes, lane) : -1;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, e), below = (1u << lane) - 1u;
+            const bool leads = e >= 0 && (same & below) == 0u;
+            const int have = leads ? __popc(same) : 0, items = (have + per - 1) / per;
+            const int before = scan_before(items << 16 | have, lane);
+            const int start = __shfl_sync(0xFFFFFFFFu, before & 0xFFFF, __ffs(same) - 1);
+            if (e >= 0) it.sorted[start + __popc(same & below)] = static_cast<int16_t>(lane);
+            write_items(it, e, before & 0xFFFF, have, before >> 16, per);
+            if (lane == 31) it.count = (before >> 16) + items;
+        }
+        __syncthreads();
+        return;
+    }
+    for (int e = t; e < a.experts; e += threads) it.tally[e] = 0;
+    __syncthreads();
+    for (int s = t; s < slots; s += threads) it.of[s] = static_cast<int16_t>(expert_of(a, id_bytes, s));
+    __syncthreads();
+    if (t < 32) {
+        for (int s0 = 0; s0 < slots; s0 += 32) {                     // places within an expert, in the order of the slots
+            const int s = s0 + lane, e = s < slots ? it.of[s] : -1;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
+            const int before = e >= 0 ? it.tally[e] : 0;
+            __syncwarp();
+            if (e >= 0) {
+                it.rank[s] = static_cast<int16_t>(before + __popc(same & ((1u << lane) - 1u)));
+                if (lane == __ffs(same) - 1) it.tally[e] = before + __popc(same);
+            }
+            __syncwarp();
+        }
+        int done = 0;                                                // items << 16 | slots so far
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+            const int e = e0 + lane, have = e < a.experts ? it.tally[e] : 0, v = ((have + per - 1) / per) << 16 | have;
+            const int before = done + scan_before(v, lane);
+            if (e < a.experts) it.tally[e] = before & 0xFFFF;
+            write_items(it, e, before & 0xFFFF, have, before >> 16, per);
+            done = __shfl_sync(0xFFFFFFFFu, before + v, 31);
+        }
+        if (lane == 0) it.count = done >> 16;
+    }
+    __syncthreads();
+    for (int s = t; s < slots; s += threads) {
+        const int e = it.of[s];
+        if (e >= 0) it.sorted[it.tally[e] + it.rank[s]] = static_cast<int16_t>(s);
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// Operands.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint4 load_weights(const uint4* p) {      // read once: not kept in L1
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// 16 bytes of a row of n elements, from element k on; zeros past its end.  kVec:
+// rows are whole pieces on 16-byte boundaries.
+template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 piece(const void* row, int k, int n, bool there) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    constexpr int ve = Elem<DT>::kVE;
+    if (kVec) {
+        if (there && k < n) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<size_t>(k) * Elem<DT>::kSize);
+            v = kWeights ? load_weights(p) : *p;
+        }
+    } else {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < ve; ++i)
+            if (there && k + i < n) {
+                if (Elem<DT>::kSize == 4)
+                    w[i & 3] = static_cast<const uint32_t*>(row)[k + i];
+                else
+                    w[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(row)[k + i]) << (16 * (i & 1));
+            }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return v;
+}
+
+template <int DT> __device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                         uint32_t b1) {
+    if (DT == SAR_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// v = hi + lo, both tf32 (11 bits): hi cut off, which cannot overflow, lo rounded.
+// An infinity is all hi.
+__device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(v) & 0xFFFFE000u;
+    const float rest = fabsf(v) <= 0x1.fffffep127f ? __fsub_rn(v, __uint_as_float(hi)) : 0.0f;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+    if (v != v) hi = 0x7FFFFFFFu;
+}
+
+// v0, v1 = hi + lo as pairs of bf16: hi cut off, lo rounded.
+__device__ __forceinline__ void split_bf16(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+    const float most = 0x1.fffffep127f;
+    const uint32_t u0 = __float_as_uint(v0), u1 = __float_as_uint(v1);
+    hi = __byte_perm(v0 != v0 ? 0x7FFFFFFFu : u0, v1 != v1 ? 0x7FFFFFFFu : u1, 0x7632);
+    const float r0 = fabsf(v0) <= most ? __fsub_rn(v0, __uint_as_float(u0 & 0xFFFF0000u)) : 0.0f;
+    const float r1 = fabsf(v1) <= most ? __fsub_rn(v1, __uint_as_float(u1 & 0xFFFF0000u)) : 0.0f;
+    const float r[2] = {r0, r1};
+    lo = narrow_word<SAR_BF16>(r);
+}
+
+// A lane's piece of two rows of weights, ready to be multiplied by the slots of
+// any number of items' eights.
+template <int DT, bool kTwo> struct Left;       // kTwo: against h, in two numbers
+
+template <int DT> struct Left<DT, false> {      // 16-bit weights against x
+    uint32_t a[4], b[4];
+    __device__ __forceinline__ void set(const uint4& p, const uint4& q) {
+        a[0] = p.x, a[1] = p.y, a[2] = p.z, a[3] = p.w, b[0] = q.x, b[1] = q.y, b[2] = q.z, b[3] = q.w;
+    }
+    __device__ __forceinline__ void multiply(float (&d)[4], const uint4& x) const {
+        mma_16<DT>(d, a[0], b[0], a[1], b[1], x.x, x.y);
+        mma_16<DT>(d, a[2], b[2], a[3], b[3], x.z, x.w);
+    }
+};
+template <> struct Left<SAR_BF16, true> {
+    uint32_t a[4], b[4];
+    __device__ __forceinline__ void set(const uint4& p, const uint4& q) {
+        a[0] = p.x, a[1] = p.y, a[2] = p.z, a[3] = p.w, b[0] = q.x, b[1] = q.y, b[2] = q.z, b[3] = q.w;
+    }
+    __device__ __forceinline__ void multiply(float (&d)[4], const float (&h)[8]) const {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_bf16(h[2 * i], h[2 * i + 1], hi[i], lo[i]);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            mma_16<SAR_BF16>(d, a[i], b[i], a[i + 1], b[i + 1], lo[i], lo[i + 1]);
+            mma_16<SAR_BF16>(d, a[i], b[i], a[i + 1], b[i + 1], hi[i], hi[i + 1]);
+        }
+    }
+};
+template <> struct Left<SAR_FP16, true> {
+    float a[8], b[8];
+    __device__ __forceinline__ void set(const uint4& p, const uint4& q) {
+        widen_word<SAR_FP16>(p.x, a), widen_word<SAR_FP16>(p.y, a + 2), widen_word<SAR_FP16>(p.z, a + 4), widen_word<SAR_FP16>(p.w, a + 6);
+        widen_word<SAR_FP16>(q.x, b), widen_word<SAR_FP16>(q.y, b + 2), widen_word<SAR_FP16>(q.z, b + 4), widen_word<SAR_FP16>(q.w, b + 6);
+    }
+    __device__ __forceinline__ void multiply(float (&d)[4], const float (&h)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(h[i], h0, l0), split_tf32(h[i + 1], h1, l1);
+            const uint32_t a0 = __float_as_uint(a[i]), a1 = __float_as_uint(b[i]), a2 = __float_as_uint(a[i + 1]), a3 = __float_as_uint(b[i + 1]);
+            mma_tf32(d, a0, a1, a2, a3, l0, l1);
+            mma_tf32(d, a0, a1, a2, a3, h0, h1);
+        }
+    }
+};
+struct LeftFp32 {
+    uint32_t ah[4], al[4], bh[4], bl[4];
+    __device__ __forceinline__ void set(const uint4& p, const uint4& q) {
+        split_tf32(__uint_as_float(p.x), ah[0], al[0]), split_tf32(__uint_as_float(p.y), ah[1], al[1]);
+        split_tf32(__uint_as_float(p.z), ah[2], al[2]), split_tf32(__uint_as_float(p.w), ah[3], al[3]);
+        split_tf32(__uint_as_float(q.x), bh[0], bl[0]), split_tf32(__uint_as_float(q.y), bh[1], bl[1]);
+        split_tf32(__uint_as_float(q.z), bh[2], bl[2]), split_tf32(__uint_as_float(q.w), bh[3], bl[3]);
+    }
+    __device__ __forceinline__ void multiply(float (&d)[4], const float (&x)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(x[i], h0, l0), split_tf32(x[i + 1], h1, l1);
+            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], l0, l1);
+            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], h0, h1);
+            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], l0, l1);
+            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], h0, h1);
+        }
+    }
+    __device__ __forceinline__ void multiply(float (&d)[4], const uint4& x) const {
+        const float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+        multiply(d, v);
+    }
+};
+template <> struct Left<SAR_FP32, false> : LeftFp32 {};
+template <> struct Left<SAR_FP32, true> : LeftFp32 {};
+
+// What a slot brings: a piece of x, or of h (kVE binary32 values).
+template <int DT> struct FromX { using Type = uint4; };
+template <int DT> struct FromH { struct Type { float v[Elem<DT>::kVE]; }; };
+
+__host__ __device__ __forceinline__ int h_ld(int hidden) { return (hidden + 7) / 8 * 8; }
+
+template <int DT> __device__ __forceinline__ void load_h(typename FromH<DT>::Type& to, const float* h, int k, int n, bool there) {
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::kVE; i += 4) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (there && k + i < n) v = *reinterpret_cast<const float4*>(h + k + i);      // rows of h end in zeros
+        to.v[i] = v.x, to.v[i + 1] = v.y, to.v[i + 2] = v.z, to.v[i + 3] = v.w;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// h = act(w_in . x).  A block takes 16 rows of an item's expert (gated: 8 rows
+// and the 8 that belong to them, which meet in one lane's sums), its warps a
+// share of k each.
+// ---------------------------------------------------------------------------
+constexpr int kInWarps = 4;
+
+template <int DT, bool kVec, int N8>
+__global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_bytes, int row_tiles) {
+    constexpr int ve = Elem<DT>::kVE, step = 8 * ve;                 // 128 bytes of a row
+    __shared__ Items it;
+    __shared__ __align__(16) float parts[kInWarps][N8][32][4];
+    pdl_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // out_kernel may sort its slots meanwhile
+    sort_slots(it, a, id_bytes, 8 * N8);
+    const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
+    const int rows = a.gated ? 2 * a.hidden : a.hidden, per_tile = a.gated ? 8 : 16, ld = h_ld(a.hidden);
+    const char* w_in = static_cast<const char*>(a.w_in);
+    const size_t row_bytes = static_cast<size_t>(a.cols) * Elem<DT>::kSize;
+    const int units = it.count * row_tiles;
+    for (int unit = static_cast<int>(blockIdx.x); unit < units; unit += static_cast<int>(gridDim.x)) {
+        const int item = unit / row_tiles, tile = unit % row_tiles, n = it.slots[item], first = it.first[item];
+        const int r0 = tile * per_tile + g, r1 = a.gated ? a.hidden + r0 : r0 + 8;
+        const bool there0 = r0 < a.hidden, there1 = a.gated ? there0 : r1 < a.hidden;
+        const char* w0 = w_in + (static_cast<size_t>(it.expert[item]) * rows + (there0 ? r0 : 0)) * row_bytes;
+        const char* w1 = w_in + (static_cast<size_t>(it.expert[item]) * rows + (there1 ? r1 : 0)) * row_bytes;
+        const char* x[N8];
+#pragma unroll
+        for (int j = 0; j < N8; ++j) {
+            const int s = 8 * j + g < n ? it.sorted[first + 8 * j + g] / a.topk : 0;
+            x[j] = static_cast<const char*>(a.x) + static_cast<size_t>(s) * a.ldx * Elem<DT>::kSize;
+        }
+        float acc[N8][4] = {};
+        constexpr int U = N8 == 4 ? 1 : 2;                           // steps whose loads are on their way together
+        for (int k0 = warp * step; k0 < a.cols; k0 += U * kInWarps * step) {
+            uint4 p[2 * U], q[2 * U], v[2 * U][N8];
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u) {
+                const int k = k0 + (u >> 1) * kInWarps * step + (u & 1) * 4 * ve + c * ve;
+                p[u] = piece<DT, kVec, true>(w0, k, a.cols, there0);
+                q[u] = piece<DT, kVec, true>(w1, k, a.cols, there1);
+#pragma unroll
+                for (int j = 0; j < N8; ++j) v[u][j] = piece<DT, kVec, false>(x[j], k, a.cols, 8 * j + g < n);
+            }
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u) {
+                Left<DT, false> w;
+                w.set(p[u], q[u]);
+#pragma unroll
+                for (int j = 0; j < N8; ++j)
+                    if (j == 0 || 8 * j < n) w.multiply(acc[j], v[u][j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N8; ++j)
+            *reinterpret_cast<float4*>(parts[warp][j][lane]) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        __syncthreads();
+        for (int j = warp; j < N8 && 8 * j < n; j += kInWarps) {
+            float z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                z[i] = parts[0][j][lane][i];
+#pragma unroll
+                for (int w = 1; w < kInWarps; ++w) z[i] = __fadd_rn(z[i], parts[w][j][lane][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {                            // slots 2 c and 2 c + 1 of the eight
+                const int at = 8 * j + 2 * c + i;
+                if (at >= n) continue;
+                float* h = static_cast<float*>(a.workspace) + static_cast<size_t>(it.sorted[first + at]) * ld;
+                const float h0 = activate(z[i], a.activation);
+                if (a.gated) {
+                    if (r0 < ld) h[r0] = there0 ? __fmul_rn(h0, z[2 + i]) : 0.0f;
+                } else {
+                    if (r0 < ld) h[r0] = there0 ? h0 : 0.0f;
+                    if (r1 < ld) h[r1] = there1 ? activate(z[2 + i], a.activation) : 0.0f;
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// out = sum of weight * (w_out . h).  A block takes 16 columns of the output for
+// all items; a warp an item's share of k at a time, whose sums are kept for
+// every slot until all are there and then added in the order of the choices.
+// ---------------------------------------------------------------------------
+constexpr int kOutWarps = 16;
+constexpr int kMostParts = 8;
+
+// Shares of k for an item: enough of them to give every warp two, as far as the
+// sums of all slots fit.
+__device__ __forceinline__ int k_parts(int items, int slots, int steps) {
+    const int want = (2 * kOutWarps + items - 1) / max(1, items);
+    return max(1, min(min(want, min(kMostParts, steps)), kMaxSlots / slots));
+}
+
+template <int DT, int WDT, bool kVec, int N8>
+__global__ void __launch_bounds__(kOutWarps * 32) out_kernel(LayerArgs a, int id_bytes) {
+    constexpr int ve = Elem<DT>::kVE, step = 8 * ve;
+    extern __shared__ float sums[];                                  // parts x slots x 16
+    __shared__ Items it;
+    if (a.hidden == 0) pdl_wait();                                   // no in_kernel, which would have waited for the ids
+    sort_slots(it, a, id_bytes, 8 * N8);
+    pdl_wait();
+    const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
+    const int slots = a.tokens * a.topk, steps = (a.hidden + step - 1) / step, ld = h_ld(a.hidden);
+    const int parts = k_parts(it.count, slots, steps), units = it.count * parts;
+    const int c0 = static_cast<int>(blockIdx.x) * 16, r0 = c0 + g, r1 = r0 + 8;
+    const bool there0 = r0 < a.cols, there1 = r1 < a.cols;
+    const size_t row_bytes = static_cast<size_t>(a.hidden) * Elem<DT>::kSize;
+    for (int unit = warp; unit < units; unit += kOutWarps) {
+        const int item = unit / parts, part = unit % parts, n = it.slots[item], first = it.first[item];
+        const char* w = static_cast<const char*>(a.w_out) + static_cast<size_t>(it.expert[item]) * a.cols * row_bytes;
+        const char *w0 = w + (there0 ? r0 : 0) * row_bytes, *w1 = w + (there1 ? r1 : 0) * row_bytes;
+        const float* h[N8];
+#pragma unroll
+        for (int j = 0; j < N8; ++j)
+            h[j] = static_cast<const float*>(a.workspace) +
+                   static_cast<size_t>(8 * j + g < n ? it.sorted[first + 8 * j + g] : 0) * ld;
+        float acc[N8][4] = {};
+        constexpr int U = N8 == 4 ? 1 : 2;
+        for (int s0 = part; s0 < steps; s0 += U * parts) {
+            uint4 p[2 * U], q[2 * U];
+            typename FromH<DT>::Type v[2 * U][N8];
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u) {
+                const int k = (s0 + (u >> 1) * parts) * step + (u & 1) * 4 * ve + c * ve;
+                p[u] = piece<DT, kVec, true>(w0, k, a.hidden, there0);
+                q[u] = piece<DT, kVec, true>(w1, k, a.hidden, there1);
+#pragma unroll
+                for (int j = 0; j < N8; ++j) load_h<DT>(v[u][j], h[j], k, a.hidden, 8 * j + g < n);
+            }
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u) {
+                Left<DT, true> l;
+                l.set(p[u], q[u]);
+#pragma unroll
+                for (int j = 0; j < N8; ++j)
+                    if (j == 0 || 8 * j < n) l.multiply(acc[j], v[u][j].v);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N8; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (8 * j + 2 * c + i < n) {
+                    float* s = sums + (static_cast<size_t>(part) * slots + it.sorted[first + 8 * j + 2 * c + i]) * 16;
+                    s[g] = acc[j][i], s[g + 8] = acc[j][2 + i];
+                }
+    }
+    __syncthreads();
+    for (int i = static_cast<int>(threadIdx.x); i < a.tokens * 16; i += kOutWarps * 32) {
+        const int t = i >> 4, col = i & 15;
+        if (c0 + col >= a.cols) continue;
+        float total = 0.0f;
+        for (int j = 0; j < a.topk; ++j) {
+            const int slot = t * a.topk + j;
+            if (expert_of(a, id_bytes, slot) < 0) continue;
+            float s = 0.0f;
+            for (int q = 0; q < parts; ++q) s = __fadd_rn(s, sums[(static_cast<size_t>(q) * slots + slot) * 16 + col]);
+            total = __fmaf_rn(a.weights != nullptr ? load_elem<WDT>(a.weights, static_cast<size_t>(slot)) : 1.0f, s, total);
+        }
+        store_elem<DT>(a.out, static_cast<size_t>(t) * a.ldo + static_cast<size_t>(c0 + col), total);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+// ---------------------------------------------------------------------------
+template <int DT, int WDT, bool kVec, int N8> cudaError_t launch_kernels(int id_bytes, const LayerArgs& a, cudaStream_t s) {
+    static std::atomic<bool> allowed[kDevices];
+    const int slots = a.tokens * a.topk;
+    cudaError_t e = allow_smem(out_kernel<DT, WDT, kVec, N8>, static_cast<size_t>(kMaxSlots) * 64, allowed);
+    if (e != cudaSuccess) return e;
+    if (a.hidden > 0) {
+        const int row_tiles = a.gated ? (a.hidden + 7) / 8 : (a.hidden + 15) / 16;
+        const size_t most = static_cast<size_t>(slots) * static_cast<size_t>(row_tiles);
+        const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * 5));
+        e = launch_kernel(in_kernel<DT, kVec, N8>, dim3(grid), dim3(kInWarps * 32), s, a, id_bytes, row_tiles);
+        if (e != cudaSuccess) return e;
+    }
+    // as k_parts with the fewest items that there can be
+    const size_t smem = static_cast<size_t>(std::max(1, std::min(kMostParts, kMaxSlots / slots))) * slots * 64;
+    return launch_kernel_smem(out_kernel<DT, WDT, kVec, N8>, dim3(static_cast<unsigned>((a.cols + 15) / 16)), dim3(kOutWarps * 32),
+                              smem, s, a, id_bytes);
 }
 
 template <int DT, int WDT> cudaError_t launch(int id_bytes, const LayerArgs& a, cudaStream_t s) {
-    const dim3 block(kWarps * 32);
-    if (a.hidden > 0) {
-        const cudaError_t e = launch_kernel(in_kernel<DT>, dim3((a.hidden + kWarps - 1) / kWarps, a.tokens * a.topk), block, s,
-                                            a, id_bytes);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_kernel(out_kernel<DT, WDT>, dim3((a.cols + kWarps - 1) / kWarps, a.tokens), block, s, a, id_bytes);
+    const auto whole = [](const void* p, size_t elements) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && elements * Elem<DT>::kSize % 16 == 0;
+    };
+    const bool vec = whole(a.x, a.ldx) && whole(a.w_in, static_cast<size_t>(a.cols)) && whole(a.w_out, static_cast<size_t>(a.hidden));
+    const int mean = a.tokens * a.topk / a.experts;                  // slots of an expert
+    const auto run = [&](auto n8) {
+        constexpr int N8 = decltype(n8)::value;
+        return vec ? launch_kernels<DT, WDT, true, N8>(id_bytes, a, s) : launch_kernels<DT, WDT, false, N8>(id_bytes, a, s);
+    };
+    if (mean <= 4) return run(std::integral_constant<int, 1>());
+    if (mean <= 10) return run(std::integral_constant<int, 2>());
+    return run(std::integral_constant<int, 4>());
 }
 
 }  // namespace
 
-size_t expert_layer_workspace_bytes(size_t slots, size_t, size_t hidden) { return 16 + slots * hidden * 4; }
+size_t expert_layer_workspace_bytes(size_t slots, size_t, size_t hidden) {
+    return 16 + slots * static_cast<size_t>(h_ld(static_cast<int>(hidden))) * sizeof(float);
+}
 
 cudaError_t launch_expert_layer(sar_dtype dt, sar_dtype wdt, int id_bytes, const LayerArgs& a, cudaStream_t s) {
     switch (dt) {

@@ -27,6 +27,7 @@
 
 #include "sar_device.cuh"
 #include "sar_internal.h"
+#include "tensor_core.cuh"
 
 namespace sar {
 namespace {
@@ -46,11 +47,23 @@ __device__ __forceinline__ float activate(float z, sar_activation act) {
 // ---------------------------------------------------------------------------
 struct Items {
     int count;
-    int16_t expert[kMaxSlots], first[kMaxSlots], slots[kMaxSlots];   // of an item: its slots are sorted[first ..]
-    int16_t sorted[kMaxSlots];
-    int16_t of[kMaxSlots], rank[kMaxSlots];                          // a slot's expert, and its place among that one's
-    int tally[SAR_MAX_EXPERTS];                                      // an expert's slots, then where they start
+    int16_t *expert, *first, *slots;     // of an item: its slots are sorted[first .. first + slots - 1]
+    int16_t* sorted;
+    int16_t *of, *item;                  // a slot's expert (-1: dropped); a kept slot's item
+    int16_t* rank;                       // scratch: a slot's place among its expert's
+    int* tally;                          // scratch: an expert's slots, then first item << 16 | first place
 };
+constexpr size_t kItemArrays = 6;
+__host__ __device__ __forceinline__ size_t items_bytes(int slots) { return (kItemArrays * 2 * static_cast<size_t>(slots) + 15) / 16 * 16; }
+__host__ __device__ __forceinline__ size_t scratch_bytes(int slots, int experts) { return 4 * static_cast<size_t>(experts) + 2 * static_cast<size_t>(slots); }
+
+// items_bytes(slots) at `at`, scratch_bytes at `scratch` until sort_slots has returned.
+__device__ __forceinline__ void place_items(Items& it, unsigned char* at, unsigned char* scratch, int slots, int experts) {
+    int16_t* p = reinterpret_cast<int16_t*>(at);
+    it.expert = p, it.first = p + slots, it.slots = p + 2 * slots, it.sorted = p + 3 * slots, it.of = p + 4 * slots, it.item = p + 5 * slots;
+    it.tally = reinterpret_cast<int*>(scratch);
+    it.rank = reinterpret_cast<int16_t*>(it.tally + experts);
+}
 
 __device__ __forceinline__ int expert_of(const LayerArgs& a, int id_bytes, int slot) {
     const int64_t e = id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[slot] : static_cast<const int32_t*>(a.ids)[slot];
@@ -76,8 +89,8 @@ __device__ __forceinline__ int scan_before(int v, int lane) {        // sum over
     return s - v;
 }
 
-// All threads of the block.
-__device__ void sort_slots(Items& it, const LayerArgs& a, int id_bytes, int per) {
+// All threads of the block; it.count is the same for all of them afterwards.
+__device__ void sort_slots(Items& it, int* count, const LayerArgs& a, int id_bytes, int per) {
     const int slots = a.tokens * a.topk, t = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x), lane = t & 31;
     if (slots <= 32) {                                               // one warp, without a count for each expert
         if (t < 32) {
@@ -86,12 +99,17 @@ __device__ void sort_slots(Items& it, const LayerArgs& a, int id_bytes, int per)
             const bool leads = e >= 0 && (same & below) == 0u;
             const int have = leads ? __popc(same) : 0, items = (have + per - 1) / per;
             const int before = scan_before(items << 16 | have, lane);
-            const int start = __shfl_sync(0xFFFFFFFFu, before & 0xFFFF, __ffs(same) - 1);
-            if (e >= 0) it.sorted[start + __popc(same & below)] = static_cast<int16_t>(lane);
+            const int of = __shfl_sync(0xFFFFFFFFu, before, __ffs(same) - 1), rank = __popc(same & below);
+            it.of[lane] = static_cast<int16_t>(e);
+            if (e >= 0) {
+                it.sorted[(of & 0xFFFF) + rank] = static_cast<int16_t>(lane);
+                it.item[lane] = static_cast<int16_t>((of >> 16) + rank / per);
+            }
             write_items(it, e, before & 0xFFFF, have, before >> 16, per);
-            if (lane == 31) it.count = (before >> 16) + items;
+            if (lane == 31) *count = (before >> 16) + items;
         }
         __syncthreads();
+        it.count = *count;
         return;
     }
     for (int e = t; e < a.experts; e += threads) it.tally[e] = 0;
@@ -114,38 +132,46 @@ __device__ void sort_slots(Items& it, const LayerArgs& a, int id_bytes, int per)
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
             const int e = e0 + lane, have = e < a.experts ? it.tally[e] : 0, v = ((have + per - 1) / per) << 16 | have;
             const int before = done + scan_before(v, lane);
-            if (e < a.experts) it.tally[e] = before & 0xFFFF;
+            if (e < a.experts) it.tally[e] = before;
             write_items(it, e, before & 0xFFFF, have, before >> 16, per);
             done = __shfl_sync(0xFFFFFFFFu, before + v, 31);
         }
-        if (lane == 0) it.count = done >> 16;
+        if (lane == 0) *count = done >> 16;
     }
     __syncthreads();
     for (int s = t; s < slots; s += threads) {
         const int e = it.of[s];
-        if (e >= 0) it.sorted[it.tally[e] + it.rank[s]] = static_cast<int16_t>(s);
+        if (e < 0) continue;
+        it.sorted[(it.tally[e] & 0xFFFF) + it.rank[s]] = static_cast<int16_t>(s);
+        it.item[s] = static_cast<int16_t>((it.tally[e] >> 16) + it.rank[s] / per);
     }
     __syncthreads();
+    it.count = *count;
 }
 
 // ---------------------------------------------------------------------------
 // Operands.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint4 load_weights(const uint4* p) {      // read once: not kept in L1
+#ifndef LAYER_HINT
+#define LAYER_HINT ".L2::256B"
+#endif
+__device__ __forceinline__ uint4 load_weights(const void* p) {       // read once: not kept in L1
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate" LAYER_HINT ".v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
     return v;
 }
 
 // 16 bytes of a row of n elements, from element k on; zeros past its end.  kVec:
 // rows are whole pieces on 16-byte boundaries.
-template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 piece(const void* row, int k, int n, bool there) {
+template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 piece(const char* row, int k, int n, bool there) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     constexpr int ve = Elem<DT>::kVE;
     if (kVec) {
         if (there && k < n) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<size_t>(k) * Elem<DT>::kSize);
-            v = kWeights ? load_weights(p) : *p;
+            const char* p = row + static_cast<size_t>(k) * Elem<DT>::kSize;
+            v = kWeights ? load_weights(p) : *reinterpret_cast<const uint4*>(p);
         }
     } else {
         uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -153,9 +179,9 @@ template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 pie
         for (int i = 0; i < ve; ++i)
             if (there && k + i < n) {
                 if (Elem<DT>::kSize == 4)
-                    w[i & 3] = static_cast<const uint32_t*>(row)[k + i];
+                    w[i & 3] = reinterpret_cast<const uint32_t*>(row)[k + i];
                 else
-                    w[i >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(row)[k + i]) << (16 * (i & 1));
+                    w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[k + i]) << (16 * (i & 1));
             }
         v = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -214,19 +240,35 @@ template <int DT> struct Left<DT, false> {      // 16-bit weights against x
         mma_16<DT>(d, a[2], b[2], a[3], b[3], x.z, x.w);
     }
 };
+// The slots' h in two numbers, split once for all rows.
+template <int DT> struct Right;
+template <> struct Right<SAR_BF16> {
+    uint32_t hi[4], lo[4];
+    __device__ __forceinline__ explicit Right(const float (&h)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_bf16(h[2 * i], h[2 * i + 1], hi[i], lo[i]);
+    }
+};
+template <int N> struct RightTf32 {
+    uint32_t hi[N], lo[N];
+    __device__ __forceinline__ explicit RightTf32(const float (&h)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) split_tf32(h[i], hi[i], lo[i]);
+    }
+};
+template <> struct Right<SAR_FP16> : RightTf32<8> { using RightTf32<8>::RightTf32; };
+template <> struct Right<SAR_FP32> : RightTf32<4> { using RightTf32<4>::RightTf32; };
+
 template <> struct Left<SAR_BF16, true> {
     uint32_t a[4], b[4];
     __device__ __forceinline__ void set(const uint4& p, const uint4& q) {
         a[0] = p.x, a[1] = p.y, a[2] = p.z, a[3] = p.w, b[0] = q.x, b[1] = q.y, b[2] = q.z, b[3] = q.w;
     }
-    __device__ __forceinline__ void multiply(float (&d)[4], const float (&h)[8]) const {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split_bf16(h[2 * i], h[2 * i + 1], hi[i], lo[i]);
+    __device__ __forceinline__ void multiply(float (&d)[4], const Right<SAR_BF16>& h) const {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-            mma_16<SAR_BF16>(d, a[i], b[i], a[i + 1], b[i + 1], lo[i], lo[i + 1]);
-            mma_16<SAR_BF16>(d, a[i], b[i], a[i + 1], b[i + 1], hi[i], hi[i + 1]);
+            mma_16<SAR_BF16>(d, a[i], b[i], a[i + 1], b[i + 1], h.lo[i], h.lo[i + 1]);
+            mma_16<SAR_BF16>(d, a[i], b[i], a[i + 1], b[i + 1], h.hi[i], h.hi[i + 1]);
         }
     }
 };
@@ -236,14 +278,12 @@ template <> struct Left<SAR_FP16, true> {
         widen_word<SAR_FP16>(p.x, a), widen_word<SAR_FP16>(p.y, a + 2), widen_word<SAR_FP16>(p.z, a + 4), widen_word<SAR_FP16>(p.w, a + 6);
         widen_word<SAR_FP16>(q.x, b), widen_word<SAR_FP16>(q.y, b + 2), widen_word<SAR_FP16>(q.z, b + 4), widen_word<SAR_FP16>(q.w, b + 6);
     }
-    __device__ __forceinline__ void multiply(float (&d)[4], const float (&h)[8]) const {
+    __device__ __forceinline__ void multiply(float (&d)[4], const Right<SAR_FP16>& h) const {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(h[i], h0, l0), split_tf32(h[i + 1], h1, l1);
             const uint32_t a0 = __float_as_uint(a[i]), a1 = __float_as_uint(b[i]), a2 = __float_as_uint(a[i + 1]), a3 = __float_as_uint(b[i + 1]);
-            mma_tf32(d, a0, a1, a2, a3, l0, l1);
-            mma_tf32(d, a0, a1, a2, a3, h0, h1);
+            mma_tf32(d, a0, a1, a2, a3, h.lo[i], h.lo[i + 1]);
+            mma_tf32(d, a0, a1, a2, a3, h.hi[i], h.hi[i + 1]);
         }
     }
 };
@@ -255,116 +295,136 @@ struct LeftFp32 {
         split_tf32(__uint_as_float(q.x), bh[0], bl[0]), split_tf32(__uint_as_float(q.y), bh[1], bl[1]);
         split_tf32(__uint_as_float(q.z), bh[2], bl[2]), split_tf32(__uint_as_float(q.w), bh[3], bl[3]);
     }
-    __device__ __forceinline__ void multiply(float (&d)[4], const float (&x)[4]) const {
+    __device__ __forceinline__ void multiply(float (&d)[4], const RightTf32<4>& x) const {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(x[i], h0, l0), split_tf32(x[i + 1], h1, l1);
-            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], l0, l1);
-            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], h0, h1);
-            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], l0, l1);
-            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], h0, h1);
+            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], x.lo[i], x.lo[i + 1]);
+            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], x.hi[i], x.hi[i + 1]);
+            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], x.lo[i], x.lo[i + 1]);
+            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], x.hi[i], x.hi[i + 1]);
         }
     }
     __device__ __forceinline__ void multiply(float (&d)[4], const uint4& x) const {
         const float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
-        multiply(d, v);
+        multiply(d, RightTf32<4>(v));
     }
 };
 template <> struct Left<SAR_FP32, false> : LeftFp32 {};
 template <> struct Left<SAR_FP32, true> : LeftFp32 {};
 
-// What a slot brings: a piece of x, or of h (kVE binary32 values).
-template <int DT> struct FromX { using Type = uint4; };
-template <int DT> struct FromH { struct Type { float v[Elem<DT>::kVE]; }; };
-
 __host__ __device__ __forceinline__ int h_ld(int hidden) { return (hidden + 7) / 8 * 8; }
 
-template <int DT> __device__ __forceinline__ void load_h(typename FromH<DT>::Type& to, const float* h, int k, int n, bool there) {
-#pragma unroll
-    for (int i = 0; i < Elem<DT>::kVE; i += 4) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (there && k + i < n) v = *reinterpret_cast<const float4*>(h + k + i);      // rows of h end in zeros
-        to.v[i] = v.x, to.v[i + 1] = v.y, to.v[i + 2] = v.z, to.v[i + 3] = v.w;
-    }
-}
-
 // ---------------------------------------------------------------------------
-// h = act(w_in . x).  A block takes 16 rows of an item's expert (gated: 8 rows
-// and the 8 that belong to them, which meet in one lane's sums), its warps a
-// share of k each.
+// h = act(w_in . x).  A block takes MT times 16 rows of an item's expert (gated:
+// 8 rows and the 8 that belong to them, which meet in one lane's sums), its warps
+// a share of k each.  Copies run ahead of the products, from one unit of rows
+// into the next.
 // ---------------------------------------------------------------------------
 constexpr int kInWarps = 4;
+#ifndef IN_CTAS
+#define IN_CTAS 8
+#endif
+#ifndef IN_U
+#define IN_U 2
+#endif
+#ifndef OUT_WARPS
+#define OUT_WARPS 16
+#endif
+#ifndef OUT_CTAS
+#define OUT_CTAS 1
+#endif
 
-template <int DT, bool kVec, int N8>
+template <int DT, bool kVec, int N8, int MT>
 __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_bytes, int row_tiles) {
-    constexpr int ve = Elem<DT>::kVE, step = 8 * ve;                 // 128 bytes of a row
-    __shared__ Items it;
-    __shared__ __align__(16) float parts[kInWarps][N8][32][4];
+    constexpr int ve = Elem<DT>::kVE, es = Elem<DT>::kSize, step = 8 * ve;      // 128 bytes of a row
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    __shared__ __align__(16) float parts[kInWarps][MT * N8][32][4];
+    __shared__ int item_count;
+    const int slots = a.tokens * a.topk;
+    Items it;
+    place_items(it, dynamic, dynamic + items_bytes(slots), slots, a.experts);
     pdl_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // out_kernel may sort its slots meanwhile
-    sort_slots(it, a, id_bytes, 8 * N8);
+    sort_slots(it, &item_count, a, id_bytes, 8 * N8);
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
     const int rows = a.gated ? 2 * a.hidden : a.hidden, per_tile = a.gated ? 8 : 16, ld = h_ld(a.hidden);
-    const char* w_in = static_cast<const char*>(a.w_in);
-    const size_t row_bytes = static_cast<size_t>(a.cols) * Elem<DT>::kSize;
+    const size_t row_bytes = static_cast<size_t>(a.cols) * es;
     const int units = it.count * row_tiles;
     for (int unit = static_cast<int>(blockIdx.x); unit < units; unit += static_cast<int>(gridDim.x)) {
         const int item = unit / row_tiles, tile = unit % row_tiles, n = it.slots[item], first = it.first[item];
-        const int r0 = tile * per_tile + g, r1 = a.gated ? a.hidden + r0 : r0 + 8;
-        const bool there0 = r0 < a.hidden, there1 = a.gated ? there0 : r1 < a.hidden;
-        const char* w0 = w_in + (static_cast<size_t>(it.expert[item]) * rows + (there0 ? r0 : 0)) * row_bytes;
-        const char* w1 = w_in + (static_cast<size_t>(it.expert[item]) * rows + (there1 ? r1 : 0)) * row_bytes;
+        const char* base = static_cast<const char*>(a.w_in) + static_cast<size_t>(it.expert[item]) * rows * row_bytes;
+        const char* w[MT][2];
+        bool there[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int top = (tile * MT + m) * per_tile + g, bottom = a.gated ? a.hidden + top : top + 8;
+            there[m][0] = top < a.hidden;
+            there[m][1] = a.gated ? there[m][0] : bottom < a.hidden;
+            w[m][0] = base + (there[m][0] ? top : 0) * row_bytes;
+            w[m][1] = base + (there[m][1] ? bottom : 0) * row_bytes;
+        }
         const char* x[N8];
 #pragma unroll
         for (int j = 0; j < N8; ++j) {
-            const int s = 8 * j + g < n ? it.sorted[first + 8 * j + g] / a.topk : 0;
-            x[j] = static_cast<const char*>(a.x) + static_cast<size_t>(s) * a.ldx * Elem<DT>::kSize;
+            const int t = 8 * j + g < n ? it.sorted[first + 8 * j + g] / a.topk : 0;
+            x[j] = static_cast<const char*>(a.x) + static_cast<size_t>(t) * a.ldx * es;
         }
-        float acc[N8][4] = {};
-        constexpr int U = N8 == 4 ? 1 : 2;                           // steps whose loads are on their way together
+        float acc[MT][N8][4] = {};
+        constexpr int U = MT == 1 && N8 < 4 && kVec ? IN_U : 1;      // steps whose loads are on their way together
         for (int k0 = warp * step; k0 < a.cols; k0 += U * kInWarps * step) {
-            uint4 p[2 * U], q[2 * U], v[2 * U][N8];
+            uint4 p[2 * U][MT][2], v[2 * U][N8];
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
                 const int k = k0 + (u >> 1) * kInWarps * step + (u & 1) * 4 * ve + c * ve;
-                p[u] = piece<DT, kVec, true>(w0, k, a.cols, there0);
-                q[u] = piece<DT, kVec, true>(w1, k, a.cols, there1);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    p[u][m][0] = piece<DT, kVec, true>(w[m][0], k, a.cols, there[m][0]);
+                    p[u][m][1] = piece<DT, kVec, true>(w[m][1], k, a.cols, there[m][1]);
+                }
 #pragma unroll
                 for (int j = 0; j < N8; ++j) v[u][j] = piece<DT, kVec, false>(x[j], k, a.cols, 8 * j + g < n);
             }
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
-                Left<DT, false> w;
-                w.set(p[u], q[u]);
+                Left<DT, false> l[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) l[m].set(p[u][m][0], p[u][m][1]);
 #pragma unroll
                 for (int j = 0; j < N8; ++j)
-                    if (j == 0 || 8 * j < n) w.multiply(acc[j], v[u][j]);
+                    if (j == 0 || 8 * j < n) {
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], v[u][j]);
+                    }
             }
         }
 #pragma unroll
-        for (int j = 0; j < N8; ++j)
-            *reinterpret_cast<float4*>(parts[warp][j][lane]) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < N8; ++j)
+                *reinterpret_cast<float4*>(parts[warp][m * N8 + j][lane]) =
+                    make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
         __syncthreads();
-        for (int j = warp; j < N8 && 8 * j < n; j += kInWarps) {
+        for (int i = warp; i < MT * N8; i += kInWarps) {
+            const int j = i % N8, top = (tile * MT + i / N8) * per_tile + g, bottom = top + 8;
+            if (8 * j >= n) continue;
             float z[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                z[i] = parts[0][j][lane][i];
+            for (int q = 0; q < 4; ++q) {
+                z[q] = parts[0][i][lane][q];
 #pragma unroll
-                for (int w = 1; w < kInWarps; ++w) z[i] = __fadd_rn(z[i], parts[w][j][lane][i]);
+                for (int v = 1; v < kInWarps; ++v) z[q] = __fadd_rn(z[q], parts[v][i][lane][q]);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {                            // slots 2 c and 2 c + 1 of the eight
-                const int at = 8 * j + 2 * c + i;
+            for (int q = 0; q < 2; ++q) {                            // slots 2 c and 2 c + 1 of the eight
+                const int at = 8 * j + 2 * c + q;
                 if (at >= n) continue;
                 float* h = static_cast<float*>(a.workspace) + static_cast<size_t>(it.sorted[first + at]) * ld;
-                const float h0 = activate(z[i], a.activation);
+                const float h0 = activate(z[q], a.activation);
                 if (a.gated) {
-                    if (r0 < ld) h[r0] = there0 ? __fmul_rn(h0, z[2 + i]) : 0.0f;
+                    if (top < ld) h[top] = top < a.hidden ? __fmul_rn(h0, z[2 + q]) : 0.0f;
                 } else {
-                    if (r0 < ld) h[r0] = there0 ? h0 : 0.0f;
-                    if (r1 < ld) h[r1] = there1 ? activate(z[2 + i], a.activation) : 0.0f;
+                    if (top < ld) h[top] = top < a.hidden ? h0 : 0.0f;
+                    if (bottom < ld) h[bottom] = bottom < a.hidden ? activate(z[2 + q], a.activation) : 0.0f;
                 }
             }
         }
@@ -373,63 +433,105 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
 }
 
 // ---------------------------------------------------------------------------
-// out = sum of weight * (w_out . h).  A block takes 16 columns of the output for
-// all items; a warp an item's share of k at a time, whose sums are kept for
-// every slot until all are there and then added in the order of the choices.
+// out = sum of weight * (w_out . h).  A cluster of blocks takes MT times 16
+// columns of the output for all items.  Its warps take an item's share of k at a
+// time, whose sums stay in their block's shared memory until all are there; then
+// they are added in the order of the choices.
 // ---------------------------------------------------------------------------
-constexpr int kOutWarps = 16;
-constexpr int kMostParts = 8;
+constexpr int kOutWarps = OUT_WARPS;
+constexpr int kMostParts = 16;
+constexpr int kMostCluster = 8;
 
-// Shares of k for an item: enough of them to give every warp two, as far as the
-// sums of all slots fit.
-__device__ __forceinline__ int k_parts(int items, int slots, int steps) {
-    const int want = (2 * kOutWarps + items - 1) / max(1, items);
-    return max(1, min(min(want, min(kMostParts, steps)), kMaxSlots / slots));
+// Shares of k for an item: enough of them to give every warp of the cluster two,
+// as far as the sums of all slots fit.
+__host__ __device__ __forceinline__ int parts_that_fit(int slots, int mt) {
+    const int fit = kMaxSlots / (slots * mt);
+    return fit < 1 ? 1 : (fit > kMostParts ? kMostParts : fit);
+}
+__device__ __forceinline__ int k_parts(int items, int slots, int steps, int warps, int mt) {
+    const int want = (2 * warps + items - 1) / max(1, items);
+    return max(1, min(min(want, steps), parts_that_fit(slots, mt)));
 }
 
-template <int DT, int WDT, bool kVec, int N8>
-__global__ void __launch_bounds__(kOutWarps * 32) out_kernel(LayerArgs a, int id_bytes) {
-    constexpr int ve = Elem<DT>::kVE, step = 8 * ve;
-    extern __shared__ float sums[];                                  // parts x slots x 16
-    __shared__ Items it;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float load_of_block(const float* p, int rank) {      // the same place in a block of the cluster
+    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+
+template <int DT, int WDT, bool kVec, int N8, int MT>
+__global__ void __launch_bounds__(kOutWarps * 32, OUT_CTAS) out_kernel(LayerArgs a, int id_bytes) {
+    constexpr int ve = Elem<DT>::kVE, es = Elem<DT>::kSize, step = 8 * ve, width = 16 * MT;
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    __shared__ int item_count;
+    const int slots = a.tokens * a.topk;
+    float* sums = reinterpret_cast<float*>(dynamic + items_bytes(slots));       // parts x slots x width; the sort's scratch before
+    Items it;
+    place_items(it, dynamic, dynamic + items_bytes(slots), slots, a.experts);
     if (a.hidden == 0) pdl_wait();                                   // no in_kernel, which would have waited for the ids
-    sort_slots(it, a, id_bytes, 8 * N8);
+    sort_slots(it, &item_count, a, id_bytes, 8 * N8);
     pdl_wait();
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
-    const int slots = a.tokens * a.topk, steps = (a.hidden + step - 1) / step, ld = h_ld(a.hidden);
-    const int parts = k_parts(it.count, slots, steps), units = it.count * parts;
-    const int c0 = static_cast<int>(blockIdx.x) * 16, r0 = c0 + g, r1 = r0 + 8;
-    const bool there0 = r0 < a.cols, there1 = r1 < a.cols;
-    const size_t row_bytes = static_cast<size_t>(a.hidden) * Elem<DT>::kSize;
-    for (int unit = warp; unit < units; unit += kOutWarps) {
+    const int blocks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
+    const int steps = (a.hidden + step - 1) / step, ld = h_ld(a.hidden);
+    const int parts = k_parts(it.count, slots, steps, kOutWarps * blocks, MT), units = it.count * parts;
+    const int c0 = static_cast<int>(blockIdx.x) * width;
+    const size_t row_bytes = static_cast<size_t>(a.hidden) * es;
+    for (int unit = rank + blocks * warp; unit < units; unit += blocks * kOutWarps) {
         const int item = unit / parts, part = unit % parts, n = it.slots[item], first = it.first[item];
-        const char* w = static_cast<const char*>(a.w_out) + static_cast<size_t>(it.expert[item]) * a.cols * row_bytes;
-        const char *w0 = w + (there0 ? r0 : 0) * row_bytes, *w1 = w + (there1 ? r1 : 0) * row_bytes;
+        const char* base = static_cast<const char*>(a.w_out) + static_cast<size_t>(it.expert[item]) * a.cols * row_bytes;
+        const char* w[MT][2];
+        bool there[MT][2];
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) {
+            const int r = c0 + 8 * m + g;
+            there[m >> 1][m & 1] = r < a.cols;
+            w[m >> 1][m & 1] = base + (r < a.cols ? r : 0) * row_bytes;
+        }
         const float* h[N8];
 #pragma unroll
         for (int j = 0; j < N8; ++j)
             h[j] = static_cast<const float*>(a.workspace) +
                    static_cast<size_t>(8 * j + g < n ? it.sorted[first + 8 * j + g] : 0) * ld;
-        float acc[N8][4] = {};
-        constexpr int U = N8 == 4 ? 1 : 2;
+        float acc[MT][N8][4] = {};
+        constexpr int U = MT == 1 && N8 == 1 && kVec ? 2 : 1;
         for (int s0 = part; s0 < steps; s0 += U * parts) {
-            uint4 p[2 * U], q[2 * U];
-            typename FromH<DT>::Type v[2 * U][N8];
+            uint4 p[2 * U][MT][2];
+            float v[2 * U][N8][ve];
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
                 const int k = (s0 + (u >> 1) * parts) * step + (u & 1) * 4 * ve + c * ve;
-                p[u] = piece<DT, kVec, true>(w0, k, a.hidden, there0);
-                q[u] = piece<DT, kVec, true>(w1, k, a.hidden, there1);
 #pragma unroll
-                for (int j = 0; j < N8; ++j) load_h<DT>(v[u][j], h[j], k, a.hidden, 8 * j + g < n);
+                for (int m = 0; m < MT; ++m) {
+                    p[u][m][0] = piece<DT, kVec, true>(w[m][0], k, a.hidden, there[m][0]);
+                    p[u][m][1] = piece<DT, kVec, true>(w[m][1], k, a.hidden, there[m][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < N8; ++j)
+#pragma unroll
+                    for (int i = 0; i < ve; i += 4) {                // rows of h end in zeros
+                        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (8 * j + g < n && k + i < a.hidden) q = *reinterpret_cast<const float4*>(h[j] + k + i);
+                        v[u][j][i] = q.x, v[u][j][i + 1] = q.y, v[u][j][i + 2] = q.z, v[u][j][i + 3] = q.w;
+                    }
             }
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
-                Left<DT, true> l;
-                l.set(p[u], q[u]);
+                Left<DT, true> l[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) l[m].set(p[u][m][0], p[u][m][1]);
 #pragma unroll
                 for (int j = 0; j < N8; ++j)
-                    if (j == 0 || 8 * j < n) l.multiply(acc[j], v[u][j].v);
+                    if (j == 0 || 8 * j < n) {
+                        const Right<DT> r(v[u][j]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], r);
+                    }
             }
         }
 #pragma unroll
@@ -437,45 +539,74 @@ __global__ void __launch_bounds__(kOutWarps * 32) out_kernel(LayerArgs a, int id
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (8 * j + 2 * c + i < n) {
-                    float* s = sums + (static_cast<size_t>(part) * slots + it.sorted[first + 8 * j + 2 * c + i]) * 16;
-                    s[g] = acc[j][i], s[g + 8] = acc[j][2 + i];
+                    float* t = sums + (static_cast<size_t>(part) * slots + it.sorted[first + 8 * j + 2 * c + i]) * width;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) t[16 * m + g] = acc[m][j][i], t[16 * m + 8 + g] = acc[m][j][2 + i];
                 }
     }
-    __syncthreads();
-    for (int i = static_cast<int>(threadIdx.x); i < a.tokens * 16; i += kOutWarps * 32) {
-        const int t = i >> 4, col = i & 15;
+    cluster_sync();
+    const int threads = blocks * kOutWarps * 32;
+    for (int i = rank * kOutWarps * 32 + static_cast<int>(threadIdx.x); i < a.tokens * width; i += threads) {
+        const int t = i / width, col = i % width;
         if (c0 + col >= a.cols) continue;
         float total = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
             const int slot = t * a.topk + j;
-            if (expert_of(a, id_bytes, slot) < 0) continue;
+            if (it.of[slot] < 0) continue;
+            const int unit = it.item[slot] * parts;
             float s = 0.0f;
-            for (int q = 0; q < parts; ++q) s = __fadd_rn(s, sums[(static_cast<size_t>(q) * slots + slot) * 16 + col]);
+            for (int q = 0; q < parts; ++q)
+                s = __fadd_rn(s, load_of_block(sums + (static_cast<size_t>(q) * slots + slot) * width + col, (unit + q) % blocks));
             total = __fmaf_rn(a.weights != nullptr ? load_elem<WDT>(a.weights, static_cast<size_t>(slot)) : 1.0f, s, total);
         }
         store_elem<DT>(a.out, static_cast<size_t>(t) * a.ldo + static_cast<size_t>(c0 + col), total);
     }
+    cluster_sync();                                                  // no block ends while another reads its sums
 }
 
 // ---------------------------------------------------------------------------
 // Host.
 // ---------------------------------------------------------------------------
-template <int DT, int WDT, bool kVec, int N8> cudaError_t launch_kernels(int id_bytes, const LayerArgs& a, cudaStream_t s) {
+template <typename... KArgs>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, KArgs... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1, attr[1].val.clusterDim.y = grid.y, attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// in: IN8 eights of slots to an item, IMT times 16 rows; out: ON8 and OMT.
+template <int DT, int WDT, bool kVec, int IN8, int IMT, int ON8, int OMT>
+cudaError_t launch_kernels(int id_bytes, const LayerArgs& a, cudaStream_t s) {
     static std::atomic<bool> allowed[kDevices];
     const int slots = a.tokens * a.topk;
-    cudaError_t e = allow_smem(out_kernel<DT, WDT, kVec, N8>, static_cast<size_t>(kMaxSlots) * 64, allowed);
+    const auto out = out_kernel<DT, WDT, kVec, ON8, OMT>;
+    const size_t scratch = scratch_bytes(slots, a.experts);
+    cudaError_t e = allow_smem(out, items_bytes(kMaxSlots) + static_cast<size_t>(kMaxSlots) * 64, allowed);
     if (e != cudaSuccess) return e;
     if (a.hidden > 0) {
-        const int row_tiles = a.gated ? (a.hidden + 7) / 8 : (a.hidden + 15) / 16;
+        const int per = (a.gated ? 8 : 16) * IMT, row_tiles = (a.hidden + per - 1) / per;
         const size_t most = static_cast<size_t>(slots) * static_cast<size_t>(row_tiles);
-        const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * 5));
-        e = launch_kernel(in_kernel<DT, kVec, N8>, dim3(grid), dim3(kInWarps * 32), s, a, id_bytes, row_tiles);
+        const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * IN_CTAS));
+        e = launch_kernel_smem(in_kernel<DT, kVec, IN8, IMT>, dim3(grid), dim3(kInWarps * 32), items_bytes(slots) + scratch, s, a,
+                               id_bytes, row_tiles);
         if (e != cudaSuccess) return e;
     }
-    // as k_parts with the fewest items that there can be
-    const size_t smem = static_cast<size_t>(std::max(1, std::min(kMostParts, kMaxSlots / slots))) * slots * 64;
-    return launch_kernel_smem(out_kernel<DT, WDT, kVec, N8>, dim3(static_cast<unsigned>((a.cols + 15) / 16)), dim3(kOutWarps * 32),
-                              smem, s, a, id_bytes);
+    const int tiles = (a.cols + 16 * OMT - 1) / (16 * OMT);
+    int blocks = 1;                                                  // as many blocks as are there at once
+    while (blocks < kMostCluster && tiles * blocks * 2 <= OUT_CTAS * kSMs) blocks *= 2;
+    const size_t sums = static_cast<size_t>(parts_that_fit(slots, OMT)) * slots * OMT * 64;
+    return launch_cluster(out, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(blocks)), kOutWarps * 32,
+                          items_bytes(slots) + std::max(scratch, sums), s, a, id_bytes);
 }
 
 template <int DT, int WDT> cudaError_t launch(int id_bytes, const LayerArgs& a, cudaStream_t s) {
@@ -484,13 +615,15 @@ template <int DT, int WDT> cudaError_t launch(int id_bytes, const LayerArgs& a, 
     };
     const bool vec = whole(a.x, a.ldx) && whole(a.w_in, static_cast<size_t>(a.cols)) && whole(a.w_out, static_cast<size_t>(a.hidden));
     const int mean = a.tokens * a.topk / a.experts;                  // slots of an expert
-    const auto run = [&](auto n8) {
-        constexpr int N8 = decltype(n8)::value;
-        return vec ? launch_kernels<DT, WDT, true, N8>(id_bytes, a, s) : launch_kernels<DT, WDT, false, N8>(id_bytes, a, s);
-    };
-    if (mean <= 4) return run(std::integral_constant<int, 1>());
-    if (mean <= 10) return run(std::integral_constant<int, 2>());
-    return run(std::integral_constant<int, 4>());
+    if (mean <= 4)
+        return vec ? launch_kernels<DT, WDT, true, 1, 1, 1, 1>(id_bytes, a, s) : launch_kernels<DT, WDT, false, 1, 1, 1, 1>(id_bytes, a, s);
+    if (mean <= 10) {
+        if (vec && a.tokens * a.topk <= kMaxSlots / 2) return launch_kernels<DT, WDT, true, 2, 2, 2, 2>(id_bytes, a, s);
+        return vec ? launch_kernels<DT, WDT, true, 2, 2, 2, 1>(id_bytes, a, s) : launch_kernels<DT, WDT, false, 2, 1, 2, 1>(id_bytes, a, s);
+    }
+    // The sums of all slots, 32 columns each, fit in a block's shared memory up to 512.
+    if (vec && a.tokens * a.topk <= kMaxSlots / 2) return launch_kernels<DT, WDT, true, 4, 2, 2, 2>(id_bytes, a, s);
+    return vec ? launch_kernels<DT, WDT, true, 4, 2, 2, 1>(id_bytes, a, s) : launch_kernels<DT, WDT, false, 4, 1, 2, 1>(id_bytes, a, s);
 }
 
 }  // namespace

@@ -27,7 +27,6 @@
 
 #include "sar_device.cuh"
 #include "sar_internal.h"
-#include "tensor_core.cuh"
 
 namespace sar {
 namespace {
@@ -152,40 +151,55 @@ __device__ void sort_slots(Items& it, int* count, const LayerArgs& a, int id_byt
 // ---------------------------------------------------------------------------
 // Operands.
 // ---------------------------------------------------------------------------
-#ifndef LAYER_HINT
-#define LAYER_HINT ".L2::256B"
-#endif
-__device__ __forceinline__ uint4 load_weights(const void* p) {       // read once: not kept in L1
+// Weights are read once: not kept in L1.  A request covers 64 bytes of a row, and
+// L2 fetches the 256 around them (32 x 8 of 128 experts: 186 -> 181 us).
+__device__ __forceinline__ uint4 load_weights(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate" LAYER_HINT ".v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
 }
 
 // 16 bytes of a row of n elements, from element k on; zeros past its end.  kVec:
-// rows are whole pieces on 16-byte boundaries.
+// rows are whole pieces on 16-byte boundaries.  Of other rows, binary32 is read
+// by elements (17 x 3 of 20 experts of 1021 / 515: 40 us, by blocks 49), 16-bit
+// types as the two 16-byte blocks that hold the piece (only blocks that hold
+// elements of the row) and put together (4 x 2 of 40 of 2001 / 2015 bf16: 76 us, by
+// elements 98).
 template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 piece(const char* row, int k, int n, bool there) {
+    constexpr int es = Elem<DT>::kSize;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    constexpr int ve = Elem<DT>::kVE;
+    const char* p = row + static_cast<size_t>(k) * es;
     if (kVec) {
-        if (there && k < n) {
-            const char* p = row + static_cast<size_t>(k) * Elem<DT>::kSize;
-            v = kWeights ? load_weights(p) : *reinterpret_cast<const uint4*>(p);
-        }
-    } else {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < ve; ++i)
-            if (there && k + i < n) {
-                if (Elem<DT>::kSize == 4)
-                    w[i & 3] = reinterpret_cast<const uint32_t*>(row)[k + i];
-                else
-                    w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[k + i]) << (16 * (i & 1));
-            }
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        if (there && k < n) v = kWeights ? load_weights(p) : *reinterpret_cast<const uint4*>(p);
+        return v;
     }
-    return v;
+    const int left = there ? n - k : 0;
+    if (es == 4) {
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(p);
+        if (left > 0) v.x = e[0];
+        if (left > 1) v.y = e[1];
+        if (left > 2) v.z = e[2];
+        if (left > 3) v.w = e[3];
+        return v;
+    }
+    uint4 next = v;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    if (left > 0) v = *reinterpret_cast<const uint4*>(p - shift);
+    if (shift > 0 && left * es > 16 - shift) next = *reinterpret_cast<const uint4*>(p - shift + 16);
+    uint32_t w[8] = {v.x, v.y, v.z, v.w, next.x, next.y, next.z, next.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t both = shift & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        const int rest = left - 2 * i;
+        w[i] = rest <= 0 ? 0u : (rest == 1 ? both & 0xFFFFu : both);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int DT> __device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -321,18 +335,10 @@ __host__ __device__ __forceinline__ int h_ld(int hidden) { return (hidden + 7) /
 // into the next.
 // ---------------------------------------------------------------------------
 constexpr int kInWarps = 4;
-#ifndef IN_CTAS
-#define IN_CTAS 8
-#endif
-#ifndef IN_U
-#define IN_U 2
-#endif
-#ifndef OUT_WARPS
-#define OUT_WARPS 16
-#endif
-#ifndef OUT_CTAS
-#define OUT_CTAS 1
-#endif
+// Blocks of a SM: as many as fit for items of eight slots (48 registers a thread),
+// twice as many as fit for the others, in turn.  32 x 8 of 128 experts with 5, 8,
+// 10, 12: 206, 186, 171, 200 us; 64 x 2 of 8 with 6, 8, 10: 434, 393, 413.
+template <int N8> constexpr int kInBlocks = N8 == 1 ? 10 : 8;
 
 template <int DT, bool kVec, int N8, int MT>
 __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_bytes, int row_tiles) {
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
             x[j] = static_cast<const char*>(a.x) + static_cast<size_t>(t) * a.ldx * es;
         }
         float acc[MT][N8][4] = {};
-        constexpr int U = MT == 1 && N8 < 4 && kVec ? IN_U : 1;      // steps whose loads are on their way together
+        constexpr int U = MT == 1 && N8 < 4 && kVec ? 2 : 1;         // steps whose loads are on their way together
         for (int k0 = warp * step; k0 < a.cols; k0 += U * kInWarps * step) {
             uint4 p[2 * U][MT][2], v[2 * U][N8];
 #pragma unroll
@@ -438,19 +444,25 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
 // time, whose sums stay in their block's shared memory until all are there; then
 // they are added in the order of the choices.
 // ---------------------------------------------------------------------------
-constexpr int kOutWarps = OUT_WARPS;
+constexpr int kOutWarps = 16;                                        // one block a SM
 constexpr int kMostParts = 16;
 constexpr int kMostCluster = 8;
 
-// Shares of k for an item: enough of them to give every warp of the cluster two,
-// as far as the sums of all slots fit.
+// Shares of k for an item: the number with the least time of a warp, which is its
+// units times their steps (and two steps' time to begin and end one), as far as
+// the sums of all slots fit.
 __host__ __device__ __forceinline__ int parts_that_fit(int slots, int mt) {
     const int fit = kMaxSlots / (slots * mt);
     return fit < 1 ? 1 : (fit > kMostParts ? kMostParts : fit);
 }
 __device__ __forceinline__ int k_parts(int items, int slots, int steps, int warps, int mt) {
-    const int want = (2 * warps + items - 1) / max(1, items);
-    return max(1, min(min(want, steps), parts_that_fit(slots, mt)));
+    const int most = max(1, min(steps / 2, parts_that_fit(slots, mt)));
+    int best = 1, least = 0x7FFFFFFF;
+    for (int p = 1; p <= most; ++p) {
+        const int time = (items * p + warps - 1) / warps * ((steps + p - 1) / p + 2);
+        if (time < least) best = p, least = time;
+    }
+    return best;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -465,7 +477,7 @@ __device__ __forceinline__ float load_of_block(const float* p, int rank) {      
 }
 
 template <int DT, int WDT, bool kVec, int N8, int MT>
-__global__ void __launch_bounds__(kOutWarps * 32, OUT_CTAS) out_kernel(LayerArgs a, int id_bytes) {
+__global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int id_bytes) {
     constexpr int ve = Elem<DT>::kVE, es = Elem<DT>::kSize, step = 8 * ve, width = 16 * MT;
     extern __shared__ __align__(16) unsigned char dynamic[];
     __shared__ int item_count;
@@ -475,13 +487,22 @@ __global__ void __launch_bounds__(kOutWarps * 32, OUT_CTAS) out_kernel(LayerArgs
     place_items(it, dynamic, dynamic + items_bytes(slots), slots, a.experts);
     if (a.hidden == 0) pdl_wait();                                   // no in_kernel, which would have waited for the ids
     sort_slots(it, &item_count, a, id_bytes, 8 * N8);
-    pdl_wait();
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
     const int blocks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
     const int steps = (a.hidden + step - 1) / step, ld = h_ld(a.hidden);
     const int parts = k_parts(it.count, slots, steps, kOutWarps * blocks, MT), units = it.count * parts;
     const int c0 = static_cast<int>(blockIdx.x) * width;
     const size_t row_bytes = static_cast<size_t>(a.hidden) * es;
+    // The weights do not depend on in_kernel: a warp's first ones go to L2 while it
+    // ends (the first two lines of 16 rows; 1 x 8 of 128 experts 25.6 -> 22.8 us).
+    if (kVec && rank + blocks * warp < units) {
+        const int unit = rank + blocks * warp, r = c0 + (lane & 15), s = unit % parts + (lane >> 4) * parts;
+        if (r < a.cols && s < steps)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.w_out) +
+                                                       (static_cast<size_t>(it.expert[unit / parts]) * a.cols + r) * row_bytes +
+                                                       static_cast<size_t>(s) * 128));
+    }
+    pdl_wait();
     for (int unit = rank + blocks * warp; unit < units; unit += blocks * kOutWarps) {
         const int item = unit / parts, part = unit % parts, n = it.slots[item], first = it.first[item];
         const char* base = static_cast<const char*>(a.w_out) + static_cast<size_t>(it.expert[item]) * a.cols * row_bytes;
@@ -596,14 +617,14 @@ cudaError_t launch_kernels(int id_bytes, const LayerArgs& a, cudaStream_t s) {
     if (a.hidden > 0) {
         const int per = (a.gated ? 8 : 16) * IMT, row_tiles = (a.hidden + per - 1) / per;
         const size_t most = static_cast<size_t>(slots) * static_cast<size_t>(row_tiles);
-        const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * IN_CTAS));
+        const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * kInBlocks<IN8>));
         e = launch_kernel_smem(in_kernel<DT, kVec, IN8, IMT>, dim3(grid), dim3(kInWarps * 32), items_bytes(slots) + scratch, s, a,
                                id_bytes, row_tiles);
         if (e != cudaSuccess) return e;
     }
     const int tiles = (a.cols + 16 * OMT - 1) / (16 * OMT);
     int blocks = 1;                                                  // as many blocks as are there at once
-    while (blocks < kMostCluster && tiles * blocks * 2 <= OUT_CTAS * kSMs) blocks *= 2;
+    while (blocks < kMostCluster && tiles * blocks * 2 <= kSMs) blocks *= 2;
     const size_t sums = static_cast<size_t>(parts_that_fit(slots, OMT)) * slots * OMT * 64;
     return launch_cluster(out, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(blocks)), kOutWarps * 32,
                           items_bytes(slots) + std::max(scratch, sums), s, a, id_bytes);

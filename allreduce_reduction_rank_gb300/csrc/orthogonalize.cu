@@ -19,7 +19,10 @@
 // Matrices between the kernels lie in blocks of 128 rows x 64 columns, 16 KiB of
 // hi and 16 KiB of lo, each as the tensor cores want it in shared memory: a tile
 // is fetched by bulk copies without a tensor map, and the same block serves as
-// an operand along its rows (X X^T, A A) and along its columns (.. X).
+// an operand along its rows (X X^T) and along its columns (.. X).  A and the
+// polynomial are symmetric: their blocks below the diagonal are neither computed
+// nor written; where they are wanted, the block across the diagonal is taken
+// along its columns.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -213,21 +216,17 @@ __device__ void step_factors(const OrthogonalizeArgs& a, const Beginning& begin,
 // ---------------------------------------------------------------------------
 // Values as two fp16 numbers.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
-    hi = __float2half_rn(v);
-    lo = __float2half_rn(__fsub_rn(v, __half2float(hi)));
-}
 
 // Eight values into 16 bytes of hi and of lo.
 __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        __half2 a, b;
-        split(v[2 * i], a.x, b.x);
-        split(v[2 * i + 1], a.y, b.y);
-        h[i] = *reinterpret_cast<uint32_t*>(&a);
-        l[i] = *reinterpret_cast<uint32_t*>(&b);
+        const __half2 a = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        const float2 w = __half22float2(a);
+        const __half2 b = __floats2half2_rn(__fsub_rn(v[2 * i], w.x), __fsub_rn(v[2 * i + 1], w.y));
+        h[i] = *reinterpret_cast<const uint32_t*>(&a);
+        l[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -339,6 +338,19 @@ template <int NT, bool SYMMETRIC> __device__ __forceinline__ Place place_of(cons
     return p;
 }
 
+// Whether the operands of a block of k are taken along their columns: X on the
+// right of the polynomial, and what lies below the diagonal of a symmetric
+// matrix.  (The NT / 128 rows of blocks on the right of A A are on one side of the
+// diagonal, or on it, which is stored whole.)
+struct Turned {
+    bool left, right;
+};
+template <int MODE, int NT> __device__ __forceinline__ Turned turned_of(const ProductArgs& a, const Place& at, int k) {
+    if (MODE == kGram) return {false, false};
+    if (MODE == kPoly) return {k / 2 < at.row, k / 2 < min((at.col + 1) * (NT / 128), a.rb) - 1};
+    return {k / 2 < at.row, true};
+}
+
 // A taker's 32 x 32 values in its staging, each half 32 rows of 64 bytes whose
 // 16-byte pieces are exchanged so that neither its rows nor its lines collide.
 __device__ __forceinline__ int staged(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
@@ -409,7 +421,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
     constexpr bool square = MODE == kGram || MODE == kPoly;
     const int row_block = row0 / 128, col_block = col0 / 64, half = col0 / 32 % 2, across = square ? 2 * a.rb : a.cb;
     if (col_block >= across) return;
-    if (square && col0 / 128 < row_block) return;                 // below the diagonal: the tile across it writes them
+    if (square && col0 / 128 < row_block) return;                 // below the diagonal
     const size_t block = static_cast<size_t>(row_block) * across + col_block;
     unsigned char* to = a.to + at.z * a.to_stride;
     if (MODE == kPoly) {
@@ -447,18 +459,6 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
         *reinterpret_cast<uint4*>(staging + 2048 + staged(lane, p)) = lo;
     }
     store_staged(staging, to + block * kBlock, row0 % 128, half, lane);
-    if (square && col0 / 128 > row_block) {                        // the same across the diagonal
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            __half hi, lo;
-            split(v[j], hi, lo);
-            unsigned char* s = staging + staged(j, lane / 8) + 2 * (lane % 8);
-            *reinterpret_cast<__half*>(s) = hi;
-            *reinterpret_cast<__half*>(s + 2048) = lo;
-        }
-        const size_t other = static_cast<size_t>(col0 / 128) * across + row0 / 64;
-        store_staged(staging, to + other * kBlock, col0 % 128, row0 / 32 % 2, lane);
-    }
 }
 
 template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 1) product_kernel(ProductArgs a) {
@@ -500,32 +500,39 @@ template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 
             bool ok = true;
             for (unsigned tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
                 const Place at = place_of<NT, square>(a, tile);
-                const unsigned char* left = a.p + at.z * a.p_stride + static_cast<size_t>(at.row) * (MODE == kGram ? a.cb : 2 * a.rb) * kBlock;
-                const unsigned char* right = a.q + at.z * a.q_stride;
+                const unsigned char *left = a.p + at.z * a.p_stride, *right = a.q + at.z * a.q_stride;
+                const int across = MODE == kGram ? a.cb : 2 * a.rb;
+                const int have = square ? min(NT / 128, a.rb - at.col * (NT / 128)) : min(NT / 64, a.cb - at.col * (NT / 64));
                 for (int k = 0; k < a.kb && ok; ++k) {
                     const int s = static_cast<int>(issued % stages);
                     ok = issued < static_cast<uint32_t>(stages) || tc::barrier_wait(empty(s), (issued / stages - 1) & 1, abort_word);
                     if (!ok) break;
                     const uint32_t to = tc::shared_address(smem + s * kStageBytes<NT>), b_hi = to + kBlock, b_lo = b_hi + NT * 128;
-                    if (square) {
-                        const int across = MODE == kGram ? a.cb : 2 * a.rb, have = min(NT / 128, a.rb - at.col * (NT / 128));
-                        tc::barrier_expect(full(s), static_cast<uint32_t>(kBlock) * (1 + have));
+                    const Turned turned = turned_of<MODE, NT>(a, at, k);
+                    // 64 rows (of k) of `count` blocks in a row, hi and lo
+                    const auto along_columns = [&](uint32_t hi, uint32_t lo, const unsigned char* from, int across_from, int first, int count) {
+                        const unsigned char* src = from + (static_cast<size_t>(k / 2) * across_from + first) * kBlock + (k % 2) * (kHalfBlock / 2);
+                        for (int j = 0; j < count; ++j) {
+                            tc::bulk_load(hi + j * (kHalfBlock / 2), src + j * kBlock, kHalfBlock / 2, full(s));
+                            tc::bulk_load(lo + j * (kHalfBlock / 2), src + j * kBlock + kHalfBlock, kHalfBlock / 2, full(s));
+                        }
+                    };
+                    tc::barrier_expect(full(s), static_cast<uint32_t>(kBlock) + static_cast<uint32_t>(square ? kBlock : kHalfBlock) * have);
+                    if (turned.left)
+                        along_columns(to, to + kHalfBlock, left, across, 2 * at.row, 2);
+                    else
+                        tc::bulk_load(to, left + (static_cast<size_t>(at.row) * across + k) * kBlock, kBlock, full(s));
+                    if (!square) {
+                        along_columns(b_hi, b_lo, right, a.cb, at.col * (NT / 64), have);
+                    } else if (turned.right) {
+                        along_columns(b_hi, b_lo, right, across, at.col * (NT / 64), 2 * have);
+                    } else {
                         for (int j = 0; j < have; ++j) {
                             const unsigned char* from = right + (static_cast<size_t>(at.col * (NT / 128) + j) * across + k) * kBlock;
                             tc::bulk_load(b_hi + j * kHalfBlock, from, kHalfBlock, full(s));
                             tc::bulk_load(b_lo + j * kHalfBlock, from + kHalfBlock, kHalfBlock, full(s));
                         }
-                    } else {
-                        const int have = min(NT / 64, a.cb - at.col * (NT / 64));
-                        tc::barrier_expect(full(s), static_cast<uint32_t>(kBlock) + static_cast<uint32_t>(kHalfBlock) * have);
-                        for (int j = 0; j < have; ++j) {
-                            const unsigned char* from =
-                                right + (static_cast<size_t>(k / 2) * a.cb + at.col * (NT / 64) + j) * kBlock + (k % 2) * (kHalfBlock / 2);
-                            tc::bulk_load(b_hi + j * (kHalfBlock / 2), from, kHalfBlock / 2, full(s));
-                            tc::bulk_load(b_lo + j * (kHalfBlock / 2), from + kHalfBlock, kHalfBlock / 2, full(s));
-                        }
                     }
-                    tc::bulk_load(to, left + static_cast<size_t>(k) * kBlock, kBlock, full(s));
                     ++issued;
                 }
             }
@@ -540,10 +547,10 @@ template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t instruction = tc::instruction_f16(128, NT, !square);
             uint32_t used = 0;
             bool ok = true;
             for (unsigned tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
+                const Place at = place_of<NT, square>(a, tile);
                 for (int k = 0; k < a.kb && ok; ++k) {
                     const uint32_t b = used & 1;
                     ok = used < 2 || tc::barrier_wait(taken(b), (used / 2 - 1) & 1, abort_word);
@@ -555,20 +562,21 @@ template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 
                     tc::fence_after();
                     const uint32_t from = tc::shared_address(smem + s * kStageBytes<NT>), acc = acc0 + b * NT;
                     const uint32_t a_hi = from, a_lo = from + kHalfBlock, b_hi = from + kBlock, b_lo = b_hi + NT * 128;
-                    constexpr uint32_t b_step = square ? 32 : 2048;           // 16 along k
-                    const auto right = [&](uint32_t at) { return tc::operand(at, square ? 0 : 8192, 1024); };
+                    const Turned turned = turned_of<MODE, NT>(a, at, k);
+                    const uint32_t instruction = tc::instruction_f16(128, NT, turned.left, turned.right);
+                    const uint32_t a_step = turned.left ? 2048 : 32, b_step = turned.right ? 2048 : 32;          // 16 along k
+                    const auto operand_a = [&](uint32_t from_a) { return tc::operand(from_a, turned.left ? kHalfBlock / 2 : 0, 1024); };
+                    const auto operand_b = [&](uint32_t from_b) { return tc::operand(from_b, turned.right ? kHalfBlock / 2 : 0, 1024); };
                     // hi lo and lo hi first, while the sums are small and their
                     // truncation with them; then hi hi.
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint64_t ah = tc::operand(a_hi + 32 * i, 0, 1024), al = tc::operand(a_lo + 32 * i, 0, 1024);
-                        const uint64_t bh = right(b_hi + b_step * i), bl = right(b_lo + b_step * i);
-                        tc::mma_f16(acc, ah, bl, instruction, i != 0);
-                        tc::mma_f16(acc, al, bh, instruction, true);
+                        tc::mma_f16(acc, operand_a(a_hi + a_step * i), operand_b(b_lo + b_step * i), instruction, i != 0);
+                        tc::mma_f16(acc, operand_a(a_lo + a_step * i), operand_b(b_hi + b_step * i), instruction, true);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        tc::mma_f16(acc, tc::operand(a_hi + 32 * i, 0, 1024), right(b_hi + b_step * i), instruction, true);
+                        tc::mma_f16(acc, operand_a(a_hi + a_step * i), operand_b(b_hi + b_step * i), instruction, true);
                     tc::mma_commit(empty(s));
                     tc::mma_commit(made(b));
                     ++used;

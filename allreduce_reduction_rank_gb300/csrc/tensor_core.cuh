@@ -92,9 +92,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t address, uint32_t lead, uin
            static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-// fp16 x fp16 into binary32: M rows of A by N rows (columns, `mn_major_b`) of B.
-__host__ __device__ constexpr uint32_t instruction_f16(int m, int n, bool mn_major_b) {
-    return 1u << 4 | (mn_major_b ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
+// fp16 x fp16 into binary32: M rows of A by N of B, either of them MN-major.
+__host__ __device__ constexpr uint32_t instruction_f16(int m, int n, bool mn_major_a, bool mn_major_b) {
+    return 1u << 4 | (mn_major_a ? 1u << 15 : 0u) | (mn_major_b ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
+           static_cast<uint32_t>(m >> 4) << 24;
 }
 
 // One thread: accumulators (+)= A B over k = 16.

@@ -466,7 +466,7 @@ __device__ __forceinline__ int k_parts(int items, int slots, int steps, int warp
 }
 
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ float load_of_block(const float* p, int rank) {      // the same place in a block of the cluster
     uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));

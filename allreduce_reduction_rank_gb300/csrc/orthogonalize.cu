@@ -300,38 +300,42 @@ struct ProductArgs {
     bool transposed;
 };
 
-// A tile is 128 rows x NT columns.  Warp 0 fetches, warp 1 multiplies (2 and 3
-// only make up the group of four whose registers are given away), eight warps
-// take the accumulators out: 32 rows and half of the columns each.
+// A tile is 128 x 128, or 256 x 256 by a pair of blocks, of 128 rows each.  Per
+// block of k a SM fetches 64 KiB either way, for twice as many products in a
+// pair: one block's tiles of 128 x 256 took 98 KiB for those, and the 12 TB/s that
+// all SMs drew from L2 bound them (4096 x 4096 bf16: 3.37 ms in all, pairs 2.93).
+//
+// Warp 0 fetches, warp 1 multiplies for both blocks (in the second it says when its
+// operands are there), 2 and 3 only make up the group of four whose registers are
+// given away; eight warps take the accumulators out: 32 rows and half of the columns
+// each.
+template <bool PAIR> constexpr int kTile = PAIR ? 256 : 128;
 constexpr int kTakers = 8, kThreads = 128 + 32 * kTakers;
 // Registers of a thread: at the launch, then of the first four warps and of the
 // takers, which hold up to 128 sums.  The shares are below what was launched.
 constexpr int kLaunchRegisters = 168, kFewRegisters = 40, kManyRegisters = 224;
 static_assert(128 * kFewRegisters + 32 * kTakers * kManyRegisters <= kThreads * kLaunchRegisters, "registers");
 constexpr int kStaging = 4096;         // of each taker: 32 rows x 32 columns, hi and lo, or binary32
-
-template <int NT> constexpr int kStageBytes = static_cast<int>(kBlock) + NT * 256;
-template <int NT> constexpr int kStages = NT == 256 ? 2 : 3;
-template <int NT> constexpr size_t kSmem = 1024 + size_t(kStages<NT>) * kStageBytes<NT> + kTakers * kStaging;
+constexpr int kStages = 3, kStageBytes = 2 * static_cast<int>(kBlock);        // 128 rows of each operand, 64 along k
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kTakers * kStaging;
 
 struct Place {
     size_t z;
-    int row, col;                      // first block of rows; first column / NT
+    int row, col;                      // in tiles
 };
 
-// The tiles of a symmetric product: those that reach the diagonal or lie above.
-template <int NT, bool SYMMETRIC> __device__ __forceinline__ Place place_of(const ProductArgs& a, unsigned tile) {
+// The tiles of a symmetric product: those on the diagonal and above.
+template <bool PAIR, bool SYMMETRIC> __device__ __forceinline__ Place place_of(const ProductArgs& a, unsigned tile) {
     Place p;
     p.z = tile / a.per_matrix;
     int left = static_cast<int>(tile % a.per_matrix);
-    constexpr int per = NT / 128;
     if (SYMMETRIC) {
-        const int across = (a.rb + per - 1) / per;
+        const int across = (a.rb * 128 + kTile<PAIR> - 1) / kTile<PAIR>;
         p.row = 0;
-        while (left >= across - p.row / per) left -= across - p.row / per, ++p.row;
-        p.col = p.row / per + left;
+        while (left >= across - p.row) left -= across - p.row, ++p.row;
+        p.col = p.row + left;
     } else {
-        const int across = (a.n + NT - 1) / NT;
+        const int across = (a.n + kTile<PAIR> - 1) / kTile<PAIR>;
         p.row = left / across;
         p.col = left % across;
     }
@@ -340,15 +344,17 @@ template <int NT, bool SYMMETRIC> __device__ __forceinline__ Place place_of(cons
 
 // Whether the operands of a block of k are taken along their columns: X on the
 // right of the polynomial, and what lies below the diagonal of a symmetric
-// matrix.  (The NT / 128 rows of blocks on the right of A A are on one side of the
-// diagonal, or on it, which is stored whole.)
+// matrix.  Of a pair's two blocks of rows (or columns) both are on one side of the
+// diagonal, or on it, where blocks are stored whole.
 struct Turned {
     bool left, right;
 };
-template <int MODE, int NT> __device__ __forceinline__ Turned turned_of(const ProductArgs& a, const Place& at, int k) {
+template <int MODE, bool PAIR> __device__ __forceinline__ Turned turned_of(const Place& at, int k) {
+    constexpr int per = PAIR ? 2 : 1;
+    const bool left = k / 2 < per * (at.row + 1) - 1, right = k / 2 < per * (at.col + 1) - 1;
     if (MODE == kGram) return {false, false};
-    if (MODE == kPoly) return {k / 2 < at.row, k / 2 < min((at.col + 1) * (NT / 128), a.rb) - 1};
-    return {k / 2 < at.row, true};
+    if (MODE == kPoly) return {left, right};
+    return {left, true};
 }
 
 // A taker's 32 x 32 values in its staging, each half 32 rows of 64 bytes whose
@@ -420,7 +426,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
     }
     constexpr bool square = MODE == kGram || MODE == kPoly;
     const int row_block = row0 / 128, col_block = col0 / 64, half = col0 / 32 % 2, across = square ? 2 * a.rb : a.cb;
-    if (col_block >= across) return;
+    if (col_block >= across || row_block >= a.rb) return;
     if (square && col0 / 128 < row_block) return;                 // below the diagonal
     const size_t block = static_cast<size_t>(row_block) * across + col_block;
     unsigned char* to = a.to + at.z * a.to_stride;
@@ -461,30 +467,35 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
     store_staged(staging, to + block * kBlock, row0 % 128, half, lane);
 }
 
-template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 1) product_kernel(ProductArgs a) {
-    constexpr bool square = MODE == kGram || MODE == kPoly;       // B's rows run along k
-    constexpr int stages = kStages<NT>;
+template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bounds__(kThreads, 1) product_kernel(ProductArgs a) {
+    constexpr bool square = MODE == kGram || MODE == kPoly;       // the right operand is a symmetric matrix's, or X's rows
+    constexpr int stages = kStages, blocks = PAIR ? 2 : 1, wide = kTile<PAIR>, depth = 512 / wide;
     extern __shared__ unsigned char dynamic[];
-    __shared__ uint64_t bars[2 * stages + 5];
+    __shared__ uint64_t bars[3 * stages + 9];
     __shared__ uint32_t tmem;
     __shared__ int aborted;
     unsigned char* smem = dynamic + (1024 - tc::shared_address(dynamic) % 1024) % 1024;
-    unsigned char* staging = smem + stages * kStageBytes<NT>;
+    unsigned char* staging = smem + stages * kStageBytes;
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+    const int rank = PAIR ? static_cast<int>(tc::cluster_rank()) : 0;
+    const unsigned first_tile = blockIdx.x / blocks, tile_step = gridDim.x / blocks;
     const uint32_t bar0 = tc::shared_address(bars);
-    const auto full = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };
-    const auto empty = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(stages + s); };
-    const auto taken = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * stages + b); };
-    const auto made = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(2 * stages + 2 + b); };
-    const uint32_t drained = bar0 + 8u * (2 * stages + 4);
+    const auto full = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };                       // fetched
+    const auto empty = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(stages + s); };             // multiplied
+    const auto other = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(2 * stages + s); };         // fetched by the other block
+    const auto taken = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(3 * stages + b); };
+    const auto made = [&](int b) { return bar0 + 8u * static_cast<uint32_t>(3 * stages + 4 + b); };
+    const uint32_t drained = bar0 + 8u * (3 * stages + 8);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) tc::barrier_init(full(s), 1), tc::barrier_init(empty(s), 1);
-        for (int b = 0; b < 2; ++b) tc::barrier_init(made(b), 1), tc::barrier_init(taken(b), kTakers);
+        for (int s = 0; s < stages; ++s) tc::barrier_init(full(s), 1), tc::barrier_init(empty(s), 1), tc::barrier_init(other(s), 1);
+        for (int b = 0; b < 4; ++b) tc::barrier_init(made(b), 1), tc::barrier_init(taken(b), kTakers * blocks);
         tc::barrier_init(drained, 1);
         aborted = 0;
         tc::barrier_init_fence();
     }
-    if (warp == 1) tc::tmem_alloc<512>(&tmem);
+    __syncthreads();
+    if (PAIR) tc::cluster_sync();                                 // the other block's barriers are there
+    if (warp == 1) tc::tmem_alloc<512, PAIR>(&tmem);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -498,41 +509,39 @@ template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 
             tc::fence_async();
             uint32_t issued = 0;
             bool ok = true;
-            for (unsigned tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
-                const Place at = place_of<NT, square>(a, tile);
+            for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
+                const Place at = place_of<PAIR, square>(a, tile);
                 const unsigned char *left = a.p + at.z * a.p_stride, *right = a.q + at.z * a.q_stride;
                 const int across = MODE == kGram ? a.cb : 2 * a.rb;
-                const int have = square ? min(NT / 128, a.rb - at.col * (NT / 128)) : min(NT / 64, a.cb - at.col * (NT / 64));
+                const int row = at.row * blocks + rank, col = at.col * blocks + rank;     // this block's rows; its part of the right
+                const int pieces = max(0, min(2, (square ? 2 * a.rb : a.cb) - 2 * col));  // blocks of 64 on the right that there are
+                const uint32_t bytes = (row < a.rb ? static_cast<uint32_t>(kBlock) : 0u) + static_cast<uint32_t>(kHalfBlock) * pieces;
                 for (int k = 0; k < a.kb && ok; ++k) {
                     const int s = static_cast<int>(issued % stages);
-                    ok = issued < static_cast<uint32_t>(stages) || tc::barrier_wait(empty(s), (issued / stages - 1) & 1, abort_word);
+                    ok = issued < static_cast<uint32_t>(stages) ||
+                         tc::barrier_wait<PAIR>(empty(s), (issued / stages - 1) & 1, abort_word);
                     if (!ok) break;
-                    const uint32_t to = tc::shared_address(smem + s * kStageBytes<NT>), b_hi = to + kBlock, b_lo = b_hi + NT * 128;
-                    const Turned turned = turned_of<MODE, NT>(a, at, k);
+                    const uint32_t to = tc::shared_address(smem + s * kStageBytes), bar = full(s);
+                    const Turned turned = turned_of<MODE, PAIR>(at, k);
                     // 64 rows (of k) of `count` blocks in a row, hi and lo
-                    const auto along_columns = [&](uint32_t hi, uint32_t lo, const unsigned char* from, int across_from, int first, int count) {
+                    const auto along_columns = [&](uint32_t hi, const unsigned char* from, int across_from, int first, int count) {
                         const unsigned char* src = from + (static_cast<size_t>(k / 2) * across_from + first) * kBlock + (k % 2) * (kHalfBlock / 2);
                         for (int j = 0; j < count; ++j) {
-                            tc::bulk_load(hi + j * (kHalfBlock / 2), src + j * kBlock, kHalfBlock / 2, full(s));
-                            tc::bulk_load(lo + j * (kHalfBlock / 2), src + j * kBlock + kHalfBlock, kHalfBlock / 2, full(s));
+                            tc::bulk_load(hi + j * (kHalfBlock / 2), src + j * kBlock, kHalfBlock / 2, bar);
+                            tc::bulk_load(hi + kHalfBlock + j * (kHalfBlock / 2), src + j * kBlock + kHalfBlock, kHalfBlock / 2, bar);
                         }
                     };
-                    tc::barrier_expect(full(s), static_cast<uint32_t>(kBlock) + static_cast<uint32_t>(square ? kBlock : kHalfBlock) * have);
-                    if (turned.left)
-                        along_columns(to, to + kHalfBlock, left, across, 2 * at.row, 2);
-                    else
-                        tc::bulk_load(to, left + (static_cast<size_t>(at.row) * across + k) * kBlock, kBlock, full(s));
-                    if (!square) {
-                        along_columns(b_hi, b_lo, right, a.cb, at.col * (NT / 64), have);
-                    } else if (turned.right) {
-                        along_columns(b_hi, b_lo, right, across, at.col * (NT / 64), 2 * have);
-                    } else {
-                        for (int j = 0; j < have; ++j) {
-                            const unsigned char* from = right + (static_cast<size_t>(at.col * (NT / 128) + j) * across + k) * kBlock;
-                            tc::bulk_load(b_hi + j * kHalfBlock, from, kHalfBlock, full(s));
-                            tc::bulk_load(b_lo + j * kHalfBlock, from + kHalfBlock, kHalfBlock, full(s));
-                        }
+                    tc::barrier_expect(bar, bytes);
+                    if (row < a.rb) {
+                        if (turned.left)
+                            along_columns(to, left, across, 2 * row, 2);
+                        else
+                            tc::bulk_load(to, left + (static_cast<size_t>(row) * across + k) * kBlock, kBlock, bar);
                     }
+                    if (turned.right)
+                        along_columns(to + kBlock, right, square ? across : a.cb, 2 * col, pieces);
+                    else if (pieces > 0)
+                        tc::bulk_load(to + kBlock, right + (static_cast<size_t>(col) * across + k) * kBlock, kBlock, bar);
                     ++issued;
                 }
             }
@@ -540,89 +549,114 @@ template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 
             // multiplied, or at least have arrived.
             for (uint32_t i = issued > static_cast<uint32_t>(stages) ? issued - stages : 0; i < issued; ++i) {
                 const int s = static_cast<int>(i % stages);
-                if (ok) ok = tc::barrier_wait(empty(s), (i / stages) & 1, abort_word);
+                if (ok) ok = tc::barrier_wait<PAIR>(empty(s), (i / stages) & 1, abort_word);
                 if (!ok) tc::barrier_wait(full(s), (i / stages) & 1, nullptr);
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         if (lane == 0) {
-            uint32_t used = 0;
+            uint32_t used = 0, chunk = 0;
             bool ok = true;
-            for (unsigned tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
-                const Place at = place_of<NT, square>(a, tile);
-                for (int k = 0; k < a.kb && ok; ++k) {
-                    const uint32_t b = used & 1;
-                    ok = used < 2 || tc::barrier_wait(taken(b), (used / 2 - 1) & 1, abort_word);
+            for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
+                const Place at = place_of<PAIR, square>(a, tile);
+                for (int k = 0; k < a.kb && ok; ++k, ++used) {
+                    const bool begins = k % CHUNK == 0, ends = (k + 1) % CHUNK == 0 || k + 1 == a.kb;
+                    const int slot = static_cast<int>(chunk % depth), s = static_cast<int>(used % stages);
+                    ok = !begins || chunk < depth || tc::barrier_wait<PAIR>(taken(slot), (chunk / depth - 1) & 1, abort_word);
+                    ok = ok && tc::barrier_wait(full(s), (used / stages) & 1, abort_word) &&
+                         (!PAIR || tc::barrier_wait<PAIR>(other(s), (used / stages) & 1, abort_word));
                     if (!ok) break;
                     tc::fence_after();
-                    const int s = static_cast<int>(used % stages);
-                    ok = tc::barrier_wait(full(s), (used / stages) & 1, abort_word);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t from = tc::shared_address(smem + s * kStageBytes<NT>), acc = acc0 + b * NT;
-                    const uint32_t a_hi = from, a_lo = from + kHalfBlock, b_hi = from + kBlock, b_lo = b_hi + NT * 128;
-                    const Turned turned = turned_of<MODE, NT>(a, at, k);
-                    const uint32_t instruction = tc::instruction_f16(128, NT, turned.left, turned.right);
+                    const uint32_t acc = acc0 + slot * wide, left = tc::shared_address(smem + s * kStageBytes), right = left + kBlock;
+                    const Turned turned = turned_of<MODE, PAIR>(at, k);
+                    const uint32_t instruction = tc::instruction_f16(wide, wide, turned.left, turned.right);
                     const uint32_t a_step = turned.left ? 2048 : 32, b_step = turned.right ? 2048 : 32;          // 16 along k
-                    const auto operand_a = [&](uint32_t from_a) { return tc::operand(from_a, turned.left ? kHalfBlock / 2 : 0, 1024); };
-                    const auto operand_b = [&](uint32_t from_b) { return tc::operand(from_b, turned.right ? kHalfBlock / 2 : 0, 1024); };
+                    const auto operand_a = [&](uint32_t from) { return tc::operand(from, turned.left ? kHalfBlock / 2 : 0, 1024); };
+                    const auto operand_b = [&](uint32_t from) { return tc::operand(from, turned.right ? kHalfBlock / 2 : 0, 1024); };
                     // hi lo and lo hi first, while the sums are small and their
                     // truncation with them; then hi hi.
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        tc::mma_f16(acc, operand_a(a_hi + a_step * i), operand_b(b_lo + b_step * i), instruction, i != 0);
-                        tc::mma_f16(acc, operand_a(a_lo + a_step * i), operand_b(b_hi + b_step * i), instruction, true);
+                        tc::mma_f16<PAIR>(acc, operand_a(left + a_step * i), operand_b(right + kHalfBlock + b_step * i), instruction,
+                                          i != 0 || !begins);
+                        tc::mma_f16<PAIR>(acc, operand_a(left + kHalfBlock + a_step * i), operand_b(right + b_step * i), instruction, true);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        tc::mma_f16(acc, operand_a(a_hi + a_step * i), operand_b(b_hi + b_step * i), instruction, true);
-                    tc::mma_commit(empty(s));
-                    tc::mma_commit(made(b));
-                    ++used;
+                        tc::mma_f16<PAIR>(acc, operand_a(left + a_step * i), operand_b(right + b_step * i), instruction, true);
+                    tc::mma_commit<PAIR>(empty(s));
+                    if (ends) tc::mma_commit<PAIR>(made(slot)), ++chunk;
                 }
             }
             if (!ok) {                                                         // products in flight
-                tc::mma_commit(drained);
+                tc::mma_commit<PAIR>(drained);
                 tc::barrier_wait(drained, 0, nullptr);
             }
+        }
+        __syncwarp();
+    } else if (PAIR && warp == 1) {
+        if (lane == 0) {                                                       // this block's operands are there
+            uint32_t seen = 0;
+            bool ok = true;
+            for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step)
+                for (int k = 0; k < a.kb && ok; ++k, ++seen) {
+                    const int s = static_cast<int>(seen % stages);
+                    ok = tc::barrier_wait(full(s), (seen / stages) & 1, abort_word);
+                    if (ok) tc::barrier_arrive_cluster(tc::barrier_of(other(s), 0));
+                }
         }
         __syncwarp();
     } else if (warp >= 4) {
         tc::more_registers<kManyRegisters>();
         const int taker = warp - 4, quarter = warp & 3, half = taker / 4;
         unsigned char* mine = staging + taker * kStaging;
-        constexpr int groups = NT / 64;                                       // of 32 columns, for each taker
+        constexpr int groups = wide / 64;                                     // of 32 columns, for each taker
+        const uint32_t taken0 = PAIR ? tc::barrier_of(taken(0), 0) : taken(0);
         uint32_t chunk = 0;
         bool ok = true;
-        for (unsigned tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
-            const Place at = place_of<NT, square>(a, tile);
+        for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
+            const Place at = place_of<PAIR, square>(a, tile);
             float sums[groups][32];
 #pragma unroll
             for (int g = 0; g < groups; ++g)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sums[g][j] = 0.0f;
-            for (int i = 0; i < a.kb && ok; ++i, ++chunk) {
-                const uint32_t b = chunk & 1;
-                ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(made(b), (chunk / 2) & 1, abort_word));
+            for (int i = 0; i < (a.kb + CHUNK - 1) / CHUNK && ok; ++i, ++chunk) {
+                const int slot = static_cast<int>(chunk % depth);
+                ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait<PAIR>(made(slot), (chunk / depth) & 1, abort_word));
                 if (!ok) break;
                 tc::fence_after();
-                const uint32_t from = acc0 + b * NT + half * (NT / 2) + (static_cast<uint32_t>(quarter) << 21);
+                const uint32_t from = acc0 + slot * wide + half * (wide / 2) + (static_cast<uint32_t>(quarter) << 21);
+                // Two loads at a time; the accumulators are free once the last have
+                // come, before they are added.
 #pragma unroll
-                for (int g = 0; g < groups; ++g) {
-                    float v[32];
-                    tc::tmem_load(from + 32 * g, v);
+                for (int g = 0; g < groups; g += 2) {
+                    uint32_t v[2][32];
+                    tc::tmem_load(from + 32 * g, v[0]);
+                    tc::tmem_load(from + 32 * g + 32, v[1]);
+                    tc::tmem_wait(v[0]);
+                    tc::tmem_wait(v[1]);
+                    if (g + 2 >= groups) {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (PAIR)
+                                tc::barrier_arrive_cluster(taken0 + 8 * slot);
+                            else
+                                tc::barrier_arrive(taken0 + 8 * slot);
+                        }
+                    }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) sums[g][j] = __fadd_rn(sums[g][j], v[j]);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sums[g + h][j] = __fadd_rn(sums[g + h][j], __uint_as_float(v[h][j]));
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::barrier_arrive(taken(b));
             }
             if (!ok) break;
             const StepFactors f = a.factors[at.z * kMaxSteps];
             const bool failed = MODE == kLast && *static_cast<volatile int*>(a.failed) != 0;
-            const int row0 = at.row * 128 + quarter * 32, col0 = at.col * NT + half * (NT / 2);
+            const int row0 = (at.row * blocks + rank) * 128 + quarter * 32, col0 = at.col * wide + half * (wide / 2);
 #pragma unroll
             for (int g = 0; g < groups; ++g) finish<MODE, DT>(a, at, f, sums[g], row0, col0 + 32 * g, mine, lane, failed);
         }
@@ -630,44 +664,68 @@ template <int MODE, int NT, int DT> __global__ void __launch_bounds__(kThreads, 
     tc::fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && aborted != 0) *static_cast<volatile int*>(a.failed) = 1;
+    if (PAIR) tc::cluster_sync();                                 // the products over both blocks' memory are done
     if (warp == 1) {
         tc::fence_after();
-        tc::tmem_free<512>(acc0);
+        tc::tmem_free<512, PAIR>(acc0);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Host.
 // ---------------------------------------------------------------------------
-template <int MODE, int NT, int DT> cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
+template <int MODE, bool PAIR, int CHUNK, int DT> cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
     static std::atomic<bool> allowed[kDevices];
     static std::atomic<int> registers;
-    cudaError_t e = allow_smem(product_kernel<MODE, NT, DT>, kSmem<NT>, allowed);
+    const auto kernel = product_kernel<MODE, PAIR, CHUNK, DT>;
+    cudaError_t e = allow_smem(kernel, kSmem, allowed);
     if (e != cudaSuccess) return e;
     if (registers.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes f;
-        if ((e = cudaFuncGetAttributes(&f, product_kernel<MODE, NT, DT>)) != cudaSuccess) return e;
+        if ((e = cudaFuncGetAttributes(&f, kernel)) != cudaSuccess) return e;
         registers.store(f.numRegs, std::memory_order_relaxed);
     }
     // The takers' registers come out of what the launch has: never wait for more.
     if (registers.load(std::memory_order_relaxed) != kLaunchRegisters) return cudaErrorInvalidConfiguration;
-    const unsigned grid = std::min<unsigned>(a.tiles, kSMs);
-    return launch_kernel_smem(product_kernel<MODE, NT, DT>, dim3(grid), dim3(kThreads), kSmem<NT>, s, a);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(PAIR ? 2 * std::min<unsigned>(a.tiles, kSMs / 2) : std::min<unsigned>(a.tiles, kSMs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int MODE, int NT, int DT = SAR_FP32> cudaError_t product(ProductArgs a, size_t batch, cudaStream_t s) {
-    const int per = NT / 128, across = (a.rb + per - 1) / per;
-    unsigned tiles = 0;
-    if (MODE == kGram || MODE == kPoly) {
-        for (int r = 0; r < a.rb; ++r) tiles += static_cast<unsigned>(across - r / per);
-    } else {
-        tiles = static_cast<unsigned>(a.rb) * static_cast<unsigned>((a.n + NT - 1) / NT);
-    }
-    a.per_matrix = tiles;
-    const size_t all = batch * tiles;
-    if (all > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    a.tiles = static_cast<unsigned>(all);
-    return launch_product<MODE, NT, DT>(a, s);
+size_t tiles_of(bool symmetric, int wide, const ProductArgs& a) {
+    const size_t rows = static_cast<size_t>((a.rb * 128 + wide - 1) / wide);
+    return symmetric ? rows * (rows + 1) / 2 : rows * static_cast<size_t>((a.n + wide - 1) / wide);
+}
+
+// Pairs of blocks or single ones, by their rounds over the SMs.  A pair's tile is two
+// of one block's for each SM, and those take longer: 128 columns of the right
+// operand are not enough for the tensor cores' full rate from shared memory, and more
+// comes from L2.  4096 x 4096, a tile's time of pairs and of singles: 37 and 47 us for
+// results of 16 bits; 45 and 50 us in binary32, where every block of k ends with the
+// accumulators being taken, and a pair's takers answer across two SMs.
+template <int MODE, int DT> cudaError_t product(ProductArgs a, size_t batch, cudaStream_t s) {
+    constexpr bool symmetric = MODE == kGram || MODE == kPoly;
+    // Blocks of 64 of k between two takings of the accumulators.  4 of them leave 7e-6
+    // of error (16 x 1024 x 1024), one 1.3e-6: results of 16 bits do not see the
+    // difference.
+    constexpr int chunk = DT == SAR_FP32 ? 1 : 4, type = MODE == kLast ? DT : SAR_FP32;
+    constexpr size_t pair_time = 200, single_time = DT == SAR_FP32 ? 110 : 129;
+    const size_t pairs = batch * tiles_of(symmetric, 256, a), singles = batch * tiles_of(symmetric, 128, a);
+    if (singles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const bool pair = a.rb > 1 && pair_time * ((pairs + kSMs / 2 - 1) / (kSMs / 2)) <= single_time * ((singles + kSMs - 1) / kSMs);
+    a.per_matrix = static_cast<unsigned>(tiles_of(symmetric, pair ? 256 : 128, a));
+    a.tiles = static_cast<unsigned>(pair ? pairs : singles);
+    return pair ? launch_product<MODE, true, chunk, type>(a, s) : launch_product<MODE, false, chunk, type>(a, s);
 }
 
 template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s) {
@@ -689,19 +747,19 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
         ProductArgs gram = g;
         gram.p = gram.q = w.x, gram.to = w.a, gram.p_stride = gram.q_stride = xs, gram.to_stride = as;
         gram.kb = g.cb;
-        if ((e = product<kGram, 256>(gram, a.batch, s)) != cudaSuccess) return e;
+        if ((e = product<kGram, DT>(gram, a.batch, s)) != cudaSuccess) return e;
         ProductArgs poly = g;
         poly.p = poly.q = w.a, poly.to = w.p, poly.p_stride = poly.q_stride = poly.to_stride = as;
         poly.kb = static_cast<int>((sz.m + 63) / 64);
-        if ((e = product<kPoly, 256>(poly, a.batch, s)) != cudaSuccess) return e;
+        if ((e = product<kPoly, DT>(poly, a.batch, s)) != cudaSuccess) return e;
         ProductArgs apply = g;
         apply.n = static_cast<int>(sz.n), apply.kb = poly.kb;
         apply.p = w.p, apply.q = w.x, apply.to = w.y, apply.p_stride = as, apply.q_stride = apply.to_stride = xs;
         if (k + 1 < a.steps) {
-            e = product<kApply, 256>(apply, a.batch, s);
+            e = product<kApply, DT>(apply, a.batch, s);
         } else {
             apply.out = a.out, apply.ldo = a.ldo, apply.ostride = a.ostride, apply.transposed = a.rows > a.cols;
-            e = product<kLast, 256, DT>(apply, a.batch, s);
+            e = product<kLast, DT>(apply, a.batch, s);
         }
         if (e != cudaSuccess) return e;
         std::swap(w.x, w.y);

@@ -74,6 +74,14 @@ def test_orthogonalize(sar, batch, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(ref.DTYPES))
+@pytest.mark.parametrize("batch,rows,cols", [(70, 256, 250), (12, 600, 600), (6, 600, 1000), (6, 1000, 600), (100, 130, 128),
+                                             (40, 200, 400), (1, 2600, 2700)])
+def test_many_tiles(sar, batch, rows, cols, dtype):
+    """Enough of them that pairs of blocks take some of the products, or all."""
+    check(sar, gradients(batch, rows, cols, ref.DTYPES[dtype], seed=rows), steps=2 if rows > 2000 else 5)
+
+
+@pytest.mark.parametrize("dtype", list(ref.DTYPES))
 @pytest.mark.parametrize("batch,rows,cols", [(3, 20, 37), (2, 150, 77), (2, 130, 140)])
 def test_layouts(sar, batch, rows, cols, dtype):
     g = gradients(batch, rows, cols, ref.DTYPES[dtype], seed=2)

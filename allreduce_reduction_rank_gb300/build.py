@@ -37,11 +37,11 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["ll_writeback.cu", "ll_fused.cu", "ll_cluster.cu", "ll_cta.cu", "rsag_e4m3b15.cu", "rsag_e4m3b15_acc.cu",
            "ll.cu", "rsag_e4m3fn_acc.cu", "rsag_e4m3fn.cu", "rsag_bf16_acc.cu", "rsag_fp16_acc.cu", "rsag_fp32_acc.cu", "rsag_fp16.cu",
            "rsag_bf16.cu", "rsag_fp32.cu", "layer_norm_bf16.cu", "layer_norm_fp16.cu", "layer_norm_fp32.cu",
-           "orthogonalize.cu", "expert_layer.cu", "layer_norm.cu", "experts.cu", "route.cu", "expert_sort.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
+           "orthogonalize.cu", "expert_layer.cu", "orthogonalize_small.cu", "layer_norm.cu", "experts.cu", "route.cu", "expert_sort.cu", "convert.cu", "rsag.cu", "sar_api.cu", "operators_api.cu",
            "noalloc.cu"]
 # The torch module's; all are compiled again for another interpreter or torch.
 BINDING_SOURCES = ["torch_binding.cpp", "torch_binding_block.cpp"]
-HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh", "layer_norm_ring.cuh", "tensor_core.cuh"]
+HEADERS = ["sar_device.cuh", "sar_internal.h", "rsag_kernels.cuh", "ll_coop.cuh", "ll_packets.cuh", "layer_norm.cuh", "layer_norm_ring.cuh", "tensor_core.cuh", "orthogonalize.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-std=c++17", "-lineinfo",

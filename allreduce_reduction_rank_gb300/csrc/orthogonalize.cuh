@@ -1,0 +1,138 @@
+// orthogonalize.cuh -- what both forms of the Newton-Schulz iteration share: the
+// norm, the powers of two that values are held times, and values as two fp16
+// numbers.
+#pragma once
+
+#include <cmath>
+
+#include "sar_device.cuh"
+#include "sar_internal.h"
+#include "tensor_core.cuh"
+
+namespace sar {
+namespace orthogonal {
+
+constexpr int kNormThreads = 256;
+constexpr size_t kHalfBlock = 16384, kBlock = 2 * kHalfBlock;
+
+// What the products of one step of one matrix multiply by: powers of two (times
+// a coefficient) between the scales of X, A and the polynomial.
+struct StepFactors {
+    float gram, square, linear, diagonal, apply, first, last, second;
+};
+constexpr size_t kMaxSteps = 64;
+
+// ---------------------------------------------------------------------------
+// The norm.
+// ---------------------------------------------------------------------------
+
+// Sums of squares whatever the values' magnitude: those that would overflow or
+// vanish are scaled, each kind in a sum of its own.
+struct Squares {
+    float big = 0.0f, mid = 0.0f, small = 0.0f;
+    __device__ __forceinline__ void add(float x) {
+        const float m = fabsf(x);
+        if (m > 0x1p45f) {
+            const float y = x * 0x1p-90f;
+            big = __fmaf_rn(y, y, big);
+        } else if (m < 0x1p-40f) {
+            const float y = x * 0x1p80f;
+            small = __fmaf_rn(y, y, small);
+        } else {
+            mid = __fmaf_rn(x, x, mid);
+        }
+    }
+};
+
+__device__ __forceinline__ float block_sum(float x, float* shared) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNormThreads / 32; ++w) s = __fadd_rn(s, shared[w]);
+    return s;
+}
+
+// What three sums of a block's (Squares) add up to.
+__device__ __forceinline__ double squares_sum(const float* sums) {
+    return static_cast<double>(sums[0]) * 0x1p180 + sums[1] + static_cast<double>(sums[2]) * 0x1p-160;
+}
+
+// The largest power of two that fp16 holds values up to `most` times, with 9% to
+// spare for the bound's and the values' roundings.
+__device__ __forceinline__ int scale_below(float most) { return most < 1e-38f ? 140 : ilogbf(60000.0f / most); }
+
+// 2^scale / (norm + eps) = f * first * second, the latter two powers of two: no
+// step leaves binary32's range where the product does not.  `top`: a bound of
+// the singular values of g / (norm + eps), and `scale` what X is held times.
+struct Beginning {
+    float f, first, second, top;
+    int scale;
+    __device__ __forceinline__ float of(float x) const { return x * first * f * second; }
+};
+
+// sum: of the squares.
+__device__ __forceinline__ Beginning beginning(double sum, float eps) {
+    const double norm = sqrt(sum), inv = 1.0 / (norm + static_cast<double>(eps));
+    if (!(inv > 0.0) || isinf(inv) || isinf(norm)) return {static_cast<float>(inv), 1.0f, 1.0f, 1.0f, 0};
+    const float top = static_cast<float>(norm * inv);
+    Beginning b;
+    b.top = top > 0.0f && top < 1.0f ? top : 1.0f;
+    b.scale = scale_below(b.top);
+    int e;
+    b.f = static_cast<float>(frexp(inv, &e));
+    e += b.scale;
+    b.first = ldexpf(1.0f, e / 2), b.second = ldexpf(1.0f, e - e / 2);
+    return b;
+}
+
+// The factors of a matrix's steps.  |p(s)| <= s (|a| + |b| s^2 + |c| s^4), and
+// never above `grown`.
+__device__ __forceinline__ void step_factors(const OrthogonalizeArgs& a, const Beginning& begin, StepFactors* to) {
+    float top = begin.top;
+    int x = begin.scale;
+    for (int k = 0; k < a.steps; ++k) {
+        const float square = top * top, most = fabsf(a.a) + square * (fabsf(a.b) + square * fabsf(a.c));
+        const float next = fminf(top * most, a.grown);
+        const int gram = 2 * x - 16, poly = scale_below(most), after = scale_below(next);
+        StepFactors f;
+        f.gram = ldexpf(1.0f, gram - 2 * x);
+        f.square = ldexpf(a.c, poly - 2 * gram);
+        f.linear = ldexpf(a.b, poly - gram);
+        f.diagonal = ldexpf(a.a, poly);
+        f.apply = ldexpf(1.0f, after - poly - x);
+        f.last = a.scale, f.first = ldexpf(1.0f, (-poly - x) / 2), f.second = ldexpf(1.0f, -poly - x - (-poly - x) / 2);
+        to[k] = f;
+        top = next, x = after;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Values as two fp16 numbers.
+// ---------------------------------------------------------------------------
+
+// Eight values into 16 bytes of hi and of lo.
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 a = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        const float2 w = __half22float2(a);
+        const __half2 b = __floats2half2_rn(__fsub_rn(v[2 * i], w.x), __fsub_rn(v[2 * i + 1], w.y));
+        h[i] = *reinterpret_cast<const uint32_t*>(&a);
+        l[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+}  // namespace orthogonal
+
+// The form for matrices of up to 128 rows (or columns): one launch.
+bool orthogonalize_small_fits(size_t rows, size_t cols);
+cudaError_t launch_orthogonalize_small(sar_dtype dt, const OrthogonalizeArgs& a, cudaStream_t s);
+
+}  // namespace sar

@@ -64,7 +64,8 @@ def check(sar, g, steps=5, coefficients=MUON, eps=1e-7, scale=1.0, **layout):
 
 SIZES = [(1, 1, 1), (1, 1, 7), (3, 5, 1), (2, 8, 8), (1, 16, 33), (5, 31, 17), (2, 64, 64), (1, 100, 60), (8, 128, 128),
          (2, 128, 200), (1, 129, 128), (1, 130, 300), (2, 256, 64), (1, 257, 255), (1, 500, 130), (1, 64, 1000), (1, 1003, 97),
-         (1, 384, 640), (40, 24, 56), (1, 512, 512)]
+         (1, 384, 640), (40, 24, 56), (1, 512, 512), (1, 8, 3648), (2, 4096, 100), (1, 4097, 100), (3, 65, 513), (1, 128, 1030),
+         (200, 16, 16)]
 
 
 @pytest.mark.parametrize("dtype", list(ref.DTYPES))

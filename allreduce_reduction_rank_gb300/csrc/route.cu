@@ -2,9 +2,15 @@
 // weights' softmax, and the logits' gradient.
 //
 // A warp takes a token.  Lane l holds the logits l, l + 32, ...: a row is read
-// once, in whole lines.  The topk largest are taken out one after another; a
-// logit is compared as the whole number of the same order (route_key), so that
-// infinities, NaN and -0 need no cases of their own.
+// once, in whole lines.  A logit is compared as the whole number of the same order
+// (route_key), so that infinities, NaN and -0 need no cases of their own.
+//
+// The best ones: the topk-th largest of the 32 lanes' largest, found by sorting
+// those, is a lower bound of what is chosen; the few logits from there on (9 to 12
+// of 256 for 8) move to a lane each and are ranked by comparing each with all.
+// Taking the largest out topk times took 70 us for 65536 tokens, 8 of 256, most of
+// it in 16 reductions over the warp a token; this takes 36, nearly all of it
+// instructions.
 #include <type_traits>
 
 #include "sar_device.cuh"
@@ -16,14 +22,27 @@ namespace {
 constexpr int kWarps = 8;
 constexpr uint32_t kMasked = 0x007FFFFFu;      // the key of minus infinity
 
-// Ascending with the value; -0 as +0, NaN above all.
+// Ascending with the value; -0 as +0, NaN above all: an addition's result is never
+// -0 here, and its NaN is always 0x7FFFFFFF.
 __device__ __forceinline__ uint32_t route_key(float x) {
-    if (x != x) return 0xFFFFFFFFu;
-    const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const int32_t u = __float_as_int(__fadd_rn(x, 0.0f));
+    return static_cast<uint32_t>(u ^ (u >> 31 | static_cast<int32_t>(0x80000000u)));
 }
 __device__ __forceinline__ float route_value(uint32_t key) {
-    return __uint_as_float(key & 0x80000000u ? (key == 0xFFFFFFFFu ? 0x7FFFFFFFu : key & 0x7FFFFFFFu) : ~key);
+    return __uint_as_float(key ^ (~static_cast<uint32_t>(static_cast<int32_t>(key) >> 31) | 0x80000000u));
+}
+
+// The lanes' values, the largest first.
+__device__ __forceinline__ uint32_t sort_lanes(uint32_t v, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int d = size >> 1; d > 0; d >>= 1) {
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, v, d);
+            const bool up = ((lane & size) == 0) == ((lane & d) == 0);          // this lane keeps the larger
+            v = up ? max(v, other) : min(v, other);
+        }
+    return v;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -47,6 +66,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    __shared__ uint64_t candidates[kWarps][32];
     const uint32_t top_key = __reduce_max_sync(0xFFFFFFFFu, best);
     const float top = top_key > kMasked ? route_value(top_key) : 0.0f;
     float total = 0.0f;
@@ -56,25 +76,49 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a) {
             if (key[i] > kMasked) total = __fadd_rn(total, expf(__fsub_rn(route_value(key[i]), top)));
         total = warp_sum(total);
     }
-    float mine = 0.0f;                         // lane j: the j-th choice
-    int id = -1;
-    for (int j = 0; j < a.topk; ++j) {
-        uint32_t local = 0;
-        int at = 0;
+    // Candidates: the logits from the topk-th largest of the lanes' largest on, or
+    // all that are not masked where fewer lanes have one.
+    const uint32_t from = max(__shfl_sync(0xFFFFFFFFu, sort_lanes(best, lane), a.topk - 1), kMasked + 1u);
+    uint64_t* place = candidates[threadIdx.x >> 5];
+    int count = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > local) local = key[i], at = i;
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, local);
-        if (most <= kMasked) break;
-        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, local == most ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu);
+    for (int i = 0; i < V; ++i) {
+        const bool is = key[i] >= from;
+        const unsigned all = __ballot_sync(0xFFFFFFFFu, is);
+        const int at = count + __popc(all & ((1u << lane) - 1u));
+        if (is && at < 32) place[at] = static_cast<uint64_t>(key[i]) << 32 | ~static_cast<uint32_t>(i * 32 + lane);
+        count += __popc(all);
+    }
+    __syncwarp();
+    float mine = 0.0f;                         // of the choice that this lane holds
+    int id = -1, rank = lane;
+    if (count <= 32) {
+        const uint64_t own = lane < count ? place[lane] : 0u;
+        rank = 0;
+        for (int c = 0; c < count; ++c) rank += place[c] > own ? 1 : 0;
+        if (lane >= count) rank = lane;        // places that no candidate takes
+        if (rank < a.topk && lane < count)
+            id = static_cast<int>(~static_cast<uint32_t>(own)), mine = expf(__fsub_rn(route_value(static_cast<uint32_t>(own >> 32)), top));
+    } else {                                   // many equal ones: one after another
+        for (int j = 0; j < a.topk; ++j) {
+            uint32_t local = 0;
+            int at = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e == static_cast<uint32_t>(i * 32 + lane)) key[i] = 0;
-        if (lane == j) id = static_cast<int>(e), mine = expf(__fsub_rn(route_value(most), top));
+            for (int i = 0; i < V; ++i)
+                if (key[i] > local) local = key[i], at = i;
+            const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, local);
+            if (most <= kMasked) break;
+            const uint32_t e =
+                __reduce_min_sync(0xFFFFFFFFu, local == most ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e == static_cast<uint32_t>(i * 32 + lane)) key[i] = 0;
+            if (lane == j) id = static_cast<int>(e), mine = expf(__fsub_rn(route_value(most), top));
+        }
     }
     if (a.softmax == SAR_SOFTMAX_CHOSEN) total = warp_sum(mine);
-    if (lane < a.topk) {
-        const size_t s = t * static_cast<size_t>(a.topk) + static_cast<size_t>(lane);
+    if (rank < a.topk) {
+        const size_t s = t * static_cast<size_t>(a.topk) + static_cast<size_t>(rank);
         static_cast<Id*>(a.ids)[s] = id;
         store_elem<WDT>(a.weights, s, id >= 0 ? __fdiv_rn(mine, total) : 0.0f);
     }
@@ -97,44 +141,49 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteArgs a
             dw = load_elem<WDT>(a.weights, s);
         }
     }
-    bool first = id >= 0;
-    float given = 0.0f;
-    for (int j = 0; j < a.topk; ++j) {
-        const int other = __shfl_sync(0xFFFFFFFFu, id, j);
-        const float g = __shfl_sync(0xFFFFFFFFu, dw, j);
-        if (other == id) {
-            given = __fadd_rn(given, g);
-            if (j < lane) first = false;
+    bool again = false;                        // a lane below has this id
+    for (int j = 0; j < a.topk; ++j) again |= __shfl_sync(0xFFFFFFFFu, id, j) == id && j < lane;
+    const bool first = id >= 0 && !again;
+    float given = dw;
+    if (__any_sync(0xFFFFFFFFu, again && id >= 0)) {
+        given = 0.0f;
+        for (int j = 0; j < a.topk; ++j) {
+            const int other = __shfl_sync(0xFFFFFFFFu, id, j);
+            const float g = __shfl_sync(0xFFFFFFFFu, dw, j);
+            if (other == id) given = __fadd_rn(given, g);
         }
     }
+    // The maximum passes over NaN; exp(NaN) makes the sum NaN, and that everything.
     float x[V];
-    float top = -INFINITY;
-    bool nan = false;
     const float chosen = first ? load_elem<DT>(a.logits, t * a.ldl + static_cast<size_t>(id)) : -INFINITY;
+    float top = chosen;
+    bool nan = chosen != chosen;
     if (a.softmax == SAR_SOFTMAX_ALL) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = i * 32 + lane;
             x[i] = e < a.experts ? load_elem<DT>(a.logits, t * a.ldl + static_cast<size_t>(e)) : -INFINITY;
             top = fmaxf(top, x[i]);
-            nan |= x[i] != x[i];
         }
-    } else {
-        top = chosen;
-        nan = chosen != chosen;
     }
-    nan = __any_sync(0xFFFFFFFFu, nan);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if (nan) top = __uint_as_float(0x7FFFFFFFu);
-    const bool empty = top == -INFINITY;
+    bool empty = top == -INFINITY;
+    if (empty) {                               // unless NaN are all that there is
+        if (a.softmax == SAR_SOFTMAX_ALL) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) nan |= x[i] != x[i];
+        }
+        empty = !__any_sync(0xFFFFFFFFu, nan);
+        top = 0.0f;
+    }
     const float p0 = first && !empty ? expf(__fsub_rn(chosen, top)) : 0.0f;
     float total = p0;
     if (a.softmax == SAR_SOFTMAX_ALL) {
         total = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = empty || i * 32 + lane >= a.experts ? 0.0f : expf(__fsub_rn(x[i], top));
+            x[i] = expf(__fsub_rn(x[i], top));                       // 0 for minus infinity
             total = __fadd_rn(total, x[i]);
         }
     }
@@ -142,13 +191,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteArgs a
     const float scale = empty ? 0.0f : __fdiv_rn(1.0f, total);
     const float p = __fmul_rn(p0, scale);
     const float down = warp_sum(first ? __fmul_rn(p, given) : 0.0f);
+    const float rest = -__fmul_rn(scale, down);
     const size_t row = t * a.ldd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         if (e < a.experts)
             store_elem<DT>(a.dlogits, row + static_cast<size_t>(e),
-                           a.softmax == SAR_SOFTMAX_ALL ? __fmul_rn(__fmul_rn(x[i], scale), -down) : 0.0f);
+                           a.softmax == SAR_SOFTMAX_ALL ? __fmul_rn(x[i], rest) : 0.0f);
     }
     __syncwarp();                              // the chosen ones again, after the row
     if (first) store_elem<DT>(a.dlogits, row + static_cast<size_t>(id), __fmul_rn(p, __fsub_rn(given, down)));

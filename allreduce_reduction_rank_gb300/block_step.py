@@ -10,9 +10,11 @@ Each rank has its own tokens; all have the same parameters.  A rank's step is
     y = x + combine(rows', weights)
 
 and back again for a given gradient of y.  The gradients of the parameters (layer norm's weight and bias, the router,
-the experts) are then summed over the ranks by one allreduce.  Layer norm, sort, dispatch, combine, their gradients and
-the allreduce are this library's calls; the matrix products are torch's.  The command checks every rank's sums against
-torch.autograd on the same step in 64 bits and prints how far they are off.
+the experts) are then summed over the ranks by one allreduce, and every rank takes the same update from them: matrices
+(each expert's, the router's) in the orthogonalised direction of their gradient, vectors along it.  Layer norm, the
+router's choice, sort, dispatch, combine, their gradients, the allreduce and the orthogonalisation are this library's
+calls; the matrix products are torch's.  The command checks every rank's sums against torch.autograd on the same step in
+64 bits, and the update against the same iteration in 64 bits, and prints how far they are off.
 """
 from __future__ import annotations
 
@@ -59,6 +61,8 @@ class RankStep:
         self.counts = torch.empty(experts, dtype=torch.int32, **new)
         self.offsets = torch.empty(experts + 1, dtype=torch.int32, **new)
         self.position = torch.empty(tokens, topk, dtype=torch.int32, **new)
+        self.ids, self.weights = torch.empty(tokens, topk, dtype=torch.int64, **new), torch.empty(tokens, topk, **new)
+        self.dscores = torch.empty(tokens, experts, **new)
         # Segments of this step: rows past the last one are never read.
         self.rows, self.made = (torch.empty(self.capacity, cols, dtype=dtype, **new) for _ in range(2))
         self.dmade, self.drows = (torch.empty(self.capacity, cols, dtype=dtype, **new) for _ in range(2))
@@ -74,8 +78,8 @@ class RankStep:
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         p = self.params
         sar.sar_layer_norm(x, self.h, p.norm_weight, p.norm_bias, self.mean, self.rstd)
-        best, self.ids = torch.topk(self.h.float() @ p.router, self.topk, dim=1)
-        self.weights = torch.softmax(best, dim=1)
+        self.scores = self.h.float() @ p.router
+        sar.sar_expert_route(self.scores, self.ids, self.weights)
         sar.sar_expert_sort(self.ids, self.counts, self.offsets, self.position, align=ALIGN, capacity=self.capacity)
         sar.sar_expert_dispatch(self.h, self.position, self.rows, self.counts, self.offsets)
         self.segments = list(zip(self.offsets.tolist(), self.offsets.tolist()[1:]))
@@ -93,10 +97,9 @@ class RankStep:
             self.dexperts[e] = self.rows[a:b].float().T @ self.dmade[a:b].float()
         sar.sar_expert_combine(self.drows, self.position, self.dh)                # the dispatch's gradient
         # through the softmax of the chosen scores to the router
-        dbest = self.weights * (self.dweights - (self.weights * self.dweights).sum(1, keepdim=True))
-        dscores = torch.zeros(x.shape[0], p.router.shape[1], device="cuda").scatter_(1, self.ids, dbest)
-        self.drouter.copy_(self.h.float().T @ dscores)
-        dh = (self.dh.float() + dscores @ p.router.T).to(x.dtype)
+        sar.sar_expert_route_backward(self.dweights, self.scores, self.ids, self.dscores)
+        self.drouter.copy_(self.h.float().T @ self.dscores)
+        dh = (self.dh.float() + self.dscores @ p.router.T).to(x.dtype)
         sar.sar_layer_norm_backward(dh, x, p.norm_weight, self.mean, self.rstd, self.dx, self.dnorm_weight, self.dnorm_bias,
                                     workspace=self.workspace)
         return self.dx + dy
@@ -109,6 +112,45 @@ def step(ranks, xs, dys):
     sums = [torch.empty_like(r.gradients) for r in ranks]
     sar.sar_allreduce([r.gradients for r in ranks], sums)
     return ys, dxs, sums
+
+
+class Update:
+    """The parameters' update from a sum of gradients (a RankStep's layout), with its buffers kept."""
+
+    def __init__(self, params: Parameters, rate: float = 0.02):
+        self.rate = rate
+        cols, experts = params.router.shape
+        self.shapes = [(cols,), (cols,), (cols, experts), (experts, cols, cols)]
+        self.router, self.experts = (torch.empty(s, device="cuda") for s in self.shapes[2:])
+        n = max(sar.sar_orthogonalize_workspace_bytes(1, cols, experts), sar.sar_orthogonalize_workspace_bytes(experts, cols, cols))
+        self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def directions(self, total: torch.Tensor):
+        """What each parameter moves against: vectors' gradients as they are, matrices' orthogonalised, with the scale that
+        gives a tall matrix's rows the length of a square one's."""
+        parts = torch.split(total, [torch.Size(s).numel() for s in self.shapes])
+        dweight, dbias, drouter, dexperts = (p.view(s) for p, s in zip(parts, self.shapes))
+        rows, cols = self.shapes[2]
+        sar.sar_orthogonalize(drouter, self.router, self.workspace, scale=max(1.0, rows / cols) ** 0.5)
+        sar.sar_orthogonalize(dexperts, self.experts, self.workspace)
+        return dweight, dbias, self.router, self.experts
+
+    def apply(self, params: Parameters, total: torch.Tensor) -> None:
+        """Moves the parameters, in place."""
+        moved = (params.norm_weight, params.norm_bias, params.router, params.experts)
+        for p, d in zip(moved, self.directions(total)):
+            p.sub_((self.rate * d).to(p.dtype))
+
+
+def orthogonal_reference(g, scale=1.0):
+    """sar_orthogonalize's iteration in 64 bits."""
+    x = g.double()
+    x = x / (x.flatten(-2).norm(dim=-1)[..., None, None] + 1e-7)
+    x = x.mT if g.shape[-2] > g.shape[-1] else x
+    for _ in range(5):
+        gram = x @ x.mT
+        x = 3.4445 * x + (-4.7750 * gram + 2.0315 * gram @ gram) @ x
+    return scale * (x.mT if g.shape[-2] > g.shape[-1] else x)
 
 
 def reference(params: Parameters, x, dy, ids):
@@ -158,6 +200,14 @@ def main() -> None:
         max(deviation(s, total) for s in sums)))
     if not all(torch.equal(s, sums[0]) for s in sums):
         raise SystemExit("block_step: the ranks' sums differ")
+    update = Update(params)
+    _, _, router, expert_matrices = update.directions(sums[0])
+    drouter, dexperts = (p.view(s) for p, s in zip(torch.split(sums[0][2 * a.cols:], [router.numel(), expert_matrices.numel()]),
+                                                   update.shapes[2:]))
+    scale = max(1.0, a.cols / a.experts) ** 0.5
+    print("  update: router %.2g, experts %.2g" % (deviation(router, orthogonal_reference(drouter, scale)),
+                                                 deviation(expert_matrices, orthogonal_reference(dexperts))))
+    update.apply(params, sums[0])
 
 
 if __name__ == "__main__":

@@ -309,14 +309,21 @@ struct LeftFp32 {
         split_tf32(__uint_as_float(q.x), bh[0], bl[0]), split_tf32(__uint_as_float(q.y), bh[1], bl[1]);
         split_tf32(__uint_as_float(q.z), bh[2], bl[2]), split_tf32(__uint_as_float(q.w), bh[3], bl[3]);
     }
+    // The tensor cores' sums lose their last bits towards zero, so that a chain of
+    // them over all of k was off by up to 9e-6: every 16 of k end in a sum of their
+    // own, the small products first, which is added rounded to nearest.
     __device__ __forceinline__ void multiply(float (&d)[4], const RightTf32<4>& x) const {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], x.lo[i], x.lo[i + 1]);
-            mma_tf32(d, al[i], bl[i], al[i + 1], bl[i + 1], x.hi[i], x.hi[i + 1]);
-            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], x.lo[i], x.lo[i + 1]);
-            mma_tf32(d, ah[i], bh[i], ah[i + 1], bh[i + 1], x.hi[i], x.hi[i + 1]);
+            mma_tf32(s, al[i], bl[i], al[i + 1], bl[i + 1], x.lo[i], x.lo[i + 1]);
+            mma_tf32(s, al[i], bl[i], al[i + 1], bl[i + 1], x.hi[i], x.hi[i + 1]);
+            mma_tf32(s, ah[i], bh[i], ah[i + 1], bh[i + 1], x.lo[i], x.lo[i + 1]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) mma_tf32(s, ah[i], bh[i], ah[i + 1], bh[i + 1], x.hi[i], x.hi[i + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = __fadd_rn(d[i], s[i]);
     }
     __device__ __forceinline__ void multiply(float (&d)[4], const uint4& x) const {
         const float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};

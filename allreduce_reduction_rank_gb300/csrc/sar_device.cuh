@@ -37,8 +37,9 @@ template <int NR> __device__ __forceinline__ int ranks(int n_rt) { return NR > 0
 // the stream drains.  Each of them calls pdl_wait() before its first
 // global-memory access: it returns once the preceding kernel has completed and
 // its writes are visible, so stream order is kept exactly.  No kernel signals
-// its dependents early (griddepcontrol.launch_dependents): measured, the early
-// signal was no faster, and slower for the LL pair.
+// its dependents early (griddepcontrol.launch_dependents) but the first of the
+// expert layer's two (expert_layer.cu): measured, the early signal was no
+// faster, and slower for the LL pair.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------

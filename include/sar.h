@@ -50,7 +50,8 @@
  *    dependent launch): one may be scheduled while the work before it in the
  *    stream drains, but it waits for that work to complete (griddepcontrol.
  *    wait) before touching memory, so stream order and results are exactly
- *    those of plain launches.  No library kernel signals its dependents early.
+ *    those of plain launches.  No library kernel signals its dependents early but
+ *    the first of sar_expert_layer's two, whose dependent is the second.
  *  - `stream` is a CUDA stream (cudaStream_t); NULL is the legacy default
  *    stream.  The current device must be the one that owns the buffers.
  */
@@ -686,9 +687,9 @@ SAR_API size_t sar_expert_layer_workspace_bytes(size_t tokens, int topk, int exp
  *   out[t] = R(sum_j weights[t * topk + j] * (w_out[e] . h))
  * over the kept choices j in ascending order.  An id outside 0 .. experts - 1
  * drops its slot: its weight is not read.  A token without a kept slot gets
- * zeros.  An expert's matrices are read once whatever the number of its
- * tokens (up to 32; once more for every further 32), and those of experts
- * without a token not at all.
+ * zeros.  An expert's matrices are read once for every 8 to 32 of its tokens
+ * (more at a time where the experts have more of them on average), and those of
+ * experts without a token not at all.
  *
  * x       : tokens x cols, leading dimension ldx.
  * weights : optional (NULL: 1), tokens * topk values of type wdtype.

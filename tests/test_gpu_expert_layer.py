@@ -108,6 +108,16 @@ def test_values_past_the_range_of_16_bits(sar):
     check_layer(sar, x, ids, w_in, w_out * 64, weights)                          # h of 2^-20
 
 
+def test_long_sums_in_binary32_stay_exact(sar):
+    """Additions rounded to nearest err independently: over 4096 of k, 64 of them a warp, by sqrt(64) * 2^-24 / sqrt(3) of
+    the sum in the mean; the tensor cores' sums of 16 of k, cut off, by up to 4 * 2^-24 of themselves.  Both products:
+    1.1e-6.  A chain of cut-off sums over all of k errs by 1e-5."""
+    x, ids, w_in, w_out, weights = case(6, 2, 4, 4096, 4096, "fp32", seed=20)
+    got = layer(sar, x, ids, w_in, w_out, weights).double()
+    want, _ = bref.expert_layer(x, ids, w_in, w_out, weights, True, "silu")
+    assert (got - want).norm() / want.norm() < 1.1e-6
+
+
 @pytest.mark.parametrize("dtype", list(ref.DTYPES))
 def test_infinities_and_nan_stay_with_their_token(sar, dtype):
     x, ids, w_in, w_out, weights = case(12, 2, 5, 64, 48, dtype, seed=12)

@@ -184,6 +184,7 @@ struct ProductArgs {
     int m, n;                    // rows and columns of the product
     int rb, cb;                  // blocks of 128 rows of P, blocks of 64 columns of X
     int kb;                      // blocks of 64 along k
+    int split;                   // blocks of a cluster that share k
     size_t p_stride, q_stride, to_stride;      // bytes from one matrix to the next
     const StepFactors* factors;  // of this step, kMaxSteps from one matrix to the next
     // kLast
@@ -191,6 +192,10 @@ struct ProductArgs {
     size_t ldo, ostride;
     bool transposed;
 };
+
+// How blocks share a tile: one has it for itself; two have 128 rows each; those of a
+// cluster have a part of k each, and add.
+enum Form { kSingle, kPair, kSplit };
 
 // A tile is 128 x 128, or 256 x 256 by a pair of blocks, of 128 rows each.  Per
 // block of k a SM fetches 64 KiB either way, for twice as many products in a
@@ -210,6 +215,8 @@ static_assert(128 * kFewRegisters + 32 * kTakers * kManyRegisters <= kThreads * 
 constexpr int kStaging = 4096;         // of each taker: 32 rows x 32 columns, hi and lo, or binary32
 constexpr int kStages = 3, kStageBytes = 2 * static_cast<int>(kBlock);        // 128 rows of each operand, 64 along k
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kTakers * kStaging;
+
+constexpr int kMostSplit = 4;
 
 struct Place {
     size_t z;
@@ -249,6 +256,10 @@ template <int MODE, bool PAIR> __device__ __forceinline__ Turned turned_of(const
     return {left, true};
 }
 
+// Where four columns of a row are among 128 x 128 sums, in floats: exchanged so that
+// a column of rows does not collide.
+__device__ __forceinline__ int quad_of(int row, int quad) { return row * 128 + ((quad ^ (row & 7)) << 2); }
+
 // A taker's 32 x 32 values in its staging, each half 32 rows of 64 bytes whose
 // 16-byte pieces are exchanged so that neither its rows nor its lines collide.
 __device__ __forceinline__ int staged(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
@@ -266,29 +277,41 @@ __device__ __forceinline__ void store_staged(const unsigned char* staging, unsig
     __syncwarp();
 }
 
-__device__ __forceinline__ void load_staged(unsigned char* staging, const unsigned char* block, int row0, int half, int lane) {
+// The same rows of A, on their way while the sums are made; then in the staging.
+struct Rows {
     uint4 v[8];
+    __device__ __forceinline__ void load(const unsigned char* block, int row0, int half, int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = row0 + i * 8 + lane / 4, p = lane % 4;
-        const unsigned char* from = block + row * 128 + (((half * 4 + p) ^ (row & 7)) << 4);
-        v[2 * i] = *reinterpret_cast<const uint4*>(from);
-        v[2 * i + 1] = *reinterpret_cast<const uint4*>(from + kHalfBlock);
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + i * 8 + lane / 4, p = lane % 4;
+            const unsigned char* from = block + row * 128 + (((half * 4 + p) ^ (row & 7)) << 4);
+            v[2 * i] = *reinterpret_cast<const uint4*>(from);
+            v[2 * i + 1] = *reinterpret_cast<const uint4*>(from + kHalfBlock);
+        }
     }
+    __device__ __forceinline__ void stage(unsigned char* staging, int lane) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4, p = lane % 4;
-        *reinterpret_cast<uint4*>(staging + staged(r, p)) = v[2 * i];
-        *reinterpret_cast<uint4*>(staging + 2048 + staged(r, p)) = v[2 * i + 1];
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4, p = lane % 4;
+            *reinterpret_cast<uint4*>(staging + staged(r, p)) = v[2 * i];
+            *reinterpret_cast<uint4*>(staging + 2048 + staged(r, p)) = v[2 * i + 1];
+        }
+        __syncwarp();
     }
-    __syncwarp();
+};
+
+// Rows row0 .., columns col0 .. of A (32 each), where they are kept.
+__device__ __forceinline__ void load_rows(Rows& rows, const ProductArgs& a, const Place& at, int row0, int col0, int lane) {
+    const int row_block = row0 / 128, col_block = col0 / 64;
+    if (row_block >= a.rb || col_block >= 2 * a.rb || col0 / 128 < row_block) return;
+    rows.load(a.p + at.z * a.p_stride + (static_cast<size_t>(row_block) * 2 * a.rb + col_block) * kBlock, row0 % 128, col0 / 32 % 2, lane);
 }
 
 // What a taker does with 32 of its row's sums, columns col0 .. of row `row`
 // (both multiples of 32 but for the lane in the row).
 template <int MODE, int DT>
 __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, const StepFactors& f, float (&v)[32], int row0, int col0,
-                                       unsigned char* staging, int lane, bool failed) {
+                                       unsigned char* staging, int lane, bool failed, const Rows& rows) {
     if (MODE == kLast) {
         if (col0 >= a.n) return;
         const int rows = a.m - row0, cols = a.n - col0;
@@ -323,7 +346,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
     const size_t block = static_cast<size_t>(row_block) * across + col_block;
     unsigned char* to = a.to + at.z * a.to_stride;
     if (MODE == kPoly) {
-        load_staged(staging, a.p + at.z * a.p_stride + block * kBlock, row0 % 128, half, lane);
+        rows.stage(staging, lane);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const uint4 hi = *reinterpret_cast<const uint4*>(staging + staged(lane, p));
@@ -359,7 +382,8 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
     store_staged(staging, to + block * kBlock, row0 % 128, half, lane);
 }
 
-template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bounds__(kThreads, 1) product_kernel(ProductArgs a) {
+template <int MODE, Form FORM, int CHUNK, int DT> __global__ void __launch_bounds__(kThreads, 1) product_kernel(ProductArgs a) {
+    constexpr bool PAIR = FORM == kPair, SPLIT = FORM == kSplit;
     constexpr bool square = MODE == kGram || MODE == kPoly;       // the right operand is a symmetric matrix's, or X's rows
     constexpr int stages = kStages, blocks = PAIR ? 2 : 1, wide = kTile<PAIR>, depth = 512 / wide;
     extern __shared__ unsigned char dynamic[];
@@ -370,7 +394,10 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
     unsigned char* staging = smem + stages * kStageBytes;
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
     const int rank = PAIR ? static_cast<int>(tc::cluster_rank()) : 0;
-    const unsigned first_tile = blockIdx.x / blocks, tile_step = gridDim.x / blocks;
+    const unsigned sharing = SPLIT ? static_cast<unsigned>(a.split) : blocks;
+    const unsigned first_tile = blockIdx.x / sharing, tile_step = gridDim.x / sharing;
+    const int part = SPLIT ? static_cast<int>(tc::cluster_rank()) : 0;
+    const int k_first = SPLIT ? part * a.kb / a.split : 0, k_end = SPLIT ? (part + 1) * a.kb / a.split : a.kb;
     const uint32_t bar0 = tc::shared_address(bars);
     const auto full = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };                       // fetched
     const auto empty = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(stages + s); };             // multiplied
@@ -407,8 +434,10 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
                 const int across = MODE == kGram ? a.cb : 2 * a.rb;
                 const int row = at.row * blocks + rank, col = at.col * blocks + rank;     // this block's rows; its part of the right
                 const int pieces = max(0, min(2, (square ? 2 * a.rb : a.cb) - 2 * col));  // blocks of 64 on the right that there are
-                const uint32_t bytes = (row < a.rb ? static_cast<uint32_t>(kBlock) : 0u) + static_cast<uint32_t>(kHalfBlock) * pieces;
-                for (int k = 0; k < a.kb && ok; ++k) {
+                const bool same = square && at.row == at.col;                             // one block for both operands
+                const uint32_t bytes =
+                    (row < a.rb ? static_cast<uint32_t>(kBlock) : 0u) + (same ? 0u : static_cast<uint32_t>(kHalfBlock) * pieces);
+                for (int k = k_first; k < k_end && ok; ++k) {
                     const int s = static_cast<int>(issued % stages);
                     ok = issued < static_cast<uint32_t>(stages) ||
                          tc::barrier_wait<PAIR>(empty(s), (issued / stages - 1) & 1, abort_word);
@@ -430,7 +459,9 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
                         else
                             tc::bulk_load(to, left + (static_cast<size_t>(row) * across + k) * kBlock, kBlock, bar);
                     }
-                    if (turned.right)
+                    if (same)
+                        ;
+                    else if (turned.right)
                         along_columns(to + kBlock, right, square ? across : a.cb, 2 * col, pieces);
                     else if (pieces > 0)
                         tc::bulk_load(to + kBlock, right + (static_cast<size_t>(col) * across + k) * kBlock, kBlock, bar);
@@ -452,15 +483,16 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
             bool ok = true;
             for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
                 const Place at = place_of<PAIR, square>(a, tile);
-                for (int k = 0; k < a.kb && ok; ++k, ++used) {
-                    const bool begins = k % CHUNK == 0, ends = (k + 1) % CHUNK == 0 || k + 1 == a.kb;
+                for (int k = k_first; k < k_end && ok; ++k, ++used) {
+                    const bool begins = (k - k_first) % CHUNK == 0, ends = (k - k_first + 1) % CHUNK == 0 || k + 1 == k_end;
                     const int slot = static_cast<int>(chunk % depth), s = static_cast<int>(used % stages);
                     ok = !begins || chunk < depth || tc::barrier_wait<PAIR>(taken(slot), (chunk / depth - 1) & 1, abort_word);
                     ok = ok && tc::barrier_wait(full(s), (used / stages) & 1, abort_word) &&
                          (!PAIR || tc::barrier_wait<PAIR>(other(s), (used / stages) & 1, abort_word));
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t acc = acc0 + slot * wide, left = tc::shared_address(smem + s * kStageBytes), right = left + kBlock;
+                    const uint32_t acc = acc0 + slot * wide, left = tc::shared_address(smem + s * kStageBytes);
+                    const uint32_t right = square && at.row == at.col ? left : left + static_cast<uint32_t>(kBlock);
                     const Turned turned = turned_of<MODE, PAIR>(at, k);
                     const uint32_t instruction = tc::instruction_f16(wide, wide, turned.left, turned.right);
                     const uint32_t a_step = turned.left ? 2048 : 32, b_step = turned.right ? 2048 : 32;          // 16 along k
@@ -495,7 +527,7 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
                 for (int k = 0; k < a.kb && ok; ++k, ++seen) {
                     const int s = static_cast<int>(seen % stages);
                     ok = tc::barrier_wait(full(s), (seen / stages) & 1, abort_word);
-                    if (ok) tc::barrier_arrive_cluster(tc::barrier_of(other(s), 0));
+                    if (ok) tc::barrier_arrive_cluster(tc::place_in(other(s), 0));
                 }
         }
         __syncwarp();
@@ -504,7 +536,7 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
         const int taker = warp - 4, quarter = warp & 3, half = taker / 4;
         unsigned char* mine = staging + taker * kStaging;
         constexpr int groups = wide / 64;                                     // of 32 columns, for each taker
-        const uint32_t taken0 = PAIR ? tc::barrier_of(taken(0), 0) : taken(0);
+        const uint32_t taken0 = PAIR ? tc::place_in(taken(0), 0) : taken(0);
         uint32_t chunk = 0;
         bool ok = true;
         for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
@@ -514,7 +546,15 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
             for (int g = 0; g < groups; ++g)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sums[g][j] = 0.0f;
-            for (int i = 0; i < (a.kb + CHUNK - 1) / CHUNK && ok; ++i, ++chunk) {
+            const int row0 = (at.row * blocks + rank) * 128 + quarter * 32, col0 = at.col * wide + half * (wide / 2);
+            // A's rows, which the polynomial adds, come with the sums (a pair's takers
+            // have no registers for them: one group after another, at the end).
+            Rows rows[FORM == kSingle ? groups : 1];
+            if (MODE == kPoly && FORM == kSingle) {
+#pragma unroll
+                for (int g = 0; g < groups; ++g) load_rows(rows[g], a, at, row0, col0 + 32 * g, lane);
+            }
+            for (int i = 0; i < (k_end - k_first + CHUNK - 1) / CHUNK && ok; ++i, ++chunk) {
                 const int slot = static_cast<int>(chunk % depth);
                 ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait<PAIR>(made(slot), (chunk / depth) & 1, abort_word));
                 if (!ok) break;
@@ -545,18 +585,64 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
                         for (int j = 0; j < 32; ++j) sums[g + h][j] = __fadd_rn(sums[g + h][j], __uint_as_float(v[h][j]));
                 }
             }
+            if (SPLIT) {                                                      // the parts of k meet below
+                float* all = reinterpret_cast<float*>(smem);
+                if (!ok) sums[0][0] = __uint_as_float(0x7FFFFFFFu);           // seen by the whole matrix in the next products
+#pragma unroll
+                for (int g = 0; g < groups; ++g)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4*>(all + quad_of(quarter * 32 + lane, half * 16 + g * 8 + j)) =
+                            make_float4(sums[g][4 * j], sums[g][4 * j + 1], sums[g][4 * j + 2], sums[g][4 * j + 3]);
+                break;
+            }
             if (!ok) break;
             const StepFactors f = a.factors[at.z * kMaxSteps];
             const bool failed = MODE == kLast && *static_cast<volatile int*>(a.failed) != 0;
-            const int row0 = (at.row * blocks + rank) * 128 + quarter * 32, col0 = at.col * wide + half * (wide / 2);
 #pragma unroll
-            for (int g = 0; g < groups; ++g) finish<MODE, DT>(a, at, f, sums[g], row0, col0 + 32 * g, mine, lane, failed);
+            for (int g = 0; g < groups; ++g) {
+                Rows& of = rows[FORM == kSingle ? g : 0];
+                if (MODE == kPoly && FORM == kPair) load_rows(of, a, at, row0, col0 + 32 * g, lane);
+                finish<MODE, DT>(a, at, f, sums[g], row0, col0 + 32 * g, mine, lane, failed, of);
+            }
+        }
+        if (SPLIT) {
+            tc::cluster_sync();
+            const Place at = place_of<PAIR, square>(a, first_tile);
+            const StepFactors f = a.factors[at.z * kMaxSteps];
+            const bool failed = MODE == kLast && (*static_cast<volatile int*>(a.failed) != 0 || *abort_word != 0);
+            const uint32_t from = tc::shared_address(smem);
+            for (int b = part + taker * a.split; b < 16; b += kTakers * a.split) {       // 16 parts of 32 x 32, in turn over the blocks
+                float v[32];
+                Rows rows;
+                if (MODE == kPoly) load_rows(rows, a, at, at.row * 128 + b / 4 * 32, at.col * 128 + b % 4 * 32, lane);
+                float4 q[kMostSplit][8];                                      // all on their way together
+#pragma unroll
+                for (int i = 0; i < kMostSplit; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t quad = from + 4u * static_cast<uint32_t>(quad_of(b / 4 * 32 + lane, b % 4 * 8 + j));
+                        q[i][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (i < a.split) q[i][j] = tc::load_cluster(tc::place_in(quad, static_cast<uint32_t>(i)));
+                    }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float4 s = q[0][j];
+#pragma unroll
+                    for (int i = 1; i < kMostSplit; ++i)
+                        s.x = __fadd_rn(s.x, q[i][j].x), s.y = __fadd_rn(s.y, q[i][j].y), s.z = __fadd_rn(s.z, q[i][j].z),
+                        s.w = __fadd_rn(s.w, q[i][j].w);
+                    v[4 * j] = s.x, v[4 * j + 1] = s.y, v[4 * j + 2] = s.z, v[4 * j + 3] = s.w;
+                }
+                finish<MODE, DT>(a, at, f, v, at.row * 128 + b / 4 * 32, at.col * 128 + b % 4 * 32, mine, lane, failed, rows);
+            }
         }
     }
+    if (SPLIT && warp < 4) tc::cluster_sync();                    // as the takers
     tc::fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && aborted != 0) *static_cast<volatile int*>(a.failed) = 1;
-    if (PAIR) tc::cluster_sync();                                 // the products over both blocks' memory are done
+    if (PAIR || SPLIT) tc::cluster_sync();                        // nothing of another block's is in use any more
     if (warp == 1) {
         tc::fence_after();
         tc::tmem_free<512, PAIR>(acc0);
@@ -566,10 +652,10 @@ template <int MODE, bool PAIR, int CHUNK, int DT> __global__ void __launch_bound
 // ---------------------------------------------------------------------------
 // Host.
 // ---------------------------------------------------------------------------
-template <int MODE, bool PAIR, int CHUNK, int DT> cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
+template <int MODE, Form FORM, int CHUNK, int DT> cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
     static std::atomic<bool> allowed[kDevices];
     static std::atomic<int> registers;
-    const auto kernel = product_kernel<MODE, PAIR, CHUNK, DT>;
+    const auto kernel = product_kernel<MODE, FORM, CHUNK, DT>;
     cudaError_t e = allow_smem(kernel, kSmem, allowed);
     if (e != cudaSuccess) return e;
     if (registers.load(std::memory_order_relaxed) == 0) {
@@ -583,14 +669,15 @@ template <int MODE, bool PAIR, int CHUNK, int DT> cudaError_t launch_product(con
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.x = FORM == kPair ? 2u : static_cast<unsigned>(a.split), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(PAIR ? 2 * std::min<unsigned>(a.tiles, kSMs / 2) : std::min<unsigned>(a.tiles, kSMs));
+    cfg.gridDim = dim3(FORM == kPair ? 2 * std::min<unsigned>(a.tiles, kSMs / 2)
+                       : FORM == kSplit ? a.tiles * static_cast<unsigned>(a.split) : std::min<unsigned>(a.tiles, kSMs));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
+    cfg.numAttrs = FORM == kSingle ? 1 : 2;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -617,7 +704,14 @@ template <int MODE, int DT> cudaError_t product(ProductArgs a, size_t batch, cud
     const bool pair = a.rb > 1 && pair_time * ((pairs + kSMs / 2 - 1) / (kSMs / 2)) <= single_time * ((singles + kSMs - 1) / kSMs);
     a.per_matrix = static_cast<unsigned>(tiles_of(symmetric, pair ? 256 : 128, a));
     a.tiles = static_cast<unsigned>(pair ? pairs : singles);
-    return pair ? launch_product<MODE, true, chunk, type>(a, s) : launch_product<MODE, false, chunk, type>(a, s);
+    if (pair) return launch_product<MODE, kPair, chunk, type>(a, s);
+    // Few tiles and a long k: the SMs that are left share it, which adds 2 to 3 us to a
+    // product and takes half or three quarters off its 0.7 us a block of k.  300 x 4000
+    // fp32 371 -> 240 us, 1024 x 1024 292 -> 263; 500 x 500 (8 blocks) would lose, 185 ->
+    // 204.
+    a.split = 1;
+    while (a.kb >= 16 && a.split < kMostSplit && singles * a.split * 2 <= kSMs) a.split *= 2;
+    return a.split > 1 ? launch_product<MODE, kSplit, chunk, type>(a, s) : launch_product<MODE, kSingle, chunk, type>(a, s);
 }
 
 template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s) {

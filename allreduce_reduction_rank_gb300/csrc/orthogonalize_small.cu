@@ -31,16 +31,6 @@ int blocks_of(size_t n) {
     return blocks;
 }
 
-__device__ __forceinline__ uint32_t shared_of(uint32_t at, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float4 load_cluster(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-    return v;
-}
 __device__ __forceinline__ void store_cluster(uint32_t at, const uint4& v) {
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -139,7 +129,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
     if (warp == 0) {
         double s = 0.0;
         if (lane < static_cast<int>(blocks)) {
-            const float4 v = load_cluster(shared_of(tc::shared_address(squares), static_cast<uint32_t>(lane)));
+            const float4 v = tc::load_cluster(tc::place_in(tc::shared_address(squares), static_cast<uint32_t>(lane)));
             const float three[3] = {v.x, v.y, v.z};
             s = squares_sum(three);
         }
@@ -230,8 +220,8 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
                     for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
                     const int r = share + e / 16, p = e % 16;
                     for (uint32_t other = 0; other < blocks; ++other) {
-                        const float4 u = load_cluster(shared_of(gram_at + quad_at(r, 2 * p), other));
-                        const float4 w = load_cluster(shared_of(gram_at + quad_at(r, 2 * p + 1), other));
+                        const float4 u = tc::load_cluster(tc::place_in(gram_at + quad_at(r, 2 * p), other));
+                        const float4 w = tc::load_cluster(tc::place_in(gram_at + quad_at(r, 2 * p + 1), other));
                         v[i][0] = __fadd_rn(v[i][0], u.x), v[i][1] = __fadd_rn(v[i][1], u.y);
                         v[i][2] = __fadd_rn(v[i][2], u.z), v[i][3] = __fadd_rn(v[i][3], u.w);
                         v[i][4] = __fadd_rn(v[i][4], w.x), v[i][5] = __fadd_rn(v[i][5], w.y);
@@ -251,8 +241,8 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
                     const int r = share + e / 16, p = e % 16;
                     const uint32_t to = gram_at + static_cast<uint32_t>(p / 8 * static_cast<int>(kBlock) + piece_at(r, p % 8));
                     for (uint32_t other = 0; other < blocks; ++other) {
-                        store_cluster(shared_of(to, other), hi);
-                        store_cluster(shared_of(to + static_cast<uint32_t>(kHalfBlock), other), lo);
+                        store_cluster(tc::place_in(to, other), hi);
+                        store_cluster(tc::place_in(to + static_cast<uint32_t>(kHalfBlock), other), lo);
                     }
                 }
             }

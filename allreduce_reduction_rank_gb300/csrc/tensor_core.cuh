@@ -43,8 +43,14 @@ __device__ __forceinline__ bool barrier_test_cluster(uint32_t bar, uint32_t pari
         : "memory");
     return done != 0;
 }
-// The same barrier in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t barrier_of(uint32_t bar, uint32_t rank) {
+// 16 bytes of a block's shared memory, at an address that place_in gave.
+__device__ __forceinline__ float4 load_cluster(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+    return v;
+}
+// The same barrier, or place in shared memory, in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t place_in(uint32_t bar, uint32_t rank) {
     uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(bar), "r"(rank));
     return at;

@@ -36,7 +36,7 @@ namespace {
 using namespace orthogonal;
 
 constexpr int kSMs = 152;
-constexpr size_t kMaxParts = 256;
+constexpr size_t kMaxParts = 512;
 
 struct Sizes {
     size_t m, n;                       // the smaller side, and the larger
@@ -80,27 +80,56 @@ Space space_of(void* workspace, size_t batch, const Sizes& s) {
     return p;
 }
 
-// parts x 3 sums for each matrix.
+// Whether the rows of all matrices start on 16-byte boundaries.
+template <int DT> __device__ __forceinline__ bool rows_aligned(const OrthogonalizeArgs& a) {
+    return ((reinterpret_cast<uintptr_t>(a.g) | a.ldg * Elem<DT>::kSize | a.gstride * Elem<DT>::kSize) & 15) == 0;
+}
+
+// The squares of pieces of kVE columns: those at c0, c0 + step, .. of row r and of
+// every `down`-th row below, in an order that alignment does not change.
+template <int DT, bool kVec>
+__device__ __forceinline__ void add_squares(Squares& q, const OrthogonalizeArgs& a, size_t base, size_t r, size_t c0, size_t down,
+                                            size_t step) {
+    constexpr int together = kVec ? 8 : 4, ve = Elem<DT>::kVE;
+    for (size_t c = c0; c < a.cols; c += step) {
+        const int have = static_cast<int>(a.cols - c < static_cast<size_t>(ve) ? a.cols - c : static_cast<size_t>(ve));
+        for (size_t i = r; i < a.rows; i += together * down) {
+            Acc<DT> x[together];
+#pragma unroll
+            for (int j = 0; j < together; ++j) {
+                const size_t row = i + static_cast<size_t>(j) * down, at = base + row * a.ldg + c;
+                if (kVec && have == ve) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < a.rows) v = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.g) + at * Elem<DT>::kSize);
+                    acc_seed<DT>(x[j], v);
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < ve; ++e) x[j].v[e] = row < a.rows && e < have ? load_elem<DT>(a.g, at + e) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < together; ++j)
+#pragma unroll
+                for (int e = 0; e < ve; ++e) q.add(x[j].v[e]);
+        }
+    }
+}
+
+// parts x 3 sums for each matrix.  A row of a block's threads, a power of two of
+// them, goes along a row of the matrix.
 template <int DT>
-__global__ void __launch_bounds__(kNormThreads) squares_kernel(OrthogonalizeArgs a, float* sums, int* failed) {
+__global__ void __launch_bounds__(kNormThreads) squares_kernel(OrthogonalizeArgs a, float* sums, int* failed, int along) {
     pdl_wait();
     __shared__ float shared[kNormThreads / 32];
-    const size_t z = blockIdx.y, threads = static_cast<size_t>(gridDim.x) * kNormThreads, base = z * a.gstride;
-    const size_t down = threads / a.cols, across = threads % a.cols;       // a thread's next element
-    const size_t first = static_cast<size_t>(blockIdx.x) * kNormThreads + threadIdx.x;
-    size_t r = first / a.cols, c = first % a.cols;
+    const size_t z = blockIdx.y, base = z * a.gstride;
+    const size_t lines = static_cast<size_t>(kNormThreads / along);
+    const size_t r = blockIdx.x * lines + threadIdx.x / along, down = gridDim.x * lines, x = threadIdx.x % along;
+    constexpr int ve = Elem<DT>::kVE;
     Squares q;
-    while (r < a.rows) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = r < a.rows ? load_elem<DT>(a.g, base + r * a.ldg + c) : 0.0f;
-            r += down, c += across;
-            if (c >= a.cols) c -= a.cols, ++r;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q.add(v[i]);
-    }
+    if (rows_aligned<DT>(a))
+        add_squares<DT, true>(q, a, base, r, x * ve, down, static_cast<size_t>(along) * ve);
+    else
+        add_squares<DT, false>(q, a, base, r, x * ve, down, static_cast<size_t>(along) * ve);
     const float big = block_sum(q.big, shared), mid = block_sum(q.mid, shared), small = block_sum(q.small, shared);
     if (threadIdx.x == 0) {
         float* out = sums + (z * gridDim.x + blockIdx.x) * 3;
@@ -109,19 +138,15 @@ __global__ void __launch_bounds__(kNormThreads) squares_kernel(OrthogonalizeArgs
     }
 }
 
-// All threads of a block of kNormThreads, parts <= kNormThreads.
-__device__ Beginning beginning_of(const float* sums, int parts, float eps) {
-    __shared__ double shared[kNormThreads / 32];
+// All threads of a block of kNormThreads.
+__device__ __forceinline__ Beginning beginning_of(const float* sums, int parts, float eps) {
+    __shared__ float shared[kNormThreads / 32];
     const int t = threadIdx.x;
-    double s = t < parts ? squares_sum(sums + 3 * t) : 0.0;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    if ((t & 31) == 0) shared[t >> 5] = s;
-    __syncthreads();
-    s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kNormThreads / 32; ++w) s += shared[w];
-    return beginning(s, eps);
+    float big = 0.0f, mid = 0.0f, small = 0.0f;
+    for (int i = t; i < parts; i += kNormThreads)
+        big = __fadd_rn(big, sums[3 * i]), mid = __fadd_rn(mid, sums[3 * i + 1]), small = __fadd_rn(small, sums[3 * i + 2]);
+    const float all_big = block_sum(big, shared), all_mid = block_sum(mid, shared), all_small = block_sum(small, shared);
+    return beginning(all_big, all_mid, all_small, eps);
 }
 
 // A block of X from g: a block of the grid each.  Where g has more rows than
@@ -132,25 +157,69 @@ __global__ void __launch_bounds__(kNormThreads) begin_kernel(OrthogonalizeArgs a
     pdl_wait();
     __shared__ float tile[128][65];
     const size_t z = blockIdx.y, r0 = static_cast<size_t>(blockIdx.x / cb) * 128, c0 = static_cast<size_t>(blockIdx.x % cb) * 64;
-    const Beginning f = beginning_of(sums + z * parts * 3, parts, a.eps);
     const int t = threadIdx.x;
-    if (blockIdx.x == 0 && t == 0) step_factors(a, f, factors + z * kMaxSteps);
+    const auto norm = [&]() {                                                 // after the loads, which do not need it
+        const Beginning f = beginning_of(sums + z * parts * 3, parts, a.eps);
+        if (blockIdx.x == 0 && t == 0) step_factors(a, f, factors + z * kMaxSteps);
+        return f;
+    };
     const size_t base = z * a.gstride;
+    unsigned char* block = x + (z * gridDim.x + blockIdx.x) * kBlock;
+    if (a.rows <= a.cols && a.cols % 8 == 0 && rows_aligned<DT>(a)) {         // pieces of eight columns, as they are
+        constexpr int es = Elem<DT>::kSize, ve = Elem<DT>::kVE;
+        uint4 w[4][es / 2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < es / 2; ++j) {
+                const size_t r = r0 + t / 8 + 32 * i, c = c0 + 8 * (t % 8) + ve * j;
+                w[i][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < a.rows && c < a.cols)
+                    w[i][j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.g) + (base + r * a.ldg + c) * es);
+            }
+        const Beginning f = norm();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = t / 8 + 32 * i, p = t % 8;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < es / 2; ++j) {
+                Acc<DT> u;
+                acc_seed<DT>(u, w[i][j]);
+#pragma unroll
+                for (int e = 0; e < ve; ++e) v[ve * j + e] = f.of(u.v[e]);
+            }
+            uint4 hi, lo;
+            split8(v, hi, lo);
+            uint4* to = reinterpret_cast<uint4*>(block + r * 128 + ((p ^ (r & 7)) << 4));
+            to[0] = hi;
+            to[kHalfBlock / 16] = lo;
+        }
+        return;
+    }
+    float v[32];
     if (a.rows <= a.cols) {
-#pragma unroll 8
+#pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const int r = t / 64 + 4 * i, c = t % 64;
-            tile[r][c] = r0 + r < a.rows && c0 + c < a.cols ? f.of(load_elem<DT>(a.g, base + (r0 + r) * a.ldg + c0 + c)) : 0.0f;
+            const size_t r = r0 + t / 64 + 4 * i, c = c0 + t % 64;
+            v[i] = r < a.rows && c < a.cols ? load_elem<DT>(a.g, base + r * a.ldg + c) : 0.0f;
         }
     } else {
-#pragma unroll 8
+#pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const int r = t % 128, c = t / 128 + 2 * i;
-            tile[r][c] = r0 + r < a.cols && c0 + c < a.rows ? f.of(load_elem<DT>(a.g, base + (c0 + c) * a.ldg + r0 + r)) : 0.0f;
+            const size_t r = r0 + t % 128, c = c0 + t / 128 + 2 * i;
+            v[i] = r < a.cols && c < a.rows ? load_elem<DT>(a.g, base + c * a.ldg + r) : 0.0f;
         }
     }
+    const Beginning f = norm();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (a.rows <= a.cols)
+            tile[t / 64 + 4 * i][t % 64] = f.of(v[i]);
+        else
+            tile[t % 128][t / 128 + 2 * i] = f.of(v[i]);
+    }
     __syncthreads();
-    unsigned char* block = x + (z * gridDim.x + blockIdx.x) * kBlock;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int at = t + kNormThreads * i, r = at / 8, p = at % 8;
@@ -718,7 +787,9 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
     const Sizes sz = sizes_of(a.rows, a.cols);
     Space w = space_of(a.workspace, a.batch, sz);
     const unsigned parts = static_cast<unsigned>(norm_parts(a.rows, a.cols)), batch = static_cast<unsigned>(a.batch);
-    cudaError_t e = launch_kernel(squares_kernel<DT>, dim3(parts, batch), dim3(kNormThreads), s, a, w.sums, w.failed);
+    int along = 1;                                        // threads to a row: as its 16-byte pieces need
+    while (along < kNormThreads && static_cast<size_t>(along) * Elem<DT>::kVE < a.cols) along *= 2;
+    cudaError_t e = launch_kernel(squares_kernel<DT>, dim3(parts, batch), dim3(kNormThreads), s, a, w.sums, w.failed, along);
     if (e != cudaSuccess) return e;
     e = launch_kernel(begin_kernel<DT>, dim3(static_cast<unsigned>(sz.x_blocks), batch), dim3(kNormThreads), s, a,
                       static_cast<const float*>(w.sums), static_cast<int>(parts), w.factors, static_cast<unsigned>(sz.cb), w.x);

@@ -127,15 +127,15 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
     __syncthreads();
     if (blocks > 1) tc::cluster_sync();
     if (warp == 0) {
-        double s = 0.0;
-        if (lane < static_cast<int>(blocks)) {
-            const float4 v = tc::load_cluster(tc::place_in(tc::shared_address(squares), static_cast<uint32_t>(lane)));
-            const float three[3] = {v.x, v.y, v.z};
-            s = squares_sum(three);
-        }
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (lane < static_cast<int>(blocks)) v = tc::load_cluster(tc::place_in(tc::shared_address(squares), static_cast<uint32_t>(lane)));
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        if (lane == 0) begin = beginning(s, a.eps);
+        for (int d = 16; d > 0; d >>= 1) {
+            v.x = __fadd_rn(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, d));
+            v.y = __fadd_rn(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, d));
+            v.z = __fadd_rn(v.z, __shfl_xor_sync(0xFFFFFFFFu, v.z, d));
+        }
+        if (lane == 0) begin = beginning(v.x, v.y, v.z, a.eps);
     }
     __syncthreads();
     if (t == kThreads - 1) step_factors(a, begin, factors);

@@ -161,34 +161,65 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
     return v;
 }
 
-// 16 bytes of a row of n elements, from element k on; zeros past its end.  kVec:
-// rows are whole pieces on 16-byte boundaries.  Of other rows, binary32 is read
-// by elements (17 x 3 of 20 experts of 1021 / 515: 40 us, by blocks 49), 16-bit
-// types as the two 16-byte blocks that hold the piece (only blocks that hold
-// elements of the row) and put together (4 x 2 of 40 of 2001 / 2015 bf16: 76 us, by
-// elements 98).
-template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 piece(const char* row, int k, int n, bool there) {
-    constexpr int es = Elem<DT>::kSize;
+// How rows lie, and what is read of them:
+// kWhole     whole pieces of 16 bytes on 16-byte boundaries, as they are;
+// kElements  binary32 off the boundaries, element by element;
+// kBlocks    16-bit types off the boundaries: the 16 rows of a left operand are taken
+//            `cycle` rows apart, which start at one distance from a boundary.  Their
+//            pieces are the blocks between the boundaries, and k begins that distance
+//            before the row, for them and for the slots, so that the weights need one
+//            load a piece and, at the ends, a mask.
+// 17 x 3 of 20 experts of 1021 / 2015 bf16: 84 us, with each piece put together from two
+// blocks 95; 17 x 3 of 20 of 1021 / 515 binary32: by elements 40 us, by blocks 74 (fewer and
+// larger units of rows).
+enum Layout { kWhole, kElements, kBlocks };
+
+// Elements k .. of a row of n, those outside it zero (k may be negative); the block
+// lies on a boundary and holds elements of the row.
+template <int DT> __device__ __forceinline__ uint4 load_block(const char* row, int k, int n, bool there) {
+    constexpr int es = Elem<DT>::kSize, ve = Elem<DT>::kVE, per = 4 / es;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    const char* p = row + static_cast<size_t>(k) * es;
-    if (kVec) {
-        if (there && k < n) v = kWeights ? load_weights(p) : *reinterpret_cast<const uint4*>(p);
-        return v;
+    if (!there || k >= n || k <= -ve) return v;
+    v = load_weights(row + static_cast<ptrdiff_t>(k) * es);
+    if (k >= 0 && k + ve <= n) return v;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = k + i * per;
+        if (per == 1) {
+            w[i] = e >= 0 && e < n ? w[i] : 0u;
+        } else {
+            const uint32_t low = e >= 0 && e < n ? 0x0000FFFFu : 0u, high = e + 1 >= 0 && e + 1 < n ? 0xFFFF0000u : 0u;
+            w[i] &= low | high;
+        }
     }
-    const int left = there ? n - k : 0;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Elements k .. of a row of x of n, whatever its alignment, those outside it zero.
+template <int DT> __device__ __forceinline__ uint4 load_x(const char* row, int k, int n, bool there) {
+    constexpr int es = Elem<DT>::kSize;
+    uint32_t w[8] = {};
     if (es == 4) {
-        const uint32_t* e = reinterpret_cast<const uint32_t*>(p);
-        if (left > 0) v.x = e[0];
-        if (left > 1) v.y = e[1];
-        if (left > 2) v.z = e[2];
-        if (left > 3) v.w = e[3];
-        return v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (there && k + i >= 0 && k + i < n) w[i] = reinterpret_cast<const uint32_t*>(row)[k + i];
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    uint4 next = v;
-    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-    if (left > 0) v = *reinterpret_cast<const uint4*>(p - shift);
+    if (!there || k >= n || k <= -8) return make_uint4(0u, 0u, 0u, 0u);
+    if (k < 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i >= 0 && k + i < n) w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[k + i]) << (16 * (i & 1));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the two 16-byte blocks that hold the piece (only blocks that hold elements of the row)
+    const char* p = row + static_cast<size_t>(k) * es;
+    const int left = n - k, shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4 v = *reinterpret_cast<const uint4*>(p - shift);
+    uint4 next = make_uint4(0u, 0u, 0u, 0u);
     if (shift > 0 && left * es > 16 - shift) next = *reinterpret_cast<const uint4*>(p - shift + 16);
-    uint32_t w[8] = {v.x, v.y, v.z, v.w, next.x, next.y, next.z, next.w};
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w, w[4] = next.x, w[5] = next.y, w[6] = next.z, w[7] = next.w;
 #pragma unroll
     for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
 #pragma unroll
@@ -200,6 +231,19 @@ template <int DT, bool kVec, bool kWeights> __device__ __forceinline__ uint4 pie
         w[i] = rest <= 0 ? 0u : (rest == 1 ? both & 0xFFFFu : both);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Where the pieces are whole: zeros past the row's end.
+template <bool kWeights> __device__ __forceinline__ uint4 load_whole(const char* p, bool there) {
+    if (!there) return make_uint4(0u, 0u, 0u, 0u);
+    return kWeights ? load_weights(p) : *reinterpret_cast<const uint4*>(p);
+}
+
+// A piece of the weights; `shift` is 0 but for kBlocks.
+template <int DT, Layout L> __device__ __forceinline__ uint4 load_left(const char* row, int k, int n, bool there, int shift) {
+    if (L == kWhole) return load_whole<true>(row + static_cast<size_t>(k) * Elem<DT>::kSize, there && k < n);
+    if (L == kElements) return load_x<DT>(row, k, n, there);
+    return load_block<DT>(row, k - shift, n, there);
 }
 
 template <int DT> __device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -336,10 +380,10 @@ template <> struct Left<SAR_FP32, true> : LeftFp32 {};
 __host__ __device__ __forceinline__ int h_ld(int hidden) { return (hidden + 7) / 8 * 8; }
 
 // ---------------------------------------------------------------------------
-// h = act(w_in . x).  A block takes MT times 16 rows of an item's expert (gated:
-// 8 rows and the 8 that belong to them, which meet in one lane's sums), its warps
-// a share of k each.  Copies run ahead of the products, from one unit of rows
-// into the next.
+// h = act(w_in . x).  A block takes MT times 16 rows of an item's expert, its warps a
+// share of k each.  Gated: of whole pieces, 8 rows and the 8 that belong to them,
+// which meet in one lane's sums; of other rows (whose two kinds start at distances of
+// their own) 16 and 16, which meet in the sums of two left operands.
 // ---------------------------------------------------------------------------
 constexpr int kInWarps = 4;
 // Blocks of a SM: as many as fit for items of eight slots (48 registers a thread),
@@ -347,8 +391,10 @@ constexpr int kInWarps = 4;
 // 10, 12: 206, 186, 171, 200 us; 64 x 2 of 8 with 6, 8, 10: 434, 393, 413.
 template <int N8> constexpr int kInBlocks = N8 == 1 ? 10 : 8;
 
-template <int DT, bool kVec, int N8, int MT>
-__global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_bytes, int row_tiles) {
+template <int DT, Layout L, int N8, int MT>
+__global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_bytes, int row_tiles, int cycle) {
+    static_assert(L != kBlocks || MT == 2, "gates and what they gate");
+    constexpr bool blocks = L == kBlocks;
     constexpr int ve = Elem<DT>::kVE, es = Elem<DT>::kSize, step = 8 * ve;      // 128 bytes of a row
     extern __shared__ __align__(16) unsigned char dynamic[];
     __shared__ __align__(16) float parts[kInWarps][MT * N8][32][4];
@@ -360,7 +406,13 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // out_kernel may sort its slots meanwhile
     sort_slots(it, &item_count, a, id_bytes, 8 * N8);
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
-    const int rows = a.gated ? 2 * a.hidden : a.hidden, per_tile = a.gated ? 8 : 16, ld = h_ld(a.hidden);
+    const int rows = a.gated ? 2 * a.hidden : a.hidden, ld = h_ld(a.hidden);
+    // The place in h of row r of 16 of the m-th left operand of a tile.
+    const auto place_of = [&](int tile, int m, int r) {
+        if (!blocks) return a.gated ? (tile * MT + m) * 8 + r % 8 : (tile * MT + m) * 16 + r;
+        return tile / cycle * (a.gated ? 16 : 32) * cycle + tile % cycle + cycle * (a.gated ? r : 16 * m + r);
+    };
+    const auto is_gated_by = [&](int m, int r) { return a.gated && (blocks ? m == 1 : r >= 8); };
     const size_t row_bytes = static_cast<size_t>(a.cols) * es;
     const int units = it.count * row_tiles;
     for (int unit = static_cast<int>(blockIdx.x); unit < units; unit += static_cast<int>(gridDim.x)) {
@@ -368,13 +420,21 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
         const char* base = static_cast<const char*>(a.w_in) + static_cast<size_t>(it.expert[item]) * rows * row_bytes;
         const char* w[MT][2];
         bool there[MT][2];
+        int shift[MT] = {}, most = 0;                                // elements from a boundary to the rows' start
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int top = (tile * MT + m) * per_tile + g, bottom = a.gated ? a.hidden + top : top + 8;
-            there[m][0] = top < a.hidden;
-            there[m][1] = a.gated ? there[m][0] : bottom < a.hidden;
-            w[m][0] = base + (there[m][0] ? top : 0) * row_bytes;
-            w[m][1] = base + (there[m][1] ? bottom : 0) * row_bytes;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * i + g, at = place_of(tile, m, r);
+                there[m][i] = at < a.hidden;
+                w[m][i] = base + (static_cast<size_t>(is_gated_by(m, r) ? a.hidden : 0) + (there[m][i] ? at : 0)) * row_bytes;
+            }
+            if (blocks) {
+                const int at = place_of(tile, m, 0);
+                const char* row = base + (static_cast<size_t>(is_gated_by(m, 0) ? a.hidden : 0) + at) * row_bytes;
+                shift[m] = at < a.hidden ? static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) / es : 0;
+                most = max(most, shift[m]);
+            }
         }
         const char* x[N8];
 #pragma unroll
@@ -383,19 +443,24 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
             x[j] = static_cast<const char*>(a.x) + static_cast<size_t>(t) * a.ldx * es;
         }
         float acc[MT][N8][4] = {};
-        constexpr int U = MT == 1 && N8 < 4 && kVec ? 2 : 1;         // steps whose loads are on their way together
-        for (int k0 = warp * step; k0 < a.cols; k0 += U * kInWarps * step) {
-            uint4 p[2 * U][MT][2], v[2 * U][N8];
+        constexpr int U = MT == 1 && N8 < 4 && L == kWhole ? 2 : 1;         // steps whose loads are on their way together
+        constexpr int xm = blocks ? MT : 1;                            // x at each left operand's k
+        for (int k0 = warp * step; k0 < a.cols + most; k0 += U * kInWarps * step) {
+            uint4 p[2 * U][MT][2], v[2 * U][xm][N8];
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
                 const int k = k0 + (u >> 1) * kInWarps * step + (u & 1) * 4 * ve + c * ve;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    p[u][m][0] = piece<DT, kVec, true>(w[m][0], k, a.cols, there[m][0]);
-                    p[u][m][1] = piece<DT, kVec, true>(w[m][1], k, a.cols, there[m][1]);
-                }
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int j = 0; j < N8; ++j) v[u][j] = piece<DT, kVec, false>(x[j], k, a.cols, 8 * j + g < n);
+                    for (int i = 0; i < 2; ++i)
+                        p[u][m][i] = load_left<DT, L>(w[m][i], k, a.cols, there[m][i], shift[m]);
+#pragma unroll
+                for (int m = 0; m < xm; ++m)
+#pragma unroll
+                    for (int j = 0; j < N8; ++j)
+                        v[u][m][j] = L == kWhole ? load_whole<false>(x[j] + static_cast<size_t>(k) * es, 8 * j + g < n && k < a.cols)
+                                                 : load_x<DT>(x[j], k - shift[m], a.cols, 8 * j + g < n);
             }
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
@@ -406,7 +471,7 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
                 for (int j = 0; j < N8; ++j)
                     if (j == 0 || 8 * j < n) {
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], v[u][j]);
+                        for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], v[u][blocks ? m : 0][j]);
                     }
             }
         }
@@ -417,28 +482,36 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
                 *reinterpret_cast<float4*>(parts[warp][m * N8 + j][lane]) =
                     make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
         __syncthreads();
-        for (int i = warp; i < MT * N8; i += kInWarps) {
-            const int j = i % N8, top = (tile * MT + i / N8) * per_tile + g, bottom = top + 8;
-            if (8 * j >= n) continue;
-            float z[4];
+        const auto sums_of = [&](int m, int j, float (&z)[4]) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                z[q] = parts[0][i][lane][q];
+                z[q] = parts[0][m * N8 + j][lane][q];
 #pragma unroll
-                for (int v = 1; v < kInWarps; ++v) z[q] = __fadd_rn(z[q], parts[v][i][lane][q]);
+                for (int v = 1; v < kInWarps; ++v) z[q] = __fadd_rn(z[q], parts[v][m * N8 + j][lane][q]);
             }
+        };
+        // z[0], z[1]: row g of the operand, slots 2 c and 2 c + 1 of the eight; z[2], z[3]: row g + 8.
+        const auto write = [&](int j, int q, int at_row, float value) {
+            const int at = 8 * j + 2 * c + q;
+            if (at < n && at_row < ld)
+                static_cast<float*>(a.workspace)[static_cast<size_t>(it.sorted[first + at]) * ld + at_row] = at_row < a.hidden ? value : 0.0f;
+        };
+        for (int i = warp; i < MT * N8; i += kInWarps) {
+            const int j = i % N8, m = i / N8;
+            if (8 * j >= n || (blocks && a.gated && m == 1)) continue;
+            float z[4], with[4];
+            sums_of(m, j, z);
+            if (blocks && a.gated) sums_of(1, j, with);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {                            // slots 2 c and 2 c + 1 of the eight
-                const int at = 8 * j + 2 * c + q;
-                if (at >= n) continue;
-                float* h = static_cast<float*>(a.workspace) + static_cast<size_t>(it.sorted[first + at]) * ld;
+            for (int q = 0; q < 2; ++q) {
                 const float h0 = activate(z[q], a.activation);
-                if (a.gated) {
-                    if (top < ld) h[top] = top < a.hidden ? __fmul_rn(h0, z[2 + q]) : 0.0f;
-                } else {
-                    if (top < ld) h[top] = top < a.hidden ? h0 : 0.0f;
-                    if (bottom < ld) h[bottom] = bottom < a.hidden ? activate(z[2 + q], a.activation) : 0.0f;
+                if (!blocks && a.gated) {
+                    write(j, q, place_of(tile, m, g), __fmul_rn(h0, z[2 + q]));
+                    continue;
                 }
+                const float h1 = activate(z[2 + q], a.activation);
+                write(j, q, place_of(tile, m, g), a.gated ? __fmul_rn(h0, with[q]) : h0);
+                write(j, q, place_of(tile, m, g + 8), a.gated ? __fmul_rn(h1, with[2 + q]) : h1);
             }
         }
         __syncthreads();
@@ -483,8 +556,9 @@ __device__ __forceinline__ float load_of_block(const float* p, int rank) {      
     return v;
 }
 
-template <int DT, int WDT, bool kVec, int N8, int MT>
-__global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int id_bytes) {
+template <int DT, int WDT, Layout L, int N8, int MT>
+__global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int id_bytes, int cycle) {
+    static_assert(L != kBlocks || MT == 1, "one distance");
     constexpr int ve = Elem<DT>::kVE, es = Elem<DT>::kSize, step = 8 * ve, width = 16 * MT;
     extern __shared__ __align__(16) unsigned char dynamic[];
     __shared__ int item_count;
@@ -496,13 +570,14 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
     sort_slots(it, &item_count, a, id_bytes, 8 * N8);
     const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, c = lane & 3;
     const int blocks = static_cast<int>(gridDim.y), rank = static_cast<int>(blockIdx.y);
-    const int steps = (a.hidden + step - 1) / step, ld = h_ld(a.hidden);
+    const int steps = (a.hidden + (L != kBlocks || a.hidden == 0 ? 0 : ve - 1) + step - 1) / step, ld = h_ld(a.hidden);
     const int parts = k_parts(it.count, slots, steps, kOutWarps * blocks, MT), units = it.count * parts;
-    const int c0 = static_cast<int>(blockIdx.x) * width;
+    const int block = static_cast<int>(blockIdx.x), c0 = block * width;
+    const auto column_of = [&](int r) { return L != kBlocks ? c0 + r : block / cycle * width * cycle + block % cycle + cycle * r; };
     const size_t row_bytes = static_cast<size_t>(a.hidden) * es;
     // The weights do not depend on in_kernel: a warp's first ones go to L2 while it
     // ends (the first two lines of 16 rows; 1 x 8 of 128 experts 25.6 -> 22.8 us).
-    if (kVec && rank + blocks * warp < units) {
+    if (L == kWhole && rank + blocks * warp < units) {
         const int unit = rank + blocks * warp, r = c0 + (lane & 15), s = unit % parts + (lane >> 4) * parts;
         if (r < a.cols && s < steps)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.w_out) +
@@ -517,17 +592,20 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
         bool there[MT][2];
 #pragma unroll
         for (int m = 0; m < 2 * MT; ++m) {
-            const int r = c0 + 8 * m + g;
+            const int r = column_of(8 * m + g);
             there[m >> 1][m & 1] = r < a.cols;
             w[m >> 1][m & 1] = base + (r < a.cols ? r : 0) * row_bytes;
         }
+        int shift = 0;                                               // elements from a boundary to the rows' start
+        if (L == kBlocks && column_of(0) < a.cols)
+            shift = static_cast<int>(reinterpret_cast<uintptr_t>(base + column_of(0) * row_bytes) & 15) / es;
         const float* h[N8];
 #pragma unroll
         for (int j = 0; j < N8; ++j)
             h[j] = static_cast<const float*>(a.workspace) +
                    static_cast<size_t>(8 * j + g < n ? it.sorted[first + 8 * j + g] : 0) * ld;
         float acc[MT][N8][4] = {};
-        constexpr int U = MT == 1 && N8 == 1 && kVec ? 2 : 1;
+        constexpr int U = MT == 1 && N8 == 1 && L == kWhole ? 2 : 1;
         for (int s0 = part; s0 < steps; s0 += U * parts) {
             uint4 p[2 * U][MT][2];
             float v[2 * U][N8][ve];
@@ -535,18 +613,28 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
             for (int u = 0; u < 2 * U; ++u) {
                 const int k = (s0 + (u >> 1) * parts) * step + (u & 1) * 4 * ve + c * ve;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    p[u][m][0] = piece<DT, kVec, true>(w[m][0], k, a.hidden, there[m][0]);
-                    p[u][m][1] = piece<DT, kVec, true>(w[m][1], k, a.hidden, there[m][1]);
-                }
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int j = 0; j < N8; ++j)
+                    for (int i = 0; i < 2; ++i)
+                        p[u][m][i] = load_left<DT, L>(w[m][i], k, a.hidden, there[m][i], shift);
 #pragma unroll
-                    for (int i = 0; i < ve; i += 4) {                // rows of h end in zeros
-                        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (8 * j + g < n && k + i < a.hidden) q = *reinterpret_cast<const float4*>(h[j] + k + i);
-                        v[u][j][i] = q.x, v[u][j][i + 1] = q.y, v[u][j][i + 2] = q.z, v[u][j][i + 3] = q.w;
+                for (int j = 0; j < N8; ++j) {
+                    const bool have = 8 * j + g < n;
+                    if (L != kBlocks) {
+#pragma unroll
+                        for (int i = 0; i < ve; i += 4) {            // rows of h end in zeros
+                            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (have && k + i < a.hidden) q = *reinterpret_cast<const float4*>(h[j] + k + i);
+                            v[u][j][i] = q.x, v[u][j][i + 1] = q.y, v[u][j][i + 2] = q.z, v[u][j][i + 3] = q.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < ve; ++i) {
+                            const int at = k - shift + i;
+                            v[u][j][i] = have && at >= 0 && at < a.hidden ? h[j][at] : 0.0f;
+                        }
                     }
+                }
             }
 #pragma unroll
             for (int u = 0; u < 2 * U; ++u) {
@@ -575,8 +663,8 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
     cluster_sync();
     const int threads = blocks * kOutWarps * 32;
     for (int i = rank * kOutWarps * 32 + static_cast<int>(threadIdx.x); i < a.tokens * width; i += threads) {
-        const int t = i / width, col = i % width;
-        if (c0 + col >= a.cols) continue;
+        const int t = i / width, col = i % width, column = column_of(col);
+        if (column >= a.cols) continue;
         float total = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
             const int slot = t * a.topk + j;
@@ -587,7 +675,7 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
                 s = __fadd_rn(s, load_of_block(sums + (static_cast<size_t>(q) * slots + slot) * width + col, (unit + q) % blocks));
             total = __fmaf_rn(a.weights != nullptr ? load_elem<WDT>(a.weights, static_cast<size_t>(slot)) : 1.0f, s, total);
         }
-        store_elem<DT>(a.out, static_cast<size_t>(t) * a.ldo + static_cast<size_t>(c0 + col), total);
+        store_elem<DT>(a.out, static_cast<size_t>(t) * a.ldo + static_cast<size_t>(column), total);
     }
     cluster_sync();                                                  // no block ends while another reads its sums
 }
@@ -612,46 +700,63 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, unsigned threads
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// in: IN8 eights of slots to an item, IMT times 16 rows; out: ON8 and OMT.
-template <int DT, int WDT, bool kVec, int IN8, int IMT, int ON8, int OMT>
-cudaError_t launch_kernels(int id_bytes, const LayerArgs& a, cudaStream_t s) {
-    static std::atomic<bool> allowed[kDevices];
-    const int slots = a.tokens * a.topk;
-    const auto out = out_kernel<DT, WDT, kVec, ON8, OMT>;
-    const size_t scratch = scratch_bytes(slots, a.experts);
-    cudaError_t e = allow_smem(out, items_bytes(kMaxSlots) + static_cast<size_t>(kMaxSlots) * 64, allowed);
-    if (e != cudaSuccess) return e;
-    if (a.hidden > 0) {
-        const int per = (a.gated ? 8 : 16) * IMT, row_tiles = (a.hidden + per - 1) / per;
-        const size_t most = static_cast<size_t>(slots) * static_cast<size_t>(row_tiles);
-        const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * kInBlocks<IN8>));
-        e = launch_kernel_smem(in_kernel<DT, kVec, IN8, IMT>, dim3(grid), dim3(kInWarps * 32), items_bytes(slots) + scratch, s, a,
-                               id_bytes, row_tiles);
-        if (e != cudaSuccess) return e;
-    }
-    const int tiles = (a.cols + 16 * OMT - 1) / (16 * OMT);
-    int blocks = 1;                                                  // as many blocks as are there at once
-    while (blocks < kMostCluster && tiles * blocks * 2 <= kSMs) blocks *= 2;
-    const size_t sums = static_cast<size_t>(parts_that_fit(slots, OMT)) * slots * OMT * 64;
-    return launch_cluster(out, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(blocks)), kOutWarps * 32,
-                          items_bytes(slots) + std::max(scratch, sums), s, a, id_bytes);
+// After how many rows their distance from a 16-byte boundary comes again.
+int cycle_of(size_t row_bytes) {
+    int cycle = 1;
+    while (row_bytes * static_cast<size_t>(cycle) % 16 != 0) cycle *= 2;
+    return cycle;
 }
 
+bool whole(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; }
+
+template <int DT, Layout L, int N8, int MT> cudaError_t launch_in(int id_bytes, const LayerArgs& a, cudaStream_t s) {
+    const int slots = a.tokens * a.topk, cycle = L != kBlocks ? 1 : cycle_of(static_cast<size_t>(a.cols) * Elem<DT>::kSize);
+    const int per = L != kBlocks ? (a.gated ? 8 : 16) * MT : (a.gated ? 16 : 32) * cycle;
+    const int row_tiles = (a.hidden + per - 1) / per * cycle;
+    const size_t most = static_cast<size_t>(slots) * static_cast<size_t>(row_tiles);
+    const unsigned grid = static_cast<unsigned>(std::min<size_t>(most, kSMs * kInBlocks<N8>));
+    return launch_kernel_smem(in_kernel<DT, L, N8, MT>, dim3(grid), dim3(kInWarps * 32),
+                              items_bytes(slots) + scratch_bytes(slots, a.experts), s, a, id_bytes, row_tiles, cycle);
+}
+
+template <int DT, int WDT, Layout L, int N8, int MT> cudaError_t launch_out(int id_bytes, const LayerArgs& a, cudaStream_t s) {
+    static std::atomic<bool> allowed[kDevices];
+    const auto out = out_kernel<DT, WDT, L, N8, MT>;
+    const cudaError_t e = allow_smem(out, items_bytes(kMaxSlots) + static_cast<size_t>(kMaxSlots) * 64, allowed);
+    if (e != cudaSuccess) return e;
+    const int slots = a.tokens * a.topk, cycle = L != kBlocks ? 1 : cycle_of(static_cast<size_t>(a.hidden) * Elem<DT>::kSize);
+    const int per = 16 * MT * cycle, tiles = (a.cols + per - 1) / per * cycle;
+    int blocks = 1;                                                  // as many blocks as are there at once
+    while (blocks < kMostCluster && tiles * blocks * 2 <= kSMs) blocks *= 2;
+    const size_t sums = static_cast<size_t>(parts_that_fit(slots, MT)) * slots * MT * 64;
+    return launch_cluster(out, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(blocks)), kOutWarps * 32,
+                          items_bytes(slots) + std::max(scratch_bytes(slots, a.experts), sums), s, a, id_bytes, cycle);
+}
+
+// Items of 8 slots up to 4 slots an expert on average, of 16 up to 10, then of 32 (on
+// the way out, whose h takes twice the registers, of 16); from 5 on two left operands
+// share the slots' side, as far as the sums of all slots fit (32 columns of 512).
 template <int DT, int WDT> cudaError_t launch(int id_bytes, const LayerArgs& a, cudaStream_t s) {
-    const auto whole = [](const void* p, size_t elements) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && elements * Elem<DT>::kSize % 16 == 0;
-    };
-    const bool vec = whole(a.x, a.ldx) && whole(a.w_in, static_cast<size_t>(a.cols)) && whole(a.w_out, static_cast<size_t>(a.hidden));
+    constexpr size_t es = Elem<DT>::kSize;
+    constexpr Layout off = es == 4 ? kElements : kBlocks;
+    constexpr int off_mt = es == 4 ? 1 : 2;
+    const bool in_whole = whole(a.w_in, static_cast<size_t>(a.cols) * es) && whole(a.x, a.ldx * es);
+    const bool out_whole = whole(a.w_out, static_cast<size_t>(a.hidden) * es);
     const int mean = a.tokens * a.topk / a.experts;                  // slots of an expert
-    if (mean <= 4)
-        return vec ? launch_kernels<DT, WDT, true, 1, 1, 1, 1>(id_bytes, a, s) : launch_kernels<DT, WDT, false, 1, 1, 1, 1>(id_bytes, a, s);
-    if (mean <= 10) {
-        if (vec && a.tokens * a.topk <= kMaxSlots / 2) return launch_kernels<DT, WDT, true, 2, 2, 2, 2>(id_bytes, a, s);
-        return vec ? launch_kernels<DT, WDT, true, 2, 2, 2, 1>(id_bytes, a, s) : launch_kernels<DT, WDT, false, 2, 1, 2, 1>(id_bytes, a, s);
+    if (a.hidden > 0) {
+        cudaError_t e;
+        if (!in_whole)
+            e = mean <= 4 ? launch_in<DT, off, 1, off_mt>(id_bytes, a, s) : launch_in<DT, off, 2, off_mt>(id_bytes, a, s);
+        else if (mean <= 4)
+            e = launch_in<DT, kWhole, 1, 1>(id_bytes, a, s);
+        else
+            e = mean <= 10 ? launch_in<DT, kWhole, 2, 2>(id_bytes, a, s) : launch_in<DT, kWhole, 4, 2>(id_bytes, a, s);
+        if (e != cudaSuccess) return e;
     }
-    // The sums of all slots, 32 columns each, fit in a block's shared memory up to 512.
-    if (vec && a.tokens * a.topk <= kMaxSlots / 2) return launch_kernels<DT, WDT, true, 4, 2, 2, 2>(id_bytes, a, s);
-    return vec ? launch_kernels<DT, WDT, true, 4, 2, 2, 1>(id_bytes, a, s) : launch_kernels<DT, WDT, false, 4, 1, 2, 1>(id_bytes, a, s);
+    if (!out_whole) return mean <= 4 ? launch_out<DT, WDT, off, 1, 1>(id_bytes, a, s) : launch_out<DT, WDT, off, 2, 1>(id_bytes, a, s);
+    if (mean <= 4) return launch_out<DT, WDT, kWhole, 1, 1>(id_bytes, a, s);
+    if (a.tokens * a.topk <= kMaxSlots / 2) return launch_out<DT, WDT, kWhole, 2, 2>(id_bytes, a, s);
+    return launch_out<DT, WDT, kWhole, 2, 1>(id_bytes, a, s);
 }
 
 }  // namespace

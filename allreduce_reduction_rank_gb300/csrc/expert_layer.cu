@@ -99,7 +99,7 @@ __device__ void sort_slots(Items& it, int* count, const LayerArgs& a, int id_byt
             const int have = leads ? __popc(same) : 0, items = (have + per - 1) / per;
             const int before = scan_before(items << 16 | have, lane);
             const int of = __shfl_sync(0xFFFFFFFFu, before, __ffs(same) - 1), rank = __popc(same & below);
-            it.of[lane] = static_cast<int16_t>(e);
+            if (lane < slots) it.of[lane] = static_cast<int16_t>(e);
             if (e >= 0) {
                 it.sorted[(of & 0xFFFF) + rank] = static_cast<int16_t>(lane);
                 it.item[lane] = static_cast<int16_t>((of >> 16) + rank / per);

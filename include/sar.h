@@ -699,8 +699,9 @@ SAR_API size_t sar_expert_layer_workspace_bytes(size_t tokens, int topk, int exp
  * workspace : 16-byte aligned, of sar_expert_layer_workspace_bytes bytes; its
  *           contents do not matter before and after.  A smaller
  *           workspace_bytes returns SAR_ERR_INVALID_ARG.
- * z and h are kept in binary32 precision (h as two numbers of the weights'
- * type where those have 16 bits).
+ * z and h are kept in binary32 precision: h, and binary32 x and weights, are
+ * multiplied as two numbers of fewer bits, so that where one of a product's
+ * factors is an infinity, an output is an infinity or NaN.
  * tokens * topk at most SAR_EXPERT_LAYER_MAX_SLOTS, topk >= 1, 1 <= experts <=
  * SAR_MAX_EXPERTS, cols and hidden at most 2^20, else SAR_ERR_INVALID_ARG;
  * longer batches go through sar_expert_sort, sar_expert_dispatch, a matrix
@@ -730,7 +731,9 @@ SAR_API size_t sar_orthogonalize_workspace_bytes(size_t batch, size_t rows, size
  * (with X^T X on the right for rows > cols, which is the same in exact
  * arithmetic).  It is what the Muon optimiser applies to a matrix in place of
  * its momentum, here of a gradient that the allreduce has summed; a matrix of
- * zeros gives zeros, one with an infinity or NaN gives NaN throughout.
+ * zeros gives zeros (NaN for eps 0), one with an infinity or NaN gives NaN
+ * throughout.  The kernels' waits for their own copies and products end after
+ * 2 s; what would have come of them is NaN.
  *
  * Products are held to binary32's precision whatever the type of g: the steps
  * multiply small singular values, and the errors in their directions, by a

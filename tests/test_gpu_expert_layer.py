@@ -179,6 +179,23 @@ def test_captured_twice_over_one_workspace(sar):
         assert torch.equal(out, layer(sar, *c))
 
 
+def test_calls_at_once(sar):
+    cs = [case(1, 8, 32, 256, 96, "bf16", seed=16), case(1, 1, 1, 64, 40, "fp16", seed=17), case(40, 4, 8, 136, 72, "bf16", seed=18),
+          case(3, 2, 5, 33, 17, "fp32", seed=19)]
+    want = [layer(sar, *c) for c in cs]
+    outs = [torch.empty_like(c[0]) for c in cs]
+    spaces = [torch.empty(sar.sar_expert_layer_workspace_bytes(c[0].shape[0], c[1].shape[1], c[2].shape[0], c[0].shape[1], c[3].shape[2]),
+                          dtype=torch.uint8, device="cuda") for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (x, ids, w_in, w_out, weights), out, ws, s in zip(cs, outs, spaces, streams):
+            sar.sar_expert_layer(x, ids, w_in, w_out, out, weights, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
+
+
 def test_refusals(sar):
     x, ids, w_in, w_out, weights = case(4, 2, 3, 16, 8, "bf16")
     out = torch.empty_like(x)

@@ -79,6 +79,22 @@ def test_extreme_logits(sar, dtype, every):
     check_route(sar, torch.tensor(rows, device="cuda", dtype=d), 4, every)
 
 
+@MODES
+@pytest.mark.parametrize("dtype,bits", [("fp32", [-1, 0x7F800001, -0x7FFFFF, 0x7FFFFFFF]), ("bf16", [-1, 0x7F81, -0x7F, 0x7FFF]),
+                                        ("fp16", [-1, 0x7C01, -0x3FF, 0x7FFF])])
+def test_every_nan_is_the_greatest(sar, dtype, bits, every):
+    """Negative, quiet and signalling ones are equal to each other and above plus infinity."""
+    d = ref.DTYPES[dtype]
+    for experts in (9, 300):
+        x = torch.zeros(1, experts, dtype=d, device="cuda")
+        x[0, 1], x[0, 2] = math.inf, -math.inf
+        for place, b in zip((3, 4, 6, experts - 1), bits):
+            x.view(torch.int32 if d == torch.float32 else torch.int16)[0, place] = b
+        assert int(torch.isnan(x).sum()) == 4
+        ids, weights = route(sar, x, 6, every)
+        assert ids.tolist() == [[3, 4, 6, experts - 1, 1, 0]] and bool(torch.isnan(weights).all())
+
+
 def backward(sar, dw, x, ids, every, gap=0, inplace=False):
     xv, _ = placed(x, gap)
     out, flat = (xv, None) if inplace else placed(torch.zeros_like(x), gap)

@@ -608,7 +608,9 @@ template <int MODE, Form FORM, int CHUNK, int DT> __global__ void __launch_bound
         const uint32_t taken0 = PAIR ? tc::place_in(taken(0), 0) : taken(0);
         uint32_t chunk = 0;
         bool ok = true;
-        for (unsigned tile = first_tile; tile < a.tiles && ok; tile += tile_step) {
+        // After a wait that ran out, the results are NaN; intermediate ones need not be
+        // there, as the last launch reads that it has happened.
+        for (unsigned tile = first_tile; tile < a.tiles && (ok || MODE == kLast); tile += tile_step) {
             const Place at = place_of<PAIR, square>(a, tile);
             float sums[groups][32];
 #pragma unroll
@@ -654,9 +656,9 @@ template <int MODE, Form FORM, int CHUNK, int DT> __global__ void __launch_bound
                         for (int j = 0; j < 32; ++j) sums[g + h][j] = __fadd_rn(sums[g + h][j], __uint_as_float(v[h][j]));
                 }
             }
+            if (!ok && lane == 0) *static_cast<volatile int*>(a.failed) = 1;
             if (SPLIT) {                                                      // the parts of k meet below
                 float* all = reinterpret_cast<float*>(smem);
-                if (!ok) sums[0][0] = __uint_as_float(0x7FFFFFFFu);           // seen by the whole matrix in the next products
 #pragma unroll
                 for (int g = 0; g < groups; ++g)
 #pragma unroll
@@ -665,9 +667,9 @@ template <int MODE, Form FORM, int CHUNK, int DT> __global__ void __launch_bound
                             make_float4(sums[g][4 * j], sums[g][4 * j + 1], sums[g][4 * j + 2], sums[g][4 * j + 3]);
                 break;
             }
-            if (!ok) break;
+            if (!ok && MODE != kLast) break;
             const StepFactors f = a.factors[at.z * kMaxSteps];
-            const bool failed = MODE == kLast && *static_cast<volatile int*>(a.failed) != 0;
+            const bool failed = MODE == kLast && (!ok || *static_cast<volatile int*>(a.failed) != 0);
 #pragma unroll
             for (int g = 0; g < groups; ++g) {
                 Rows& of = rows[FORM == kSingle ? g : 0];
@@ -679,7 +681,7 @@ template <int MODE, Form FORM, int CHUNK, int DT> __global__ void __launch_bound
             tc::cluster_sync();
             const Place at = place_of<PAIR, square>(a, first_tile);
             const StepFactors f = a.factors[at.z * kMaxSteps];
-            const bool failed = MODE == kLast && (*static_cast<volatile int*>(a.failed) != 0 || *abort_word != 0);
+            const bool failed = MODE == kLast && *static_cast<volatile int*>(a.failed) != 0;
             const uint32_t from = tc::shared_address(smem);
             for (int b = part + taker * a.split; b < 16; b += kTakers * a.split) {       // 16 parts of 32 x 32, in turn over the blocks
                 float v[32];

@@ -202,6 +202,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
             add_sums(sums[0], 128 * b + 64 * half);
             add_sums(sums[1], 128 * b + 64 * half + 32);
         }
+        if (!ok) sums[0][0] = __uint_as_float(0x7FFFFFFFu);       // a wait ran out: NaN for the whole matrix
         if (blocks > 1) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {

@@ -167,6 +167,23 @@ def test_captured_twice_over_one_workspace(sar):
         assert torch.equal(out, run(sar, g))
 
 
+def test_calls_at_once(sar):
+    """On streams of their own, with workspaces of their own: one launch, clusters that share k, pairs and single blocks."""
+    gs = [gradients(8, 128, 128, torch.float32, 12), gradients(1, 300, 1100, torch.float16, 13), gradients(1, 128, 4000, torch.bfloat16, 14),
+          gradients(2, 1003, 357, torch.float16, 15), gradients(1, 1024, 1536, torch.bfloat16, 16), gradients(6, 16, 24, torch.float32, 17)]
+    want = [run(sar, g) for g in gs]
+    outs = [torch.empty_like(g) for g in gs]
+    spaces = [torch.empty(sar.sar_orthogonalize_workspace_bytes(*g.shape), dtype=torch.uint8, device="cuda") for g in gs]
+    streams = [torch.cuda.Stream() for _ in gs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, out, ws, s in zip(gs, outs, spaces, streams):
+            sar.sar_orthogonalize(g, out, ws, stream=s)
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
+
+
 def test_refusals(sar):
     g = gradients(2, 8, 12, torch.float32)
     out, ws = torch.empty_like(g), torch.empty(sar.sar_orthogonalize_workspace_bytes(2, 8, 12), dtype=torch.uint8, device="cuda")

@@ -83,6 +83,13 @@ def test_many_tiles(sar, batch, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(ref.DTYPES))
+@pytest.mark.parametrize("batch,rows,cols", [(9, 300, 640), (13, 300, 300), (14, 200, 257), (12, 300, 300), (1, 700, 660)])
+def test_tiles_of_either_width(sar, batch, rows, cols, dtype):
+    """About where the products' tiles of 64 columns outnumber the SMs: 9 x 3 x 10, 13 x 12, 14 x 2 x 5; and below."""
+    check(sar, gradients(batch, rows, cols, ref.DTYPES[dtype], rows + batch))
+
+
+@pytest.mark.parametrize("dtype", list(ref.DTYPES))
 @pytest.mark.parametrize("batch,rows,cols", [(3, 20, 37), (2, 150, 77), (2, 130, 140)])
 def test_layouts(sar, batch, rows, cols, dtype):
     g = gradients(batch, rows, cols, ref.DTYPES[dtype], seed=2)

@@ -153,6 +153,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteArgs a
             if (other == id) given = __fadd_rn(given, g);
         }
     }
+    if (!__any_sync(0xFFFFFFFFu, first)) {     // nothing to give a gradient to, whatever the logits
+        for (int e = lane; e < a.experts; e += 32) store_elem<DT>(a.dlogits, t * a.ldd + static_cast<size_t>(e), 0.0f);
+        return;
+    }
     // The maximum passes over NaN; exp(NaN) makes the sum NaN, and that everything.
     float x[V];
     const float chosen = first ? load_elem<DT>(a.logits, t * a.ldl + static_cast<size_t>(id)) : -INFINITY;

@@ -654,7 +654,8 @@ SAR_API sar_status sar_expert_route(const void* logits, size_t ldl, void* ids, i
  * not in 0 .. experts - 1 count for nothing, also in the softmax over the
  * chosen; an id that a token has twice is one expert, whose gradients add up.
  * A token without a chosen expert, or with minus infinity for all of its
- * logits, gets zeros.  dweights of dropped slots are not read.
+ * logits, gets zeros (without a chosen one also where its logits hold NaN or
+ * infinities).  dweights of dropped slots are not read.
  *
  * dlogits may be logits (same ld).  SAR_SOFTMAX_CHOSEN reads the chosen logits
  * only.

@@ -379,6 +379,17 @@ template <> struct Left<SAR_FP32, true> : LeftFp32 {};
 
 __host__ __device__ __forceinline__ int h_ld(int hidden) { return (hidden + 7) / 8 * 8; }
 
+// The tensor cores' sums lose their last bits towards zero (by up to 4 * 2^-24 of them a
+// product), so that a chain of them over a long k falls behind where its terms have one
+// sign: 16-bit types by 1.7e-3 over 2^20 of k, by 7e-4 over 65536 on the way out.  A warp's
+// chain ends after kChain products at most and joins its earlier ones, rounded to nearest,
+// in the place in shared memory where its sums go at last.  In binary32, whose chains are
+// 16 of k long (LeftFp32), so do kChain / 2 of their additions.  64 x 2 of 8 of 4096 / 8192
+// fp16 395 -> 397 us, bf16 357 -> 375; 32 x 8 of 128 bf16 172 -> 173.
+constexpr int kChain = 128;
+// The steps of a chain; kTwo: against h.
+template <int DT, bool kTwo> constexpr int kFold = kChain / (DT == SAR_FP32 || !kTwo ? 4 : DT == SAR_FP16 ? 16 : 8);
+
 // ---------------------------------------------------------------------------
 // h = act(w_in . x).  A block takes MT times 16 rows of an item's expert, its warps a
 // share of k each.  Gated: of whole pieces, 8 rows and the 8 that belong to them,
@@ -391,8 +402,14 @@ constexpr int kInWarps = 4;
 // 10, 12: 206, 186, 171, 200 us; 64 x 2 of 8 with 6, 8, 10: 434, 393, 413.
 template <int N8> constexpr int kInBlocks = N8 == 1 ? 10 : 8;
 
+// Blocks of a SM that the registers have to leave room for, where the compiler would take
+// more of them (16 bits, 32 slots: 136, and three blocks; 64 x 2 of 8 fp16 446 us, with room
+// for four 397).  0: no such bound, which costs spills elsewhere (32 x 8 of 128 bf16 191 us
+// with one block to leave room for, 216 with ten, 173 without).
+template <int DT, Layout L, int N8> constexpr int kResident = L != kWhole || N8 == 1 ? 0 : DT == SAR_FP32 ? (N8 == 2 ? 3 : 2) : N8 == 2 ? 6 : 4;
+
 template <int DT, Layout L, int N8, int MT>
-__global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_bytes, int row_tiles, int cycle) {
+__global__ void __launch_bounds__(kInWarps * 32, kResident<DT, L, N8>) in_kernel(LayerArgs a, int id_bytes, int row_tiles, int cycle) {
     static_assert(L != kBlocks || MT == 2, "gates and what they gate");
     constexpr bool blocks = L == kBlocks;
     constexpr int ve = Elem<DT>::kVE, es = Elem<DT>::kSize, step = 8 * ve;      // 128 bytes of a row
@@ -442,45 +459,56 @@ __global__ void __launch_bounds__(kInWarps * 32) in_kernel(LayerArgs a, int id_b
             const int t = 8 * j + g < n ? it.sorted[first + 8 * j + g] / a.topk : 0;
             x[j] = static_cast<const char*>(a.x) + static_cast<size_t>(t) * a.ldx * es;
         }
-        float acc[MT][N8][4] = {};
         constexpr int U = MT == 1 && N8 < 4 && L == kWhole ? 2 : 1;         // steps whose loads are on their way together
         constexpr int xm = blocks ? MT : 1;                            // x at each left operand's k
-        for (int k0 = warp * step; k0 < a.cols + most; k0 += U * kInWarps * step) {
-            uint4 p[2 * U][MT][2], v[2 * U][xm][N8];
+        constexpr int stride = U * kInWarps * step, chain = kFold<DT, false> / U * stride;
+        const int end = a.cols + most;
+        for (int k1 = warp * step; k1 == warp * step || k1 < end; k1 += chain) {
+            float acc[MT][N8][4] = {};
+            for (int k0 = k1; k0 < min(end, k1 + chain); k0 += stride) {
+                uint4 p[2 * U][MT][2], v[2 * U][xm][N8];
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) {
-                const int k = k0 + (u >> 1) * kInWarps * step + (u & 1) * 4 * ve + c * ve;
+                for (int u = 0; u < 2 * U; ++u) {
+                    const int k = k0 + (u >> 1) * kInWarps * step + (u & 1) * 4 * ve + c * ve;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        p[u][m][i] = load_left<DT, L>(w[m][i], k, a.cols, there[m][i], shift[m]);
+                        for (int i = 0; i < 2; ++i)
+                            p[u][m][i] = load_left<DT, L>(w[m][i], k, a.cols, there[m][i], shift[m]);
 #pragma unroll
-                for (int m = 0; m < xm; ++m)
+                    for (int m = 0; m < xm; ++m)
+#pragma unroll
+                        for (int j = 0; j < N8; ++j)
+                            v[u][m][j] = L == kWhole ? load_whole<false>(x[j] + static_cast<size_t>(k) * es, 8 * j + g < n && k < a.cols)
+                                                     : load_x<DT>(x[j], k - shift[m], a.cols, 8 * j + g < n);
+                }
+#pragma unroll
+                for (int u = 0; u < 2 * U; ++u) {
+                    Left<DT, false> l[MT];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) l[m].set(p[u][m][0], p[u][m][1]);
 #pragma unroll
                     for (int j = 0; j < N8; ++j)
-                        v[u][m][j] = L == kWhole ? load_whole<false>(x[j] + static_cast<size_t>(k) * es, 8 * j + g < n && k < a.cols)
-                                                 : load_x<DT>(x[j], k - shift[m], a.cols, 8 * j + g < n);
+                        if (j == 0 || 8 * j < n) {
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], v[u][blocks ? m : 0][j]);
+                        }
+                }
             }
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) {
-                Left<DT, false> l[MT];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) l[m].set(p[u][m][0], p[u][m][1]);
-#pragma unroll
-                for (int j = 0; j < N8; ++j)
-                    if (j == 0 || 8 * j < n) {
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], v[u][blocks ? m : 0][j]);
+                for (int j = 0; j < N8; ++j) {
+                    float4* at = reinterpret_cast<float4*>(parts[warp][m * N8 + j][lane]);
+                    const float(&v)[4] = acc[m][j];
+                    float4 sum = make_float4(v[0], v[1], v[2], v[3]);
+                    if (k1 > warp * step) {
+                        const float4 had = *at;
+                        sum = make_float4(__fadd_rn(had.x, v[0]), __fadd_rn(had.y, v[1]), __fadd_rn(had.z, v[2]), __fadd_rn(had.w, v[3]));
                     }
-            }
+                    *at = sum;
+                }
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < N8; ++j)
-                *reinterpret_cast<float4*>(parts[warp][m * N8 + j][lane]) =
-                    make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
         __syncthreads();
         const auto sums_of = [&](int m, int j, float (&z)[4]) {
 #pragma unroll
@@ -604,61 +632,68 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
         for (int j = 0; j < N8; ++j)
             h[j] = static_cast<const float*>(a.workspace) +
                    static_cast<size_t>(8 * j + g < n ? it.sorted[first + 8 * j + g] : 0) * ld;
-        float acc[MT][N8][4] = {};
         constexpr int U = MT == 1 && N8 == 1 && L == kWhole ? 2 : 1;
-        for (int s0 = part; s0 < steps; s0 += U * parts) {
-            uint4 p[2 * U][MT][2];
-            float v[2 * U][N8][ve];
+        const int stride = U * parts, chain = kFold<DT, true> / U * stride;
+        for (int s1 = part; s1 == part || s1 < steps; s1 += chain) {
+            float acc[MT][N8][4] = {};
+            for (int s0 = s1; s0 < min(steps, s1 + chain); s0 += stride) {
+                uint4 p[2 * U][MT][2];
+                float v[2 * U][N8][ve];
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) {
-                const int k = (s0 + (u >> 1) * parts) * step + (u & 1) * 4 * ve + c * ve;
+                for (int u = 0; u < 2 * U; ++u) {
+                    const int k = (s0 + (u >> 1) * parts) * step + (u & 1) * 4 * ve + c * ve;
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        p[u][m][i] = load_left<DT, L>(w[m][i], k, a.hidden, there[m][i], shift);
+                        for (int i = 0; i < 2; ++i)
+                            p[u][m][i] = load_left<DT, L>(w[m][i], k, a.hidden, there[m][i], shift);
 #pragma unroll
-                for (int j = 0; j < N8; ++j) {
-                    const bool have = 8 * j + g < n;
-                    if (L != kBlocks) {
+                    for (int j = 0; j < N8; ++j) {
+                        const bool have = 8 * j + g < n;
+                        if (L != kBlocks) {
 #pragma unroll
-                        for (int i = 0; i < ve; i += 4) {            // rows of h end in zeros
-                            float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (have && k + i < a.hidden) q = *reinterpret_cast<const float4*>(h[j] + k + i);
-                            v[u][j][i] = q.x, v[u][j][i + 1] = q.y, v[u][j][i + 2] = q.z, v[u][j][i + 3] = q.w;
-                        }
-                    } else {
+                            for (int i = 0; i < ve; i += 4) {            // rows of h end in zeros
+                                float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                if (have && k + i < a.hidden) q = *reinterpret_cast<const float4*>(h[j] + k + i);
+                                v[u][j][i] = q.x, v[u][j][i + 1] = q.y, v[u][j][i + 2] = q.z, v[u][j][i + 3] = q.w;
+                            }
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < ve; ++i) {
-                            const int at = k - shift + i;
-                            v[u][j][i] = have && at >= 0 && at < a.hidden ? h[j][at] : 0.0f;
+                            for (int i = 0; i < ve; ++i) {
+                                const int at = k - shift + i;
+                                v[u][j][i] = have && at >= 0 && at < a.hidden ? h[j][at] : 0.0f;
+                            }
                         }
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < 2 * U; ++u) {
+                    Left<DT, true> l[MT];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) l[m].set(p[u][m][0], p[u][m][1]);
+#pragma unroll
+                    for (int j = 0; j < N8; ++j)
+                        if (j == 0 || 8 * j < n) {
+                            const Right<DT> r(v[u][j]);
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], r);
+                        }
+                }
             }
 #pragma unroll
-            for (int u = 0; u < 2 * U; ++u) {
-                Left<DT, true> l[MT];
+            for (int j = 0; j < N8; ++j)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) l[m].set(p[u][m][0], p[u][m][1]);
+                for (int i = 0; i < 2; ++i)
+                    if (8 * j + 2 * c + i < n) {
+                        float* t = sums + (static_cast<size_t>(part) * slots + it.sorted[first + 8 * j + 2 * c + i]) * width + g;
 #pragma unroll
-                for (int j = 0; j < N8; ++j)
-                    if (j == 0 || 8 * j < n) {
-                        const Right<DT> r(v[u][j]);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) l[m].multiply(acc[m][j], r);
+                        for (int m = 0; m < MT; ++m) {
+                            const float v0 = acc[m][j][i], v1 = acc[m][j][2 + i];
+                            t[16 * m] = s1 > part ? __fadd_rn(t[16 * m], v0) : v0;
+                            t[16 * m + 8] = s1 > part ? __fadd_rn(t[16 * m + 8], v1) : v1;
+                        }
                     }
-            }
         }
-#pragma unroll
-        for (int j = 0; j < N8; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (8 * j + 2 * c + i < n) {
-                    float* t = sums + (static_cast<size_t>(part) * slots + it.sorted[first + 8 * j + 2 * c + i]) * width;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) t[16 * m + g] = acc[m][j][i], t[16 * m + 8 + g] = acc[m][j][2 + i];
-                }
     }
     cluster_sync();
     const int threads = blocks * kOutWarps * 32;

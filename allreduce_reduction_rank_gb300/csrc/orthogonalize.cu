@@ -86,9 +86,10 @@ template <int DT> __device__ __forceinline__ bool rows_aligned(const Orthogonali
 }
 
 // The squares of pieces of kVE columns: those at c0, c0 + step, .. of row r and of
-// every `down`-th row below, in an order that alignment does not change.
+// every `down`-th row below, four pieces a short sum, in an order that alignment does
+// not change.
 template <int DT, bool kVec>
-__device__ __forceinline__ void add_squares(Squares& q, const OrthogonalizeArgs& a, size_t base, size_t r, size_t c0, size_t down,
+__device__ __forceinline__ void add_squares(LongSquares& q, const OrthogonalizeArgs& a, size_t base, size_t r, size_t c0, size_t down,
                                             size_t step) {
     constexpr int together = kVec ? 8 : 4, ve = Elem<DT>::kVE;
     for (size_t c = c0; c < a.cols; c += step) {
@@ -108,9 +109,14 @@ __device__ __forceinline__ void add_squares(Squares& q, const OrthogonalizeArgs&
                 for (int e = 0; e < ve; ++e) x[j].v[e] = row < a.rows && e < have ? load_elem<DT>(a.g, at + e) : 0.0f;
             }
 #pragma unroll
-            for (int j = 0; j < together; ++j)
+            for (int j = 0; j < together; j += 4) {
+                Squares four;
 #pragma unroll
-                for (int e = 0; e < ve; ++e) q.add(x[j].v[e]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < ve; ++e) four.add(x[j + i].v[e]);
+                q.add(four);
+            }
         }
     }
 }
@@ -125,12 +131,12 @@ __global__ void __launch_bounds__(kNormThreads) squares_kernel(OrthogonalizeArgs
     const size_t lines = static_cast<size_t>(kNormThreads / along);
     const size_t r = blockIdx.x * lines + threadIdx.x / along, down = gridDim.x * lines, x = threadIdx.x % along;
     constexpr int ve = Elem<DT>::kVE;
-    Squares q;
+    LongSquares q;
     if (rows_aligned<DT>(a))
         add_squares<DT, true>(q, a, base, r, x * ve, down, static_cast<size_t>(along) * ve);
     else
         add_squares<DT, false>(q, a, base, r, x * ve, down, static_cast<size_t>(along) * ve);
-    const float big = block_sum(q.big, shared), mid = block_sum(q.mid, shared), small = block_sum(q.small, shared);
+    const float big = block_sum(q.sum.big, shared), mid = block_sum(q.sum.mid, shared), small = block_sum(q.sum.small, shared);
     if (threadIdx.x == 0) {
         float* out = sums + (z * gridDim.x + blockIdx.x) * 3;
         out[0] = big, out[1] = mid, out[2] = small;

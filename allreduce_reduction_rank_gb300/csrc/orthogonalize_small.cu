@@ -119,8 +119,10 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         if (i < 4 * cols) {
+            Squares eight;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q.add(v[i][j]);
+            for (int j = 0; j < 8; ++j) eight.add(v[i][j]);
+            q.add(eight);
         }
     const float big = block_sum(q.big, shared), mid = block_sum(q.mid, shared), small = block_sum(q.small, shared);
     if (t == 0) squares[0] = big, squares[1] = mid, squares[2] = small, squares[3] = 0.0f;

@@ -852,6 +852,7 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
 }  // namespace
 
 size_t orthogonalize_workspace_bytes(size_t batch, size_t rows, size_t cols) {
+    if (orthogonalize_small_fits(rows, cols)) return kHead;           // which lies in shared memory only
     const Sizes s = sizes_of(rows, cols);
     return kHead + sums_bytes(batch) + batch * kMaxSteps * sizeof(StepFactors) + batch * (2 * s.x_blocks + 2 * s.a_blocks) * kBlock;
 }

@@ -719,7 +719,9 @@ SAR_API sar_status sar_expert_layer(const void* x, size_t ldx, const void* ids, 
 
 /*
  * sar_orthogonalize_workspace_bytes -- bytes of the workspace that
- * sar_orthogonalize needs (0 for sizes that it refuses; never 0 otherwise).
+ * sar_orthogonalize needs (0 for sizes that it refuses; never 0 otherwise):
+ * 16 for matrices of up to 128 rows and 4096 columns, or the other way round,
+ * whatever their number.  One of more bytes serves as well.
  */
 SAR_API size_t sar_orthogonalize_workspace_bytes(size_t batch, size_t rows, size_t cols);
 

@@ -12,8 +12,8 @@ Each rank has its own tokens; all have the same parameters.  A rank's step is
 and back again for a given gradient of y.  The gradients of the parameters (layer norm's weight and bias, the router,
 the experts) are then summed over the ranks by one allreduce, and every rank takes the same update from them: matrices
 (each expert's, the router's) in the orthogonalised direction of their gradient, vectors along it.  Layer norm, the
-router's choice, sort, dispatch, combine, their gradients, the allreduce and the orthogonalisation are this library's
-calls; the matrix products are torch's.  The command checks every rank's sums against torch.autograd on the same step in
+router's choice (of up to 32 experts a token; torch's beyond), sort, dispatch, combine, their gradients, the allreduce and
+the orthogonalisation are this library's calls; the matrix products are torch's.  The command checks every rank's sums against torch.autograd on the same step in
 64 bits, and the update against the same iteration in 64 bits, and prints how far they are off.
 """
 from __future__ import annotations
@@ -61,7 +61,6 @@ class RankStep:
         self.counts = torch.empty(experts, dtype=torch.int32, **new)
         self.offsets = torch.empty(experts + 1, dtype=torch.int32, **new)
         self.position = torch.empty(tokens, topk, dtype=torch.int32, **new)
-        self.ids, self.weights = torch.empty(tokens, topk, dtype=torch.int64, **new), torch.empty(tokens, topk, **new)
         self.dscores = torch.empty(tokens, experts, **new)
         # Segments of this step: rows past the last one are never read.
         self.rows, self.made = (torch.empty(self.capacity, cols, dtype=dtype, **new) for _ in range(2))
@@ -79,7 +78,7 @@ class RankStep:
         p = self.params
         sar.sar_layer_norm(x, self.h, p.norm_weight, p.norm_bias, self.mean, self.rstd)
         self.scores = self.h.float() @ p.router
-        sar.sar_expert_route(self.scores, self.ids, self.weights)
+        self.choose()
         sar.sar_expert_sort(self.ids, self.counts, self.offsets, self.position, align=ALIGN, capacity=self.capacity)
         sar.sar_expert_dispatch(self.h, self.position, self.rows, self.counts, self.offsets)
         self.segments = list(zip(self.offsets.tolist(), self.offsets.tolist()[1:]))
@@ -87,6 +86,24 @@ class RankStep:
             torch.matmul(self.rows[a:b], p.experts[e], out=self.made[a:b])
         sar.sar_expert_combine(self.made, self.position, self.out, self.weights)
         return x + self.out
+
+    def choose(self) -> None:
+        """The tokens' ids and weights from their scores; new tensors, which the next step leaves alone."""
+        if self.topk > sar.SAR_MAX_TOPK:                     # more than the router makes
+            best, self.ids = torch.topk(self.scores, self.topk, dim=1)
+            self.weights = torch.softmax(best, dim=1)
+            return
+        shape = self.scores.shape[0], self.topk
+        self.ids, self.weights = torch.empty(shape, dtype=torch.int64, device="cuda"), torch.empty(shape, device="cuda")
+        sar.sar_expert_route(self.scores, self.ids, self.weights)
+
+    def choose_backward(self) -> None:
+        """The scores' gradient from the weights'."""
+        if self.topk > sar.SAR_MAX_TOPK:
+            dbest = self.weights * (self.dweights - (self.weights * self.dweights).sum(1, keepdim=True))
+            self.dscores.zero_().scatter_(1, self.ids, dbest)
+            return
+        sar.sar_expert_route_backward(self.dweights, self.scores, self.ids, self.dscores)
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor) -> torch.Tensor:
         p = self.params
@@ -97,7 +114,7 @@ class RankStep:
             self.dexperts[e] = self.rows[a:b].float().T @ self.dmade[a:b].float()
         sar.sar_expert_combine(self.drows, self.position, self.dh)                # the dispatch's gradient
         # through the softmax of the chosen scores to the router
-        sar.sar_expert_route_backward(self.dweights, self.scores, self.ids, self.dscores)
+        self.choose_backward()
         self.drouter.copy_(self.h.float().T @ self.dscores)
         dh = (self.dh.float() + self.dscores @ p.router.T).to(x.dtype)
         sar.sar_layer_norm_backward(dh, x, p.norm_weight, self.mean, self.rstd, self.dx, self.dnorm_weight, self.dnorm_bias,

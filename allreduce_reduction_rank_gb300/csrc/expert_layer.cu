@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kOutWarps * 32, 1) out_kernel(LayerArgs a, int
         float total = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
             const int slot = t * a.topk + j;
-            if (it.of[slot] < 0) continue;
+            if (it.of[slot] < 0 || a.hidden == 0) continue;          // no sum, whatever its weight
             const int unit = it.item[slot] * parts;
             float s = 0.0f;
             for (int q = 0; q < parts; ++q)

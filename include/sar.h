@@ -706,7 +706,8 @@ SAR_API size_t sar_expert_layer_workspace_bytes(size_t tokens, int topk, int exp
  * tokens * topk at most SAR_EXPERT_LAYER_MAX_SLOTS, topk >= 1, 1 <= experts <=
  * SAR_MAX_EXPERTS, cols and hidden at most 2^20, else SAR_ERR_INVALID_ARG;
  * longer batches go through sar_expert_sort, sar_expert_dispatch, a matrix
- * product for each segment and sar_expert_combine.  hidden == 0 gives zeros.
+ * product for each segment and sar_expert_combine.  hidden == 0 gives zeros,
+ * also for weights of infinity or NaN.
  */
 SAR_API sar_status sar_expert_layer(const void* x, size_t ldx, const void* ids, int id_bytes, const void* weights,
                                     const void* w_in, const void* w_out, void* out, size_t ldo, size_t tokens,

@@ -286,6 +286,9 @@ static_assert(128 * kFewRegisters + 32 * kTakers * kManyRegisters <= kThreads * 
 constexpr int kStaging = 4096;         // of each taker: 32 rows x 32 columns, hi and lo, or binary32
 constexpr int kStages = 3, kStageBytes = 2 * static_cast<int>(kBlock);        // 128 rows of each operand, 64 along k
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kTakers * kStaging;
+// One block a SM: blocks of a pair or a cluster that waited for another one's tensor memory
+// could wait for each other (as in orthogonalize_small.cu).
+static_assert(kSmem >= (size_t(224) << 10), "shared memory");
 
 constexpr int kMostSplit = 4;
 

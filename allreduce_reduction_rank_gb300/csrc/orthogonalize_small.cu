@@ -24,6 +24,12 @@ using namespace orthogonal;
 constexpr int kThreads = 256;
 constexpr int kColumns = 256, kMostBlocks = 16;
 constexpr int kMostSteps = 64;
+// Shared memory of a cluster's block: nearly all of a SM's 228 KiB, whatever its columns
+// need (160 KiB at least).  A block takes all of its SM's tensor memory before it waits for
+// its cluster; were two clusters' blocks, or another kernel's that multiply there, to share
+// SMs, one could wait for columns of the other and the other for its.
+constexpr size_t kAlone = size_t(224) << 10;
+static_assert(1024 + (kColumns / 64 + 2) * kBlock <= kAlone, "shared memory");
 
 int blocks_of(size_t n) {
     int blocks = 1;
@@ -365,7 +371,7 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
     const int blocks = blocks_of(n);
     const size_t width = (n + static_cast<size_t>(blocks) * 64 - 1) / (static_cast<size_t>(blocks) * 64) * 64;
     const auto kernel = small_kernel<DT>;
-    cudaError_t e = allow_smem(kernel, 1024 + (kColumns / 64 + 2) * kBlock, allowed);
+    cudaError_t e = allow_smem(kernel, kAlone, allowed);
     if (e != cudaSuccess) return e;
     if (blocks > 8) {                                             // more than is portable, once per device
         int dev = 0;
@@ -385,7 +391,7 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.batch));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 1024 + (width / 64 + 2) * kBlock;
+    cfg.dynamicSmemBytes = blocks > 1 ? kAlone : 1024 + (width / 64 + 2) * kBlock;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;

@@ -39,7 +39,10 @@ template <int NR> __device__ __forceinline__ int ranks(int n_rt) { return NR > 0
 // its writes are visible, so stream order is kept exactly.  No kernel signals
 // its dependents early (griddepcontrol.launch_dependents) but the first of the
 // expert layer's two (expert_layer.cu): measured, the early signal was no
-// faster, and slower for the LL pair.
+// faster, and slower for the LL pair.  The second of those two reads the ids and
+// prefetches weights before its pdl_wait().  What wrote them had completed by
+// then: every block of the first signals only after its own pdl_wait(), and the
+// second starts when all of them have.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------

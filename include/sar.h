@@ -51,7 +51,9 @@
  *    stream drains, but it waits for that work to complete (griddepcontrol.
  *    wait) before touching memory, so stream order and results are exactly
  *    those of plain launches.  No library kernel signals its dependents early but
- *    the first of sar_expert_layer's two, whose dependent is the second.
+ *    the first of sar_expert_layer's two, whose dependent is the second: that one
+ *    reads the ids and prefetches weights while the first still runs, after all
+ *    work before the first has completed.
  *  - `stream` is a CUDA stream (cudaStream_t); NULL is the legacy default
  *    stream.  The current device must be the one that owns the buffers.
  */

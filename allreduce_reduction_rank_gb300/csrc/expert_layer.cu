@@ -397,9 +397,13 @@ template <int DT, bool kTwo> constexpr int kFold = kChain / (DT == SAR_FP32 || !
 // their own) 16 and 16, which meet in the sums of two left operands.
 // ---------------------------------------------------------------------------
 constexpr int kInWarps = 4;
-// Blocks of a SM: as many as fit for items of eight slots (48 registers a thread),
-// twice as many as fit for the others, in turn.  32 x 8 of 128 experts with 5, 8,
-// 10, 12: 206, 186, 171, 200 us; 64 x 2 of 8 with 6, 8, 10: 434, 393, 413.
+// Blocks of the grid for a SM, in turn where fewer fit: 10 of items of eight slots fit in
+// 16 bits (48 registers), 8 in binary32 (62), four off the boundaries (113); of the others
+// two to six.  With 3, 4, 5, 8, 10, 12 of eight slots (us): 32 x 8 of 128 bf16 263, 221, 202,
+// 180, 173, 196, fp32 621, 541, 494, 470, 485, 466; 17 x 3 of 20 of 1021 / 2015 bf16 94, 80,
+// 100, 83, 84, 85.  With 2, 3, 4, 6, 8, 10 of more: 64 x 2 of 8 bf16 493, 403, 372, 416, 375,
+// 394; 24 x 2 of 8 of 2048 / 4096 fp32 245, 210, 240, 210, 210, 212; 40 x 2 of 8 of 1022 /
+// 2014 fp16 86, 74, 63, 65, 65, 65.
 template <int N8> constexpr int kInBlocks = N8 == 1 ? 10 : 8;
 
 // Blocks of a SM that the registers have to leave room for, where the compiler would take
@@ -768,9 +772,21 @@ template <int DT, int WDT, Layout L, int N8, int MT> cudaError_t launch_out(int 
                           items_bytes(slots) + std::max(scratch_bytes(slots, a.experts), sums), s, a, id_bytes, cycle);
 }
 
-// Items of 8 slots up to 4 slots an expert on average, of 16 up to 10, then of 32 (on
-// the way out, whose h takes twice the registers, of 16); from 5 on two left operands
-// share the slots' side, as far as the sums of all slots fit (32 columns of 512).
+// Slots of an item, by the slots that an expert has on average (of all experts: the host
+// does not know which ones are chosen; where all tokens choose few of many experts, items
+// stay at 8 and an expert's weights are read again for every 8 of its tokens):
+// 8 up to 4 an expert.  8 experts of 2048 / 4096 with 8, and with 16 slots an item (us):
+//   3 an expert: bf16 74.9, 74.4; 4: bf16 74.3, 75.8, fp32 198, 194; 5: 81.8, 78.9, fp32
+//   213, 200; 8: 102, 87.
+// 32 from 11 on, in binary32 from 21 on, with two left operands that share the slots' side,
+// on the way in (on the way out, whose h takes twice the registers, 16).  8 experts of 4096
+// / 8192 with 16, and with 32: 11 an expert: bf16 355, 329, fp32 1048, 1160; 16: fp16 454,
+//   395, fp32 1365, 1390; 24: fp32 1928, 1777.  Of 2048 / 768 an expert's weights pass
+//   quickly and 32 cost up to 9% (bf16 14 an expert: 55, 60; 24: 66, 69; 32: 89, 84).
+// Off the 16-byte boundaries 8 up to 6, then 16: 8 experts of 2046 / 4094 with 8, and with
+//   16: 6 an expert: bf16 137, 143, fp16 140, 159, fp32 295, 299; 7: 162, 157, 165, 172,
+//   337, 320; 8: 176, 163, 180, 178, 365, 332.
+// On the way out two left operands as far as the sums of all slots fit (32 columns of 512).
 template <int DT, int WDT> cudaError_t launch(int id_bytes, const LayerArgs& a, cudaStream_t s) {
     constexpr size_t es = Elem<DT>::kSize;
     constexpr Layout off = es == 4 ? kElements : kBlocks;
@@ -778,17 +794,18 @@ template <int DT, int WDT> cudaError_t launch(int id_bytes, const LayerArgs& a, 
     const bool in_whole = whole(a.w_in, static_cast<size_t>(a.cols) * es) && whole(a.x, a.ldx * es);
     const bool out_whole = whole(a.w_out, static_cast<size_t>(a.hidden) * es);
     const int mean = a.tokens * a.topk / a.experts;                  // slots of an expert
+    const int many = es == 4 ? 20 : 10, off_few = 6;
     if (a.hidden > 0) {
         cudaError_t e;
         if (!in_whole)
-            e = mean <= 4 ? launch_in<DT, off, 1, off_mt>(id_bytes, a, s) : launch_in<DT, off, 2, off_mt>(id_bytes, a, s);
+            e = mean <= off_few ? launch_in<DT, off, 1, off_mt>(id_bytes, a, s) : launch_in<DT, off, 2, off_mt>(id_bytes, a, s);
         else if (mean <= 4)
             e = launch_in<DT, kWhole, 1, 1>(id_bytes, a, s);
         else
-            e = mean <= 10 ? launch_in<DT, kWhole, 2, 2>(id_bytes, a, s) : launch_in<DT, kWhole, 4, 2>(id_bytes, a, s);
+            e = mean <= many ? launch_in<DT, kWhole, 2, 2>(id_bytes, a, s) : launch_in<DT, kWhole, 4, 2>(id_bytes, a, s);
         if (e != cudaSuccess) return e;
     }
-    if (!out_whole) return mean <= 4 ? launch_out<DT, WDT, off, 1, 1>(id_bytes, a, s) : launch_out<DT, WDT, off, 2, 1>(id_bytes, a, s);
+    if (!out_whole) return mean <= off_few ? launch_out<DT, WDT, off, 1, 1>(id_bytes, a, s) : launch_out<DT, WDT, off, 2, 1>(id_bytes, a, s);
     if (mean <= 4) return launch_out<DT, WDT, kWhole, 1, 1>(id_bytes, a, s);
     if (a.tokens * a.topk <= kMaxSlots / 2) return launch_out<DT, WDT, kWhole, 2, 2>(id_bytes, a, s);
     return launch_out<DT, WDT, kWhole, 2, 1>(id_bytes, a, s);

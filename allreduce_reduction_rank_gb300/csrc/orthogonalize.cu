@@ -397,7 +397,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Place& at, co
         const int rows = a.m - row0, cols = a.n - col0;
         const size_t base = at.z * a.ostride;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = failed ? __uint_as_float(0x7FFFFFFFu) : __fmul_rn(__fmul_rn(__fmul_rn(v[j], f.first), f.last), f.second);
+        for (int j = 0; j < 32; ++j) v[j] = failed ? __uint_as_float(0x7FFFFFFFu) : __fmul_rn(__fmul_rn(__fmul_rn(v[j], f.first), f.second), f.third);
         if (a.transposed) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)

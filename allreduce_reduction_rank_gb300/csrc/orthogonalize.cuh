@@ -16,9 +16,11 @@ constexpr int kNormThreads = 256;
 constexpr size_t kHalfBlock = 16384, kBlock = 2 * kHalfBlock;
 
 // What the products of one step of one matrix multiply by: powers of two (times
-// a coefficient) between the scales of X, A and the polynomial.
+// a coefficient) between the scales of X, A and the polynomial; after the last step
+// three that together make the result, each between it and the product, so that none
+// leaves binary32's range where the result does not.
 struct StepFactors {
-    float gram, square, linear, diagonal, apply, first, last, second;
+    float gram, square, linear, diagonal, apply, first, second, third;
 };
 constexpr size_t kMaxSteps = 64;
 
@@ -126,7 +128,10 @@ __device__ __forceinline__ void step_factors(const OrthogonalizeArgs& a, const B
         f.linear = ldexpf(a.b, poly - gram);
         f.diagonal = ldexpf(a.a, poly);
         f.apply = ldexpf(1.0f, after - poly - x);
-        f.last = a.scale, f.first = ldexpf(1.0f, (-poly - x) / 2), f.second = ldexpf(1.0f, -poly - x - (-poly - x) / 2);
+        int e;                                                       // first * second * third = scale 2^(-poly - x)
+        const float scale = frexpf(a.scale, &e);
+        e -= poly + x;
+        f.first = ldexpf(scale, e / 3), f.second = ldexpf(1.0f, e / 3), f.third = ldexpf(1.0f, e - e / 3 * 2);
         to[k] = f;
         top = next, x = after;
     }

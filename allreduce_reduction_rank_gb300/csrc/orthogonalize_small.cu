@@ -330,7 +330,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads, 1) small_kernel(Or
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                s[j] = failed ? __uint_as_float(0x7FFFFFFFu) : __fmul_rn(__fmul_rn(__fmul_rn(s[j], f.first), f.last), f.second);
+                s[j] = failed ? __uint_as_float(0x7FFFFFFFu) : __fmul_rn(__fmul_rn(__fmul_rn(s[j], f.first), f.second), f.third);
             const size_t to = blockIdx.y * a.ostride;
             if (tall) {
 #pragma unroll

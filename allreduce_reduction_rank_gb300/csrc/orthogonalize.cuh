@@ -79,8 +79,10 @@ __device__ __forceinline__ float block_sum(float x, float* shared) {
 }
 
 // The largest power of two that fp16 holds values up to `most` times, with 9% to
-// spare for the bound's and the values' roundings.
-__device__ __forceinline__ int scale_below(float most) { return most < 1e-38f ? 140 : ilogbf(60000.0f / most); }
+// spare for the bound's and the values' roundings.  most > 0; the quotient stays finite.
+__device__ __forceinline__ int scale_below(float most) {
+    return most < 1e-30f ? 100 + ilogbf(60000.0f / (most * 0x1p100f)) : ilogbf(60000.0f / most);
+}
 
 // 2^scale / (norm + eps) = f * first * second, the latter two powers of two: no
 // step leaves binary32's range where the product does not.  `top`: a bound of

@@ -102,7 +102,9 @@ __device__ __forceinline__ Beginning beginning(float big, float mid, float small
         square = big + mid * 0x1p-90f * 0x1p-90f, k_eps = eps * 0x1p-90f, k = 90;
     else if (mid != 0.0f)
         square = mid + small * 0x1p-80f * 0x1p-80f, k_eps = eps, k = 0;
-    const float m = sqrtf(square), whole = m + k_eps, inv = __fdiv_rn(1.0f, whole);
+    float m = sqrtf(square);
+    if (isinf(k_eps)) m = m * 0x1p-80f, k_eps = eps, k = 0;          // eps above 2^48 beside small values only
+    const float whole = m + k_eps, inv = __fdiv_rn(1.0f, whole);
     if (!(inv > 0.0f) || isinf(inv)) return {inv, 1.0f, 1.0f, 1.0f, 0};         // NaN, infinity, zeros with eps 0
     const float top = __fdiv_rn(m, whole);
     Beginning b;

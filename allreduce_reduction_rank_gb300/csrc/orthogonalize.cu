@@ -13,8 +13,9 @@
 //
 // The tensor cores' accumulators lose their last bits to truncation, always
 // towards zero.  A sum of squares (the diagonal of A) over thousands of columns
-// would be off by 2^-15, so the accumulators are taken out every 64 columns and
-// added in registers, rounded to nearest, while the next 64 are multiplied.
+// would be off by 2^-15, so the accumulators are taken out every 64 columns (every
+// 256 for g of 16 bits, see product below) and added in registers, rounded to nearest,
+// while the next are multiplied.
 //
 // Matrices between the kernels lie in blocks of 128 rows x 64 columns, 16 KiB of
 // hi and 16 KiB of lo, each as the tensor cores want it in shared memory: a tile
@@ -270,9 +271,8 @@ struct ProductArgs {
 
 // A tile is 128 x 128, 128 x 64 where there are few, or 256 x 256 by a pair of blocks,
 // of 128 rows each.  Per block of k a SM fetches 64 KiB either way, for twice as many
-// products in a pair: one block's tiles of 128 x 256 took 98 KiB for those, and the 12
-// TB/s that all SMs drew from L2 bound them (4096 x 4096 bf16: 3.37 ms in all, pairs
-// 2.93).
+// products in a pair: one block's tiles of 128 x 256 took 98 KiB for those, and what all
+// SMs drew from L2 bound them (4096 x 4096 bf16: 3.37 ms in all, pairs 2.93).
 //
 // Warp 0 fetches, warp 1 multiplies for both blocks (in the second it says when its
 // operands are there), 2 and 3 only make up the group of four whose registers are
@@ -779,14 +779,20 @@ size_t tiles_of(bool symmetric, Form form, const ProductArgs& a) {
 // Pairs of blocks or single ones, by their rounds over the SMs.  A pair's tile is two
 // of one block's for each SM, and those take longer: 128 columns of the right
 // operand are not enough for the tensor cores' full rate from shared memory, and more
-// comes from L2.  4096 x 4096, a tile's time of pairs and of singles: 37 and 47 us for
-// results of 16 bits; 45 and 50 us in binary32, where every block of k ends with the
-// accumulators being taken, and a pair's takers answer across two SMs.
+// comes from L2.  4096 x 4096, the time of a pair's tile and that of two single ones, which
+// is as much for each SM: 37 and 47 us for g of 16 bits; 45 and 50 us in binary32, where every
+// block of k ends with the accumulators being taken, and a pair's takers answer across two
+// SMs.  All steps (us) by this rule, with pairs always, with pairs never: 4096 x 4096 bf16
+// 2876, 2880, 3468, fp32 3652, 3603, 3857; 2048 x 2048 bf16 495, 627, 547, fp32 566, 778,
+// 591; 16 x 1024 x 1024 bf16 1019, 1127, 1043, fp32 1121, 1428, 1122; 4096 x 11008 bf16
+// 6551, 6454, 8132; 8192 x 2048 bf16 1412, 1660, 1521; 3 x 2048 x 2048 fp32 1537, 1696, 1620;
+// 12 x 600 x 600 fp32 370, 455, 351.
 template <int MODE, int DT> cudaError_t product(ProductArgs a, size_t batch, cudaStream_t s) {
     constexpr bool symmetric = MODE == kGram || MODE == kPoly;
-    // Blocks of 64 of k between two takings of the accumulators.  4 of them leave 7e-6
-    // of error (16 x 1024 x 1024), one 1.3e-6: results of 16 bits do not see the
-    // difference.
+    // Blocks of 64 of k between two takings of the accumulators.  One leaves 2e-6 to 4e-6
+    // of error (2-norm, five steps of 3.4445, 500 to 3000 rows; 6e-6 after twelve), 4 of
+    // them 6e-6 to 9e-6 (3e-5): a result of 16 bits is rounded by 1e-4 or 1e-3 of itself.
+    // With one, 4096 x 4096 bf16 would take 3606 us (2876), 2048 x 2048 566 (495).
     constexpr int chunk = DT == SAR_FP32 ? 1 : 4, type = MODE == kLast ? DT : SAR_FP32;
     constexpr size_t pair_time = 200, single_time = DT == SAR_FP32 ? 110 : 129;
     const size_t pairs = batch * tiles_of(symmetric, kPair, a), singles = batch * tiles_of(symmetric, kSingle, a);

@@ -702,9 +702,13 @@ SAR_API size_t sar_expert_layer_workspace_bytes(size_t tokens, int topk, int exp
  * workspace : 16-byte aligned, of sar_expert_layer_workspace_bytes bytes; its
  *           contents do not matter before and after.  A smaller
  *           workspace_bytes returns SAR_ERR_INVALID_ARG.
- * z and h are kept in binary32 precision: h, and binary32 x and weights, are
- * multiplied as two numbers of fewer bits, so that where one of a product's
- * factors is an infinity, an output is an infinity or NaN.
+ * z and h are binary32 values, sums run in binary32 (in part cut off in place of
+ * rounded, for 128 products in a row at most).  h is multiplied as two numbers of
+ * fewer bits, which hold 16 bits of it beside bf16 weights (off by 2^-16 at most)
+ * and 22 beside others; so are binary32 x and weights.  Where one of a product's
+ * factors is an infinity, an output is therefore an infinity or NaN.
+ * Of x, w_in and w_out whole 16-byte blocks that hold elements are read, also at
+ * their first and last element (bytes outside do not matter).
  * tokens * topk at most SAR_EXPERT_LAYER_MAX_SLOTS, topk >= 1, 1 <= experts <=
  * SAR_MAX_EXPERTS, cols and hidden at most 2^20, else SAR_ERR_INVALID_ARG;
  * longer batches go through sar_expert_sort, sar_expert_dispatch, a matrix
@@ -741,10 +745,14 @@ SAR_API size_t sar_orthogonalize_workspace_bytes(size_t batch, size_t rows, size
  * throughout.  The kernels' waits for their own copies and products end after
  * 2 s; what would have come of them is NaN.
  *
- * Products are held to binary32's precision whatever the type of g: the steps
- * multiply small singular values, and the errors in their directions, by a
- * each (485 times in five steps of 3.4445).  Errors are relative to the norm of
- * a step's X: elements and singular values below 2^-30 of it may be lost.
+ * The steps multiply small singular values, and the errors in their directions,
+ * by a each (485 times in five steps of 3.4445; wherever the polynomial's slope is
+ * above 1, errors grow by it), so products are not taken in 16 bits whatever the
+ * type of g.  For binary32 g they are held to binary32's precision: after five such
+ * steps the result is off by about 4e-6 in the 2-norm.  For 16-bit g sums are cut
+ * off more coarsely: about 1e-5 (3e-5 after twelve steps), before the rounding to
+ * the type.  Errors are relative to the norm of a step's X: elements and singular
+ * values below 2^-30 of it may be lost.
  *
  * g, out  : matrix i starts at i * gstride (ostride) elements; leading
  *           dimensions ldg, ldo.  out may be g (same ld and stride).  The

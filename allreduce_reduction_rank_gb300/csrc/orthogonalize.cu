@@ -288,7 +288,7 @@ constexpr int kStages = 3, kStageBytes = 2 * static_cast<int>(kBlock);        //
 constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kTakers * kStaging;
 // One block a SM: blocks of a pair or a cluster that waited for another one's tensor memory
 // could wait for each other (as in orthogonalize_small.cu).
-static_assert(kSmem >= (size_t(224) << 10), "shared memory");
+static_assert(kSmem >= (size_t(192) << 10), "shared memory");
 
 constexpr int kMostSplit = 4;
 

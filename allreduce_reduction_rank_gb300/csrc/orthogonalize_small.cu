@@ -30,12 +30,12 @@ using namespace orthogonal;
 constexpr int kThreads = 256;
 constexpr int kColumns = 256, kMostBlocks = 16;
 constexpr int kMostSteps = 64;
-// Shared memory of a cluster's block: nearly all of a SM's 228 KiB, whatever its columns
-// need (160 KiB at least).  A block takes all of its SM's tensor memory before it waits for
-// its cluster; were two clusters' blocks, or another kernel's that multiply there, to share
-// SMs, one could wait for columns of the other and the other for its.
-constexpr size_t kAlone = size_t(224) << 10;
-static_assert(1024 + (kColumns / 64 + 2) * kBlock <= kAlone, "shared memory");
+// Shared memory that a cluster's block asks for at least, whatever its columns need (160
+// KiB or more): with it in a SM's 228 KiB no other kernel that multiplies there finds room.
+// A block takes all of its SM's tensor memory before it waits for its cluster; were two
+// clusters' blocks to share SMs, one could wait for columns of the other and the other for
+// its.  224 KiB, which leave less of L1, cost up to 3% of matrices of 17 to 64 rows.
+constexpr size_t kAlone = size_t(192) << 10;
 
 // A power of two, so that a cluster's rows and exchanges split evenly: 2100 columns take 16
 // blocks, of which 11 have some.
@@ -379,7 +379,7 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
     const int blocks = blocks_of(n);
     const size_t width = (n + static_cast<size_t>(blocks) * 64 - 1) / (static_cast<size_t>(blocks) * 64) * 64;
     const auto kernel = small_kernel<DT>;
-    cudaError_t e = allow_smem(kernel, kAlone, allowed);
+    cudaError_t e = allow_smem(kernel, std::max(kAlone, 1024 + (kColumns / 64 + 2) * kBlock), allowed);
     if (e != cudaSuccess) return e;
     if (blocks > 8) {                                             // more than is portable, once per device
         int dev = 0;
@@ -399,7 +399,7 @@ template <int DT> cudaError_t launch(const OrthogonalizeArgs& a, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.batch));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = blocks > 1 ? kAlone : 1024 + (width / 64 + 2) * kBlock;
+    cfg.dynamicSmemBytes = std::max(blocks > 1 ? kAlone : 0, 1024 + (width / 64 + 2) * kBlock);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;

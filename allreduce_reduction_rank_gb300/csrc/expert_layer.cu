@@ -16,11 +16,11 @@
 // slots of one expert, each block for itself.  The sort is stable, so that every
 // block has the same items.
 //
-// Precision: x and 16-bit weights are multiplied as they are, sums in binary32 (the tensor
-// cores' are cut off, see kChain).  h is not rounded to the type: bf16 weights meet it as two bf16 numbers (16
-// bits), fp16 ones (whose range it may leave) as two tf32 numbers (21 bits) with
-// the weights widened exactly; binary32 values on both sides are two tf32
-// numbers each, all four products.
+// Precision: x and 16-bit weights are multiplied as they are, sums in binary32 (the
+// tensor cores' are cut off, see kChain).  h is not rounded to the type: bf16 weights
+// meet it as two bf16 numbers (16 bits), fp16 ones (whose range it may leave) as two tf32
+// numbers (22 bits) with the weights widened exactly; binary32 values on both sides are
+// two tf32 numbers each, all four products.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
